@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -95,6 +96,20 @@ def load():
                                        ctypes.c_uint, P]
         lib.fp8_rmsnorm_quant.restype = I
         lib.fp8_rmsnorm_quant.argtypes = [P, I, P, ctypes.c_float, I64, I64, P, P, I, P, P, P]
+        lib.fp8_kv_plan.restype = I
+        lib.fp8_kv_plan.argtypes = [P, P, I64, I64, I64, P, I64, P, I64, P, P, P, P, P, P]
+        lib.fp8_qk_norm_rope_append.restype = I
+        lib.fp8_qk_norm_rope_append.argtypes = [P, I, I64, I64, I64, I64, I64, P, P,
+                                                ctypes.c_float, P, I64, I64, I, P, P, P, P, P, P,
+                                                P, I64, I64, P]
+        lib.fp8_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+        lib.fp8_kv_attention_workspace_bytes.argtypes = []
+        lib.fp8_kv_attention_workspace_zero_bytes.restype = ctypes.c_size_t
+        lib.fp8_kv_attention_workspace_zero_bytes.argtypes = []
+        lib.fp8_kv_attention.restype = I
+        lib.fp8_kv_attention.argtypes = [P, I, I64, I64, I64, I64, I64, P, P, P, P, I64, I64, P,
+                                         I64, P, P, I64, I64, ctypes.c_float, I64, P, P, I, P, P,
+                                         P]
         _lib = lib
         return lib
 
@@ -435,3 +450,250 @@ def fp8_w8a16_mm(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                                  _stream(x.device))
     _check(st, "fp8_w8a16_mm")
     return y
+
+
+KV_PAGE_SIZES = (16, 32, 64, 128)
+KV_MIN_SCALE = 2.0 ** -64  # FP8L_KV_MIN_SCALE
+
+
+class KvCache(NamedTuple):
+    """A paged FP8 cache: codes uint8 [num_pages, kv_heads, page_size / 8,
+    head_dim / 16, 8, 16] and block scales float32 [num_pages, kv_heads]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2] * 8
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3] * 16
+
+    @property
+    def kv_heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def num_pages(self) -> int:
+        return self.k.shape[0]
+
+
+class KvPlan(NamedTuple):
+    """Outputs of fp8_kv_plan (all int32, on the device)."""
+    q_offsets: torch.Tensor
+    kv_lens: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    used: torch.Tensor
+
+
+def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, device=None) -> KvCache:
+    """A zero-filled paged FP8 cache."""
+    if page_size not in KV_PAGE_SIZES or head_dim not in (64, 128):
+        raise ValueError("page_size is 16, 32, 64 or 128, head_dim 64 or 128")
+    device = torch.device("cuda") if device is None else torch.device(device)
+    shape = (num_pages, kv_heads, page_size // 8, head_dim // 16, 8, 16)
+    codes = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.full((num_pages, kv_heads), KV_MIN_SCALE, dtype=torch.float32, device=device)
+              for _ in range(2)]
+    return KvCache(*codes, *scales)
+
+
+def _kv_check_cache(cache: KvCache):
+    k, v, ks, vs = cache
+    _need_cuda(k, v, ks, vs)
+    if k.dim() != 6 or k.shape[4:] != (8, 16) or v.shape != k.shape or \
+            ks.shape != k.shape[:2] or vs.shape != ks.shape:
+        raise ValueError("cache codes are [num_pages, kv_heads, page_size / 8, head_dim / 16, 8, "
+                         "16] and scales [num_pages, kv_heads]")
+    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or ks.dtype != torch.float32 or \
+            vs.dtype != torch.float32:
+        raise ValueError("cache codes are uint8, scales float32")
+
+
+def _need_int32(**ts):
+    for name, t in ts.items():
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+
+
+def _same_device(first: torch.Tensor, *ts):
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors are on different devices")
+
+
+def fp8_kv_plan(q_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
+                free_pages: torch.Tensor, tokens: int, page_size: int,
+                plan: KvPlan | None = None) -> KvPlan:
+    """Places a step's new tokens in pages (fp8_kv_plan).  q_lens, kv_lens:
+    int32 [R], new and cached tokens of each request; block_table: int32 [R,
+    W], new entries written in place; free_pages: int32 [F], taken from the
+    front; tokens: rows of the step's token tensors.  Returns KvPlan
+    (q_offsets [R + 1], kv_lens after the step [R], positions and slots
+    [tokens], used [2]: pages taken, tokens without a page), in `plan`'s
+    tensors when given."""
+    _need_cuda(q_lens, kv_lens, block_table, free_pages, *(plan or ()))
+    _need_int32(q_lens=q_lens, kv_lens=kv_lens, block_table=block_table, free_pages=free_pages)
+    if block_table.dim() != 2:
+        raise ValueError("block_table is [requests, table_width]")
+    R, W = block_table.shape
+    if q_lens.shape != (R,) or kv_lens.shape != (R,):
+        raise ValueError("q_lens and kv_lens have one entry per row of block_table")
+    tokens, device = int(tokens), q_lens.device
+    _same_device(q_lens, kv_lens, block_table, free_pages, *(plan or ()))
+    if plan is None:
+        # one allocation, 4-byte aligned parts
+        buf = torch.empty(2 * R + 3 + 2 * max(tokens, 0), dtype=torch.int32, device=device)
+        plan = KvPlan(*buf.split([R + 1, R, max(tokens, 0), max(tokens, 0), 2]))
+    else:
+        _need_int32(**plan._asdict())
+        if [t.shape for t in plan] != [(R + 1,), (R,), (tokens,), (tokens,), (2,)]:
+            raise ValueError("plan tensors are [R + 1], [R], [tokens], [tokens], [2]")
+    with torch.cuda.device(device):
+        st = load().fp8_kv_plan(
+            q_lens.data_ptr(), kv_lens.data_ptr(), R, tokens, page_size, block_table.data_ptr(),
+            W, free_pages.data_ptr(), free_pages.numel(), plan.q_offsets.data_ptr(),
+            plan.kv_lens.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(),
+            plan.used.data_ptr(), _stream(device))
+    _check(st, "fp8_kv_plan")
+    return plan
+
+
+def _rows(x: torch.Tensor) -> int:
+    """Row stride of a token tensor whose rows are dense (any row stride)."""
+    want = 1
+    for d in range(x.dim() - 1, 0, -1):
+        if x.shape[d] > 1 and x.stride(d) != want:
+            raise ValueError("expected dense rows (only the row stride may differ)")
+        want *= x.shape[d]
+    return x.stride(0) if x.shape[0] > 1 else want
+
+
+def fp8_qk_norm_rope_append(qkv: torch.Tensor, cache: KvCache, positions: torch.Tensor,
+                            slots: torch.Tensor, cos_sin: torch.Tensor | None = None,
+                            q_gamma: torch.Tensor | None = None,
+                            k_gamma: torch.Tensor | None = None, eps: float = 1e-6,
+                            interleaved: bool = False,
+                            q: torch.Tensor | None = None) -> torch.Tensor:
+    """Per-head norms of queries and keys, the position rotation, and keys and
+    values quantized into the cache (fp8_qk_norm_rope_append).  qkv: [tokens,
+    (q_heads + 2 kv_heads) * head_dim], fp16 or bf16, rows at any stride;
+    positions, slots: int32 [tokens] (fp8_kv_plan); cos_sin: float32
+    [max_positions, rot] or None (no rotation); q_gamma, k_gamma: [head_dim]
+    or None (no norm).  Returns q [tokens, q_heads, head_dim]."""
+    _kv_check_cache(cache)
+    _need_cuda(positions, slots, cos_sin, q_gamma, k_gamma, q)
+    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
+        raise TypeError("expected CUDA tensors")
+    _need_int32(positions=positions, slots=slots)
+    hkv, dim = cache.kv_heads, cache.head_dim
+    if qkv.dim() != 2 or qkv.shape[1] % dim != 0:
+        raise ValueError("qkv is [tokens, (q_heads + 2 kv_heads) * head_dim]")
+    T, heads = qkv.shape[0], qkv.shape[1] // dim - 2 * hkv
+    if positions.shape != (T,) or slots.shape != (T,):
+        raise ValueError("positions and slots have one entry per token")
+    if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32):
+        raise ValueError("cos_sin is float32 [max_positions, rot]")
+    for gamma in (q_gamma, k_gamma):
+        if gamma is not None and (gamma.shape != (dim,) or gamma.dtype != qkv.dtype):
+            raise ValueError("q_gamma and k_gamma are [head_dim] of qkv's dtype")
+    if q is None:
+        q = torch.empty((T, max(heads, 0), dim), dtype=qkv.dtype, device=qkv.device)
+    elif q.shape != (T, heads, dim) or q.dtype != qkv.dtype:
+        raise ValueError("q is [tokens, q_heads, head_dim] of qkv's dtype")
+    _same_device(qkv, *cache, positions, slots, cos_sin, q_gamma, k_gamma, q)
+    with torch.cuda.device(qkv.device):
+        st = load().fp8_qk_norm_rope_append(
+            qkv.data_ptr(), _DTYPE_CODE.get(qkv.dtype, -1), T, _rows(qkv), heads, hkv, dim,
+            q_gamma.data_ptr() if q_gamma is not None else None,
+            k_gamma.data_ptr() if k_gamma is not None else None, float(eps),
+            cos_sin.data_ptr() if cos_sin is not None else None,
+            cos_sin.shape[0] if cos_sin is not None else 0,
+            cos_sin.shape[1] if cos_sin is not None else 0, 1 if interleaved else 0,
+            positions.data_ptr(), slots.data_ptr(), q.data_ptr(), cache.k.data_ptr(),
+            cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+            cache.num_pages, cache.page_size, _stream(qkv.device))
+    _check(st, "fp8_qk_norm_rope_append")
+    return q
+
+
+_attention_workspaces = {}
+
+
+def fp8_kv_attention_workspace(device=None) -> torch.Tensor:
+    """A workspace of fp8_kv_attention for the current stream of `device`:
+    allocated once per stream and reused (its counters zeroed), so calls on
+    different streams do not share one.  During a graph capture without such
+    a workspace the graph gets its own, zeroed at every replay."""
+    device = torch.device("cuda", torch.cuda.current_device() if device is None
+                          else torch.device(device).index or 0)
+    key = (device, _stream(device))
+    ws = _attention_workspaces.get(key)
+    if ws is None:
+        lib = load()
+        ws = torch.empty(lib.fp8_kv_attention_workspace_bytes(), dtype=torch.uint8, device=device)
+        ws[: lib.fp8_kv_attention_workspace_zero_bytes()].zero_()
+        if not torch.cuda.is_current_stream_capturing():
+            _attention_workspaces[key] = ws
+    return ws
+
+
+def fp8_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
+                     q_offsets: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int,
+                     sm_scale: float | None = None, window: int = 0, out_dtype=None,
+                     out_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, want_lse: bool = False,
+                     ws: torch.Tensor | None = None):
+    """Causal attention of q [tokens, q_heads, head_dim] (rows at any stride)
+    over the paged cache (fp8_kv_attention): decode, drafted tokens, prompt
+    chunks.  block_table: int32 [R, W]; q_offsets: int32 [R + 1], kv_lens:
+    int32 [R] after the step (fp8_kv_plan); max_q_len: host bound of a
+    request's new tokens.  sm_scale defaults to head_dim ** -0.5; window > 0
+    limits each row to its last `window` keys; out_dtype: q's (default) or
+    uint8 (E4M3 codes of out / out_scale).  Returns (out, lse or None)."""
+    _kv_check_cache(cache)
+    _need_cuda(block_table, q_offsets, kv_lens, out_scale, out, lse, ws)
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("expected CUDA tensors")
+    _need_int32(block_table=block_table, q_offsets=q_offsets, kv_lens=kv_lens)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q is [tokens, q_heads, head_dim]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table is [requests, table_width]")
+    R, W = block_table.shape
+    if q_offsets.shape != (R + 1,) or kv_lens.shape != (R,):
+        raise ValueError("q_offsets is [requests + 1], kv_lens [requests]")
+    T, heads, dim = q.shape
+    if out_dtype is None:
+        out_dtype = q.dtype if out is None else out.dtype
+    if out_dtype == torch.float8_e4m3fn:
+        out_dtype = torch.uint8
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=out_dtype, device=q.device)
+    elif out.shape != q.shape or _codes(out).dtype != out_dtype:
+        raise ValueError("out is [tokens, q_heads, head_dim] of out_dtype")
+    if out_scale is not None and (out_scale.dtype != torch.float32 or out_scale.numel() != 1):
+        raise ValueError("out_scale is one float32")
+    if lse is None and want_lse:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    elif lse is not None and (lse.shape != (T, heads) or lse.dtype != torch.float32):
+        raise ValueError("lse is float32 [tokens, q_heads]")
+    if ws is None:
+        ws = fp8_kv_attention_workspace(q.device)
+    _same_device(q, *cache, block_table, q_offsets, kv_lens, out_scale, out, lse, ws)
+    with torch.cuda.device(q.device):
+        st = load().fp8_kv_attention(
+            q.data_ptr(), _DTYPE_CODE.get(q.dtype, -1), T, _rows(q), heads, cache.kv_heads, dim,
+            cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+            cache.v_scale.data_ptr(), cache.num_pages, cache.page_size, block_table.data_ptr(), W,
+            q_offsets.data_ptr(), kv_lens.data_ptr(), R, int(max_q_len),
+            float(dim ** -0.5 if sm_scale is None else sm_scale), int(window),
+            out_scale.data_ptr() if out_scale is not None else None, out.data_ptr(),
+            _DTYPE_CODE.get(out_dtype, -1), lse.data_ptr() if lse is not None else None,
+            ws.data_ptr(), _stream(q.device))
+    _check(st, "fp8_kv_attention")
+    return out, lse

@@ -1,0 +1,48 @@
+// Pieces shared by the paged FP8 cache kernels: the cache's address
+// arithmetic, the programmatic launch, the host checks of a cache.
+#pragma once
+
+#include "common.cuh"
+
+namespace fp8l {
+
+constexpr int64_t kKvMaxRequests = 8192;
+
+// Byte offset of token `o` (in its page), dimension 16 c of page-and-head
+// `ph` = page * kv_heads + head: octets of tokens, then 16-byte chunks of
+// dimensions, then the octet's eight rows.
+__host__ __device__ __forceinline__ int64_t kv_chunk_offset(int64_t ph, int page_size, int dim, int o, int c) {
+    return ph * page_size * dim + static_cast<int64_t>(o >> 3) * 8 * dim + c * 128 + (o & 7) * 16;
+}
+
+inline bool kv_page_size_ok(int64_t page_size) {
+    return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128;
+}
+
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Launches `kernel` as a programmatic dependent of the preceding kernel on
+// the stream: its blocks may become resident before that kernel ends, and
+// run griddepcontrol.wait before their first global access.
+template <typename Params>
+inline int launch_dependent(void (*kernel)(Params), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                            const Params &p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FP8L_OK : FP8L_ECUDA;
+}
+
+__device__ __forceinline__ void grid_dependency_sync() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+}  // namespace fp8l

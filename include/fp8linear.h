@@ -418,6 +418,149 @@ FP8L_API int fp8_quant_per_tensor_noalloc(const void *x, int x_dtype, int64_t ro
                                           int64_t cols, uint8_t *q, float *scale,
                                           void *stream);
 
+/* ------------------------------------------------------------------------
+ * Paged FP8 key/value cache: the attention between the q/k/v product and the
+ * o product of a decode layer or a prompt chunk ("Marlin fp8": decode
+ * latency is quoted with a static cache; the pages define neither the cache
+ * nor the attention, so these are the plain Llama definitions over E4M3
+ * blocks).  fp8_kv_plan, fp8_qk_norm_rope_append and fp8_kv_attention are
+ * additions to version 7: a caller tells their presence by the symbols.
+ *
+ * Cache layout.  A page holds `page_size` (16, 32, 64 or 128) consecutive
+ * tokens of one sequence.  k_cache and v_cache are each
+ *     uint8 [num_pages][kv_heads][page_size / 8][head_dim / 16][8][16]:
+ * token o of a page and dimension d of its head are at octet o / 8, chunk
+ * d / 16, row o % 8, byte d % 16.  The 128-byte [8][16] blocks are the core
+ * matrices the tensor core reads, and the tokens [8a, 8b) of a page and head
+ * are one contiguous run of bytes.  k_scale and v_scale are
+ * float32 [num_pages][kv_heads]: the value of a code c is dec(c) * scale.
+ * num_pages * page_size < 2^31; head_dim is 64 or 128.  A block table is
+ * int32 [requests][table_width]: entry [r][b] is the page of the tokens
+ * [b * page_size, (b + 1) * page_size) of request r.
+ * int32 and float arrays need their natural alignment only; caches, q, qkv
+ * and out are 16-byte aligned. */
+
+/* Smallest block scale, that of a block of zeros (a scale of 1, as the
+ * linear layer gives a tensor of zeros, would be large beside the scales of
+ * other blocks of the same sequence). */
+#define FP8L_KV_MIN_SCALE 5.421010862427522e-20f /* 2^-64 */
+
+/* Places the new tokens of a step in pages: block table and slot map built
+ * on the GPU from the requests' lengths, without a host round trip.
+ *
+ * Request r has kv_lens[r] tokens in the cache and q_lens[r] new ones
+ * (negative lengths count as 0); its new tokens are the rows
+ * q_offsets[r] .. q_offsets[r+1]-1 of the step's token tensors of `tokens`
+ * rows (requests in order; tokens past the last row are cut off).  With
+ *   old  = ceil(kv / page_size),   need = max(0, min(ceil((kv + q) / page_size),
+ *   table_width) - old),   base = sum of need over the requests before,
+ * new block k < need of the request is free_pages[base + k], written to
+ * block_table[r][old + k] (-1 when base + k >= num_free); the other entries
+ * of the table are kept.  Then
+ *   q_offsets[requests + 1]  the row offsets
+ *   kv_lens_out[requests]    min(kv + q, page_size * (blocks it has)): the
+ *                            lengths after the step
+ *   positions[tokens]        kv + (row - q_offsets[r]); 0 for rows past the
+ *                            last request
+ *   slots[tokens]            page * page_size + position % page_size; -1 for
+ *                            a token without a page and for rows past the
+ *                            last request
+ *   used[2]                  pages taken from the front of free_pages; new
+ *                            tokens without a page (0: all were placed)
+ * q_lens, kv_lens: int32 [requests]; block_table: int32 [requests,
+ * table_width], in and out; free_pages: int32 [num_free].  No input other
+ * than block_table is written, so a call may be repeated with the same
+ * result.  1 <= requests <= 8192, 0 <= tokens < 2^31, table_width >= 1,
+ * num_free * page_size < 2^31,
+ * the sums of the lengths fit an int32. */
+FP8L_API int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_t requests,
+                         int64_t tokens, int64_t page_size, int32_t *block_table,
+                         int64_t table_width, const int32_t *free_pages, int64_t num_free,
+                         int32_t *q_offsets, int32_t *kv_lens_out, int32_t *positions,
+                         int32_t *slots, int32_t *used, void *stream);
+
+/* The step between the q/k/v product and the attention, in one launch: norms
+ * of queries and keys per head, the position rotation, and the keys and
+ * values quantized into the paged cache.
+ *
+ * qkv: [tokens, (q_heads + 2 kv_heads) * head_dim] of dtype (FP8L_F16 or
+ * FP8L_BF16), rows `qkv_stride` elements apart (a multiple of 8): q heads,
+ * then k heads, then v heads.  In float32, per token and head:
+ *   q, k:  x <- x * (1 / sqrt(mean_d x_d^2 + eps)) * gamma_d   (gamma NULL:
+ *          no norm; q_gamma and k_gamma are [head_dim] of dtype)
+ *   q, k:  the first rot dimensions rotate by the token's row of cos_sin:
+ *          (a, b) <- (a cos_i - b sin_i, b cos_i + a sin_i), i < rot / 2, the
+ *          pair being dimensions (i, i + rot/2), or (2i, 2i+1) when
+ *          `interleaved`; cos_sin: float32 [max_positions, rot], cosines then
+ *          sines; rot = 0 or a multiple of 16 up to head_dim; positions:
+ *          int32 [tokens], clamped into the table
+ *   q:     rounded to dtype into q_out [tokens, q_heads, head_dim]
+ *   k, v:  quantized from float32 into the cache at slots[token] (int32, as
+ *          fp8_kv_plan writes them; a slot out of range leaves the token
+ *          out).  Per page and head, over the call's tokens in the page:
+ *            s_new = max(amax / 448, FP8L_KV_MIN_SCALE)
+ *            s     = s_new when the first of them has offset 0 in the page,
+ *                    else max(s_old, s_new)
+ *            code  = E4M3(x / s)   (IEEE quotient, saturating, as
+ *                    fp8_quant_per_tensor)
+ *          and when s > s_old the codes of the page's earlier tokens become
+ *          E4M3((dec(c) * s_old) / s).
+ * The slots of a page's tokens are ascending and consecutive in token order,
+ * and the pages are owned by one request each.  Deterministic; no workspace.
+ * q_heads a positive multiple of kv_heads; (q_heads + 2 kv_heads) *
+ * head_dim <= 2^20; eps >= 0 and finite. */
+FP8L_API int fp8_qk_norm_rope_append(const void *qkv, int dtype, int64_t tokens,
+                                     int64_t qkv_stride, int64_t q_heads, int64_t kv_heads,
+                                     int64_t head_dim, const void *q_gamma, const void *k_gamma,
+                                     float eps, const float *cos_sin, int64_t max_positions,
+                                     int64_t rot, int interleaved, const int32_t *positions,
+                                     const int32_t *slots, void *q_out, uint8_t *k_cache,
+                                     uint8_t *v_cache, float *k_scale, float *v_scale,
+                                     int64_t num_pages, int64_t page_size, void *stream);
+
+/* Bytes of fp8_kv_attention's workspace, and how many of them, from the
+ * start, the caller fills with zeros once (status word and merge counters;
+ * every call leaves the counters at zero).  As with the other workspace,
+ * calls that may overlap on the GPU need one each; fp8l_read_status reads
+ * its status word. */
+FP8L_API size_t fp8_kv_attention_workspace_bytes(void);
+FP8L_API size_t fp8_kv_attention_workspace_zero_bytes(void);
+
+/* Causal attention of a step's queries over the paged cache: decode (one
+ * token per request), a few drafted tokens, and prompt chunks, ragged.
+ *
+ * Row i (0 <= i < n) of request r, n = q_offsets[r+1] - q_offsets[r], has
+ * position p = kv_lens[r] - n + i (its own key is in the cache) and sees the
+ * keys j <= p, with window > 0 only those j > p - window.  Per query head h
+ * (kv head h / (q_heads / kv_heads)):
+ *   s_j = sm_scale * q . k_j,    out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = ln sum_j exp(s_j)
+ * with k_j, v_j the cache's values.  A row that sees no key gives out = 0
+ * and lse = -inf.  Products and sums are float32 (the tensor core's
+ * accumulator); the softmax weights enter the second product rounded to at
+ * least 11 bits, or 2^-25 of the row's largest weight.
+ *
+ * q: [tokens, q_heads, head_dim] of q_dtype (FP8L_F16 or FP8L_BF16), rows
+ * `q_stride` elements apart (a multiple of 8); q_offsets: int32
+ * [requests + 1]; kv_lens: int32 [requests], lengths after the step's
+ * append; block_table as above, its entries for the tokens below kv_lens
+ * valid pages (others are never read as data); max_q_len: an upper bound of
+ * n known on the host (it selects the kernel; 0 means no rows).
+ * out: [tokens, q_heads, head_dim] of out_dtype: q_dtype, or FP8L_E4M3 codes
+ * of out / out_scale[0] (the static input scale of the o product); rows
+ * outside the requests are not written.  lse: NULL or float [tokens,
+ * q_heads].  0 <= window; 0 < sm_scale, finite.  1 <= requests <= 8192.
+ * Deterministic: the same call gives the same bits. */
+FP8L_API int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_stride,
+                              int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                              const uint8_t *k_cache, const uint8_t *v_cache,
+                              const float *k_scale, const float *v_scale, int64_t num_pages,
+                              int64_t page_size, const int32_t *block_table,
+                              int64_t table_width, const int32_t *q_offsets,
+                              const int32_t *kv_lens, int64_t requests, int64_t max_q_len,
+                              float sm_scale, int64_t window, const float *out_scale, void *out,
+                              int out_dtype, float *lse, void *workspace, void *stream);
+
 /* Waits for `stream`, then reads and clears the workspace's status word and
  * the library's own status word on the current device (where
  * fp8_w8a16_mm, which takes no workspace, records its time-outs; looked up

@@ -1,0 +1,277 @@
+"""fp8_kv_attention against the formulas in 64 bits.
+
+Bounds, with A = sum_j p_j |v_j| of an output: rounding to the output's type
+(unit roundoff 2^-8 bf16, 2^-11 fp16 of it); weights rounded to 11 bits (2^-11 A), or to
+2^-25 of the row's largest weight w = p * block scale (n keys of at most 448);
+float32 sums and exponentials (2^-17 A); the scores' float32 sums (D
+roundings of 2^-24 of sum_d |q_d k_d|, twice for numerator and denominator),
+which change every weight by that factor.  lse: the same score error plus
+2^-18 of itself.  E4M3 outputs are the rounding of a value that close."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_quantized_linear_gb300 as fl
+import kv_ref
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+def make(dtype, page, hq, hkv, dim, q_lens, kv_lens, seed=0, sink=0.0, spare=3, v_spread=0.5,
+         zero_pages=False, stride=None, magnitude=1.0):
+    """Queries, a cache whose unused parts hold NaN codes and NaN scales, and
+    the 64-bit keys and values of each request."""
+    rng = np.random.default_rng(seed)
+    gen = torch.Generator().manual_seed(seed)
+    blocks = [-(-int(n) // page) for n in kv_lens]
+    num_pages = sum(blocks) + spare
+    ids = rng.permutation(num_pages)
+    width = max(1, max(blocks)) + 1
+    table = np.full((len(kv_lens), width), -1)
+    codes = np.full((2, num_pages, hkv, page, dim), 0x7F, np.uint8)
+    scales = np.full((2, num_pages, hkv), np.nan, np.float32)
+    u = rng.standard_normal((hkv, dim))
+    u /= np.linalg.norm(u, axis=1, keepdims=True)
+    at = 0
+    for r, L in enumerate(kv_lens):
+        table[r, :blocks[r]] = ids[at:at + blocks[r]]
+        at += blocks[r]
+        for b in range(blocks[r]):
+            n = min(page, int(L) - b * page)
+            pg = table[r, b]
+            c = rng.integers(0, 256, (2, hkv, n, dim), dtype=np.uint8)
+            c[(c & 127) == 127] = 3
+            # codes of normal-like magnitude: exponents 4..14
+            c[:, :, :, :] = (c & 0x87) | (rng.integers(4, 15, c.shape) << 3).astype(np.uint8)
+            c[(c & 127) == 127] = 0x70
+            codes[:, pg, :, :n] = c
+            scales[0, pg] = np.exp(0.2 * rng.standard_normal(hkv)) / 100 * magnitude
+            scales[1, pg] = np.exp(v_spread * rng.standard_normal(hkv)) / 100
+            if zero_pages and b % 2:
+                codes[1, pg, :, :n] = 0
+                scales[1, pg] = kv_ref.MIN_SCALE
+            if sink and b == 0:
+                k0 = np.clip(u * 200, -240, 240)
+                codes[0, pg, :, 0] = torch.from_numpy(k0).to(torch.float8_e4m3fn).view(
+                    torch.uint8).numpy()
+    T = int(sum(q_lens))
+    x = torch.randn(T, stride or hq * dim, generator=gen)
+    if sink:
+        x[:, :hq * dim] += sink * torch.from_numpy(np.repeat(u, hq // hkv, 0).reshape(-1)).float()
+    q = x.to(dtype).to(DEV)[:, :hq * dim].unflatten(1, (hq, dim))
+    cache = fl.KvCache(kv_ref.to_layout(codes[0]).to(DEV), kv_ref.to_layout(codes[1]).to(DEV),
+                       torch.from_numpy(scales[0]).to(DEV), torch.from_numpy(scales[1]).to(DEV))
+    value = torch.from_numpy(kv_ref.TABLE).to(DEV)
+
+    def rows(i):
+        out = []
+        for r, L in enumerate(kv_lens):
+            pg = torch.from_numpy(table[r, :blocks[r]].copy()).to(DEV)
+            c = value[torch.from_numpy(codes[i]).to(DEV)[pg].long()]
+            s = torch.from_numpy(scales[i]).to(DEV)[pg].double()
+            y = (c * s[:, :, None, None]).permute(1, 0, 2, 3).reshape(hkv, -1, dim)
+            out.append(y[:, :int(L)].contiguous())
+        return out
+
+    off = np.concatenate([[0], np.cumsum(q_lens)])
+    return dict(q=q, cache=cache, table=i32(table), off=off, kv=np.asarray(kv_lens), k=rows(0),
+                v=rows(1), v_scale=scales[1], n=max(int(x) for x in q_lens))
+
+
+def run(s, **kw):
+    return fl.fp8_kv_attention(s["q"], s["cache"], s["table"], i32(s["off"]), i32(s["kv"]),
+                               kw.pop("max_q_len", s["n"]), **kw)
+
+
+def check(s, window=0, out="same", sm_scale=None, **kw):
+    dim = s["q"].shape[2]
+    scale = dim ** -0.5 if sm_scale is None else sm_scale
+    os = torch.full((1,), 0.02, device=DEV) if out == "e4m3" else None
+    got, lse = run(s, window=window, out_dtype=torch.uint8 if out == "e4m3" else None,
+                   out_scale=os, want_lse=True, sm_scale=sm_scale, **kw)
+    want, want_lse, spread, reach = kv_ref.attention(s["q"].double(), s["k"], s["v"], s["off"],
+                                                     s["kv"], scale, window)
+    longest = max([int(n) for n in s["kv"]] + [1])
+    top = np.nanmax(np.where(np.isnan(s["v_scale"]), 0, s["v_scale"]))
+    score = dim * 2.0 ** -24 * reach[:, :, None]
+    slack = spread * (2.0 ** -11 + 2.0 ** -17 + 2 * score) + longest * 448 * top * 2.0 ** -25
+    if out == "e4m3":
+        # half a step of the coded value, and the saturation
+        c = kv_ref.TABLE[got.cpu().numpy()]
+        ok = kv_ref.nearest_code_ok((want / 0.02).cpu().numpy(), c, (slack / 0.02).cpu().numpy())
+        assert ok.all(), (np.argwhere(~ok)[:5], c[~ok][:5], (want / 0.02).cpu().numpy()[~ok][:5])
+    else:
+        half = 2.0 ** -8 if got.dtype == torch.bfloat16 else 2.0 ** -11
+        err = (got.double() - want).abs()
+        bound = slack + half * (want.abs() + slack) + 2.0 ** -25
+        assert bool((err <= bound).all()), (err / bound).max().item()
+    empty = want_lse == -math.inf
+    assert torch.equal(lse == -math.inf, empty)
+    e = (lse.double() - want_lse).abs()[~empty]
+    assert bool((e <= (2.0 ** -18 * (1 + want_lse.abs()) + score[:, :, 0])[~empty]).all()), e.max()
+    if empty.any():
+        assert bool((got[empty] == 0).all())
+    return got, lse
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("hq,hkv,dim", [(8, 2, 64), (32, 8, 128), (6, 2, 128), (3, 3, 64)])
+def test_decode(page, hq, hkv, dim, dtype):
+    kv = [1, 2, 15, 16, 17, 127, 128, 129, 300, 1000]
+    check(make(dtype, page, hq, hkv, dim, [1] * len(kv), kv, seed=page + hq))
+
+
+@pytest.mark.parametrize("group", [1, 2, 5, 8, 16, 32, 48])
+def test_query_groups(group):
+    check(make(torch.bfloat16, 64, 2 * group, 2, 128, [1, 1, 1], [700, 33, 256], seed=group))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", [2, 3, 5, 8, 13])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_drafted_tokens(n, dim, dtype):
+    kv = [n, n + 1, 64 + n, 500, 129]
+    check(make(dtype, 16, 8, 2, dim, [n] * 5, kv, seed=n), window=0)
+    check(make(dtype, 64, 4, 1, dim, [n, 0, 1, n, 2], kv, seed=n), window=100)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page,dim,window", [(16, 64, 0), (64, 128, 0), (128, 128, 200),
+                                             (32, 128, 1), (64, 64, 77)])
+def test_prompts(page, dim, window, dtype):
+    q = [130, 0, 1, 257, 64, 31]
+    kv = [130, 40, 900, 600, 64, 1031]
+    check(make(dtype, page, 8, 2, dim, q, kv, seed=page + window), window=window)
+
+
+def test_long_prompt_few_heads():
+    check(make(torch.bfloat16, 64, 2, 1, 128, [1500], [3001], seed=3))
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_one_long_context(n):
+    s = make(torch.bfloat16, 128, 8, 1, 128, [n], [70001], seed=4, sink=8.0)
+    check(s)
+    check(s, window=33333)
+
+
+@pytest.mark.parametrize("q_lens", [[1] * 37, [200, 1, 7]])
+def test_e4m3_output(q_lens):
+    kv = [n + 61 * (i + 1) for i, n in enumerate(q_lens)]
+    check(make(torch.bfloat16, 64, 8, 2, 128, q_lens, kv, seed=9), out="e4m3")
+    check(make(torch.float16, 32, 4, 4, 64, q_lens, kv, seed=9), out="e4m3", window=40)
+
+
+@pytest.mark.parametrize("q_lens", [[5, 1, 3], [90, 1, 40]])
+def test_rows_that_see_no_key(q_lens):
+    # fewer keys than rows: the first rows have nothing to see
+    check(make(torch.bfloat16, 16, 4, 2, 64, q_lens, [3, 0, 2], seed=1))
+
+
+@pytest.mark.parametrize("n", [1, 100])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_first_token_that_draws_the_weight(n, dtype):
+    check(make(dtype, 64, 8, 2, 128, [n], [4000], seed=6, sink=14.0))
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_block_scales_far_apart(n):
+    check(make(torch.bfloat16, 16, 8, 2, 128, [n], [777], seed=7, v_spread=3.0))
+    check(make(torch.bfloat16, 16, 8, 2, 128, [n], [777], seed=7, zero_pages=True))
+
+
+@pytest.mark.parametrize("n", [1, 100])
+@pytest.mark.parametrize("magnitude", [1e-3, 30.0])
+def test_flat_and_sharp_scores(n, magnitude):
+    check(make(torch.bfloat16, 32, 8, 2, 128, [n], [900], seed=8, magnitude=magnitude))
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_strided_queries_and_scale(n):
+    s = make(torch.bfloat16, 64, 4, 2, 128, [n, n], [500, 129], seed=2, stride=8 * 128)
+    assert s["q"].stride(0) == 1024
+    check(s, sm_scale=0.2)
+
+
+@pytest.mark.parametrize("n", [1, 3, 80])
+def test_rows_outside_the_requests_are_not_written(n):
+    s = make(torch.bfloat16, 64, 4, 2, 128, [n, n], [200, 100], seed=2)
+    T = 2 * n
+    q = torch.cat([s["q"], torch.full((3, 4, 128), math.nan, device=DEV).bfloat16()])
+    out = torch.full((T + 3, 4, 128), 7.0, device=DEV, dtype=torch.bfloat16)
+    a, _ = run(s)
+    b, _ = run(dict(s, q=q), out=out)
+    assert torch.equal(b[:T], a) and bool((b[T:] == 7.0).all())
+
+
+@pytest.mark.parametrize("n", [1, 4, 90])
+def test_same_bits_every_time_and_on_another_stream(n):
+    s = make(torch.bfloat16, 64, 8, 2, 128, [n] * 5, [3000, 200, 1, 800, 5000], seed=2)
+    first, lse = run(s, want_lse=True)
+    for _ in range(3):
+        again, l2 = run(s, want_lse=True)
+        assert torch.equal(first, again) and torch.equal(lse, l2)
+    side = torch.cuda.Stream(DEV)
+    side.wait_stream(torch.cuda.current_stream(DEV))
+    with torch.cuda.stream(side):
+        other, _ = run(s)
+    main, _ = run(s)  # may overlap the other stream's call
+    side.synchronize()
+    assert torch.equal(first, other) and torch.equal(first, main)
+
+
+@pytest.mark.parametrize("n", [1, 4, 90])
+def test_graph_capture_and_replay_with_new_lengths(n):
+    s = make(torch.float16, 16, 8, 2, 64, [n] * 3, [1000, 1200, 950], seed=5)
+    off, kv = i32(s["off"]), i32(s["kv"])
+    call = lambda: fl.fp8_kv_attention(s["q"], s["cache"], s["table"], off, kv, s["n"])  # noqa: E731
+    eager, _ = call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, _ = call()
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+    kv.copy_(i32([n, 700, 333]))
+    eager, _ = call()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_offsets_past_32_bits(n):
+    # pages beyond 4 GB of codes, slots beyond 2^22
+    page, hkv, dim = 128, 8, 128
+    s = make(torch.bfloat16, page, 8, hkv, dim, [n, n], [400, 150], seed=3)
+    small = s["cache"]
+    num = 40000
+    shift = num - small.num_pages
+    assert num * page * hkv * dim > 2 ** 32
+    big = [torch.empty((num,) + tuple(t.shape[1:]), dtype=t.dtype, device=DEV) for t in small]
+    for b, t in zip(big, small):
+        b[shift:] = t
+    table = torch.where(s["table"] >= 0, s["table"] + shift, s["table"])
+    a, _ = run(s)
+    b, _ = run(dict(s, cache=fl.KvCache(*big), table=table))
+    assert torch.equal(a, b)
+
+
+def test_no_rows():
+    s = make(torch.bfloat16, 64, 4, 2, 128, [1], [200], seed=2)
+    out, lse = fl.fp8_kv_attention(s["q"][:0], s["cache"], s["table"], i32([0, 0]), i32([200]), 1,
+                                   want_lse=True)
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+    fresh = torch.full((1, 4, 128), 5.0, device=DEV, dtype=torch.bfloat16)
+    out, _ = fl.fp8_kv_attention(s["q"], s["cache"], s["table"], i32([0, 0]), i32([200]), 1,
+                                 out=fresh)
+    assert bool((out == 5.0).all())

@@ -1,0 +1,79 @@
+"""fp8_kv_plan against a loop over requests: block tables, slots, positions,
+offsets and lengths are whole numbers and have to be equal."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_quantized_linear_gb300 as fl
+import kv_ref
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+def check(q, kv, page, tokens=None, width=None, free=None, seed=0):
+    rng = np.random.default_rng(seed)
+    q, kv = np.asarray(q), np.asarray(kv)
+    tokens = int(np.maximum(q, 0).sum()) if tokens is None else tokens
+    old = -(-np.maximum(kv, 0) // page)
+    total = -(-(np.maximum(kv, 0) + np.maximum(q, 0)) // page)
+    width = max(1, int(total.max())) if width is None else width
+    ids = rng.permutation(int(total.sum()) + 9)
+    table = np.full((len(q), width), -1)
+    at = 0
+    for r in range(len(q)):
+        n = min(int(old[r]), width)
+        table[r, :n] = ids[at:at + n]
+        at += n
+    pages = ids[at:] if free is None else ids[at:at + free]
+    want = kv_ref.plan(q, kv, table, pages, tokens, page)
+    t = i32(table)
+    for _ in range(2):  # a repeated call gives the same
+        p = fl.fp8_kv_plan(i32(q), i32(kv), t, i32(pages), tokens, page)
+        for name in ("q_offsets", "kv_lens", "positions", "slots", "used"):
+            assert np.array_equal(getattr(p, name).cpu().numpy(), want[name]), name
+        assert np.array_equal(t.cpu().numpy(), want["table"])
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("R", [1, 2, 63, 513, 1500])
+def test_random_lengths(R, page):
+    rng = np.random.default_rng(R * page)
+    check(rng.integers(0, 40, R), rng.integers(0, 700, R), page, seed=R)
+
+
+def test_decode_step_and_page_boundaries():
+    check(np.ones(130, int), np.arange(130), 16)
+    check(np.ones(5, int), [0, 15, 16, 17, 32], 16)
+
+
+def test_long_prompts():
+    check([20001, 0, 3, 9999], [5, 100, 0, 64], 64)
+
+
+def test_empty_requests_and_negative_lengths():
+    check([0, 0, 0], [0, 5, 16], 16)
+    check([0, -4, 7, 0], [0, 3, -2, 0], 32)
+
+
+def test_padded_and_cut_rows():
+    check([3, 2], [10, 0], 16, tokens=11)   # rows past the last request
+    check([3, 9, 4], [10, 0, 20], 16, tokens=7)  # the last tokens do not fit
+
+
+def test_pages_run_out():
+    check([30, 40, 50], [3, 16, 31], 16, free=4)
+    check([30, 40], [3, 16], 16, free=0)
+
+
+def test_table_width_limits_a_request():
+    check([100, 20], [10, 0], 16, width=4)
+
+
+def test_most_requests():
+    rng = np.random.default_rng(5)
+    check(rng.integers(0, 3, 8192), rng.integers(0, 50, 8192), 16, seed=2)
