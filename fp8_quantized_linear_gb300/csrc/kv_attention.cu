@@ -9,39 +9,21 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "kv_device.cuh"
-#include "quant_device.cuh"
-#include "tc_device.cuh"
+#include <atomic>
+
+#include "kv_attention_decode.cuh"
+#include "kv_attention_params.cuh"
 
 namespace fp8l {
 namespace {
 
 constexpr int kAttThreads = 128;
 
-struct AttnParams {
-    const uint16_t *q;
-    int tokens;
-    int64_t q_stride;
-    int q_heads, kv_heads, dim;
-    const uint8_t *k_cache, *v_cache;
-    const float *k_scale, *v_scale;
-    int num_pages, page_shift;
-    const int32_t *block_table;
-    int table_width;
-    const int32_t *q_offsets, *kv_lens;
-    int requests;
-    float sm_scale;
-    int window;
-    const float *out_scale;
-    void *out;
-    int q_dtype, out_dtype;
-    float *lse;
-};
-
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
 }
 
+template <int QDT, int DIM>
 __global__ void __launch_bounds__(kAttThreads) kv_attention_kernel(const AttnParams p) {
     __shared__ float qs[128], ws[kAttThreads], red[8];
     grid_dependency_sync();
@@ -60,10 +42,10 @@ __global__ void __launch_bounds__(kAttThreads) kv_attention_kernel(const AttnPar
     const int first = p.window > 0 ? max(0, last - p.window + 1) : 0;
     const int g = h / (p.q_heads / p.kv_heads);
     const int P = 1 << p.page_shift;
-    if (tid < p.dim) {
-        const uint16_t raw = p.q[static_cast<int64_t>(t) * p.q_stride + h * p.dim + tid];
-        qs[tid] = (p.q_dtype == FP8L_BF16 ? __uint_as_float(static_cast<uint32_t>(raw) << 16)
-                                          : __half2float(__ushort_as_half(raw))) * p.sm_scale;
+    if (tid < DIM) {
+        const uint16_t raw = p.q[static_cast<int64_t>(t) * p.q_stride + h * DIM + tid];
+        qs[tid] = (QDT == FP8L_BF16 ? __uint_as_float(static_cast<uint32_t>(raw) << 16)
+                                          : __half2float(__ushort_as_half(raw))) * p.score_scale;
     }
     float m = -INFINITY, l = 0.0f, acc = 0.0f;
     __syncthreads();
@@ -76,9 +58,9 @@ __global__ void __launch_bounds__(kAttThreads) kv_attention_kernel(const AttnPar
                                  p.num_pages - 1);
             ph = static_cast<int64_t>(page) * p.kv_heads + g;
             float dot = 0.0f;
-            for (int c = 0; c < p.dim / 16; ++c) {
+            for (int c = 0; c < DIM / 16; ++c) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(
-                    p.k_cache + kv_chunk_offset(ph, P, p.dim, j & (P - 1), c));
+                    p.k_cache + kv_chunk_offset(ph, P, DIM, j & (P - 1), c));
                 const uint8_t *b = reinterpret_cast<const uint8_t *>(&u);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) dot = fmaf(qs[16 * c + i], e4m3_value(b[i]), dot);
@@ -91,8 +73,8 @@ __global__ void __launch_bounds__(kAttThreads) kv_attention_kernel(const AttnPar
         __syncthreads();
         mt = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
         const float mn = fmaxf(m, mt);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - mn);
-        const float w = s == -INFINITY ? 0.0f : expf(s - mn);
+        const float keep = m == -INFINITY ? 0.0f : exp2f(m - mn);
+        const float w = s == -INFINITY ? 0.0f : exp2f(s - mn);
         ws[tid] = w;
         float sum = w;
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -101,32 +83,62 @@ __global__ void __launch_bounds__(kAttThreads) kv_attention_kernel(const AttnPar
         l = l * keep + ((red[4] + red[5]) + (red[6] + red[7]));
         acc *= keep;
         m = mn;
-        if (tid < p.dim) {
+        if (tid < DIM) {
             for (int i = max(first - j0, 0); i < min(kAttThreads, last + 1 - j0); ++i) {
                 const int k = j0 + i;
                 const int page = min(max(p.block_table[static_cast<int64_t>(r) * p.table_width + (k >> p.page_shift)], 0),
                                      p.num_pages - 1);
                 const int64_t vh = static_cast<int64_t>(page) * p.kv_heads + g;
-                const uint8_t c = p.v_cache[kv_chunk_offset(vh, P, p.dim, k & (P - 1), tid >> 4) + (tid & 15)];
+                const uint8_t c = p.v_cache[kv_chunk_offset(vh, P, DIM, k & (P - 1), tid >> 4) + (tid & 15)];
                 acc = fmaf(ws[i] * p.v_scale[vh], e4m3_value(c), acc);
             }
         }
         __syncthreads();
     }
     const float o = l > 0.0f ? acc / l : 0.0f;
-    const int64_t at = (static_cast<int64_t>(t) * p.q_heads + h);
-    if (tid < p.dim) {
-        if (p.out_dtype == FP8L_E4M3)
-            static_cast<uint8_t *>(p.out)[at * p.dim + tid] = code_of(o, p.out_scale[0]);
-        else
-            static_cast<uint16_t *>(p.out)[at * p.dim + tid] =
-                static_cast<uint16_t>(pack_out16(o, o, p.out_dtype) & 0xFFFFu);
-    }
-    if (tid == 0 && p.lse != nullptr) p.lse[at] = l > 0.0f ? m + logf(l) : -INFINITY;
+    const float x[1] = {o};
+    if (tid < DIM) attn_store<1>(p, t, h, DIM, tid, x);
+    if (tid == 0 && p.lse != nullptr) attn_store_lse(p, t, h, m, l);
 }
 
-constexpr size_t kAttnZeroBytes = 4096;
-constexpr size_t kAttnWorkspaceBytes = 4096;
+// Workspace: status word, merge counters (zero between calls), partials
+constexpr size_t kAttnCountersOffset = 64;
+constexpr size_t kAttnZeroBytes = 2048;
+constexpr int kDecMaxRows = 16;
+constexpr size_t kAttnWorkspaceBytes =
+    kAttnZeroBytes + sizeof(float) * 2 * kDecMaxCtas * kDecMaxRows * (128 + 2);
+static_assert(kAttnCountersOffset + 4 * kDecMaxCtas <= kAttnZeroBytes, "counters fit");
+
+constexpr int kDecSmemPerCta = 113 * 1024 - 512;  // two CTAs per SM
+
+template <int QDT, int DIM, int ROWS>
+int launch_decode(AttnParams p, int sms, cudaStream_t stream) {
+    using Sm = DecSmem<QDT, DIM, ROWS>;
+    int stages = (kDecSmemPerCta - Sm::kFixedBytes) / Sm::kStageBytes;
+    stages = stages < kDecMaxStages ? stages : kDecMaxStages;
+    p.stages = stages;
+    const int smem = stages * Sm::kStageBytes + Sm::kFixedBytes;
+    auto kernel = kv_attention_decode_kernel<QDT, DIM, ROWS>;
+    static std::atomic<unsigned> ready{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FP8L_ECUDA;
+    if (!(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+            return FP8L_ECUDA;
+        ready.fetch_or(1u << dev, std::memory_order_release);
+    }
+    const int ctas = 2 * sms < kDecMaxCtas ? 2 * sms : kDecMaxCtas;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), kDecThreads, smem, stream, p);
+}
+
+template <int QDT, int DIM>
+int launch_attention(const AttnParams &p, int64_t rows, int sms, cudaStream_t stream) {
+    if (rows <= 8) return launch_decode<QDT, DIM, 8>(p, sms, stream);
+    if (rows <= 16) return launch_decode<QDT, DIM, 16>(p, sms, stream);
+    return launch_dependent(kv_attention_kernel<QDT, DIM>, dim3(static_cast<unsigned>(p.tokens) * p.q_heads),
+                            kAttThreads, 0, stream, p);
+}
 
 }  // namespace
 }  // namespace fp8l
@@ -170,7 +182,6 @@ int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_strid
     p.q_stride = q_stride;
     p.q_heads = static_cast<int>(q_heads);
     p.kv_heads = static_cast<int>(kv_heads);
-    p.dim = static_cast<int>(head_dim);
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.k_scale = k_scale;
@@ -182,15 +193,28 @@ int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_strid
     p.q_offsets = q_offsets;
     p.kv_lens = kv_lens;
     p.requests = static_cast<int>(requests);
-    p.sm_scale = sm_scale;
+    p.score_scale = sm_scale * 1.44269504088896341f;
     p.window = static_cast<int>(window < INT32_MAX ? window : 0);
     p.out_scale = out_scale;
     p.out = out;
-    p.q_dtype = q_dtype;
     p.out_dtype = out_dtype;
     p.lse = lse;
-    return launch_dependent(kv_attention_kernel, dim3(static_cast<unsigned>(tokens * q_heads)), kAttThreads, 0,
-                            as_stream(stream), p);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.status = status_word(workspace);
+    p.counters = reinterpret_cast<unsigned *>(ws + kAttnCountersOffset);
+    p.partials = reinterpret_cast<float *>(ws + kAttnZeroBytes);
+    const WaitConfig waits = wait_config();
+    p.wait_cycles = waits.cycles;
+    p.stall = waits.stall;
+    p.stages = 0;
+    // query rows of one request and kv head at most
+    const int64_t rows = (max_q_len < tokens ? max_q_len : tokens) * (q_heads / kv_heads);
+    const cudaStream_t s = as_stream(stream);
+    if (q_dtype == FP8L_BF16)
+        return head_dim == 128 ? launch_attention<FP8L_BF16, 128>(p, rows, sms, s)
+                               : launch_attention<FP8L_BF16, 64>(p, rows, sms, s);
+    return head_dim == 128 ? launch_attention<FP8L_F16, 128>(p, rows, sms, s)
+                           : launch_attention<FP8L_F16, 64>(p, rows, sms, s);
 }
 
 }  // extern "C"
