@@ -1,11 +1,8 @@
 // Causal attention over the paged FP8 cache (fp8_kv_attention).
 //
-//   s_j = sm_scale q . k_j,   out = sum_j exp(s_j) v_j / sum_j exp(s_j)
-//
-// One block per (token, query head): tiles of 128 keys, one key per thread
-// for the scores, one dimension per thread for the weighted values, with the
-// running maximum m and sum l of the softmax carried from tile to tile
-// (a larger maximum rescales l and the accumulator by exp(m_old - m_new)).
+// Few query rows per request and kv head go to the decode kernel
+// (kv_attention_decode.cuh), more to the prompt kernel
+// (kv_attention_prompt.cuh); this file checks the arguments and chooses.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -13,131 +10,66 @@
 
 #include "kv_attention_decode.cuh"
 #include "kv_attention_params.cuh"
+#include "kv_attention_prompt.cuh"
 
 namespace fp8l {
 namespace {
-
-constexpr int kAttThreads = 128;
-
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-template <int QDT, int DIM>
-__global__ void __launch_bounds__(kAttThreads) kv_attention_kernel(const AttnParams p) {
-    __shared__ float qs[128], ws[kAttThreads], red[8];
-    grid_dependency_sync();
-    const int t = static_cast<int>(blockIdx.x) / p.q_heads, h = static_cast<int>(blockIdx.x) % p.q_heads;
-    if (t < p.q_offsets[0] || t >= p.q_offsets[p.requests]) return;
-    int lo = 0, hi = p.requests;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.q_offsets[mid] <= t)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const int r = lo, tid = static_cast<int>(threadIdx.x);
-    const int last = p.kv_lens[r] - (p.q_offsets[r + 1] - t);
-    const int first = p.window > 0 ? max(0, last - p.window + 1) : 0;
-    const int g = h / (p.q_heads / p.kv_heads);
-    const int P = 1 << p.page_shift;
-    if (tid < DIM) {
-        const uint16_t raw = p.q[static_cast<int64_t>(t) * p.q_stride + h * DIM + tid];
-        qs[tid] = (QDT == FP8L_BF16 ? __uint_as_float(static_cast<uint32_t>(raw) << 16)
-                                          : __half2float(__ushort_as_half(raw))) * p.score_scale;
-    }
-    float m = -INFINITY, l = 0.0f, acc = 0.0f;
-    __syncthreads();
-    for (int j0 = first & ~(kAttThreads - 1); j0 <= last; j0 += kAttThreads) {
-        const int j = j0 + tid;
-        float s = -INFINITY;
-        int64_t ph = 0;
-        if (j >= first && j <= last) {
-            const int page = min(max(p.block_table[static_cast<int64_t>(r) * p.table_width + (j >> p.page_shift)], 0),
-                                 p.num_pages - 1);
-            ph = static_cast<int64_t>(page) * p.kv_heads + g;
-            float dot = 0.0f;
-            for (int c = 0; c < DIM / 16; ++c) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(
-                    p.k_cache + kv_chunk_offset(ph, P, DIM, j & (P - 1), c));
-                const uint8_t *b = reinterpret_cast<const uint8_t *>(&u);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) dot = fmaf(qs[16 * c + i], e4m3_value(b[i]), dot);
-            }
-            s = dot * p.k_scale[ph];
-        }
-        float mt = s;
-        for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, o));
-        if ((tid & 31) == 0) red[tid >> 5] = mt;
-        __syncthreads();
-        mt = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float mn = fmaxf(m, mt);
-        const float keep = m == -INFINITY ? 0.0f : exp2f(m - mn);
-        const float w = s == -INFINITY ? 0.0f : exp2f(s - mn);
-        ws[tid] = w;
-        float sum = w;
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if ((tid & 31) == 0) red[4 + (tid >> 5)] = sum;
-        __syncthreads();
-        l = l * keep + ((red[4] + red[5]) + (red[6] + red[7]));
-        acc *= keep;
-        m = mn;
-        if (tid < DIM) {
-            for (int i = max(first - j0, 0); i < min(kAttThreads, last + 1 - j0); ++i) {
-                const int k = j0 + i;
-                const int page = min(max(p.block_table[static_cast<int64_t>(r) * p.table_width + (k >> p.page_shift)], 0),
-                                     p.num_pages - 1);
-                const int64_t vh = static_cast<int64_t>(page) * p.kv_heads + g;
-                const uint8_t c = p.v_cache[kv_chunk_offset(vh, P, DIM, k & (P - 1), tid >> 4) + (tid & 15)];
-                acc = fmaf(ws[i] * p.v_scale[vh], e4m3_value(c), acc);
-            }
-        }
-        __syncthreads();
-    }
-    const float o = l > 0.0f ? acc / l : 0.0f;
-    const float x[1] = {o};
-    if (tid < DIM) attn_store<1>(p, t, h, DIM, tid, x);
-    if (tid == 0 && p.lse != nullptr) attn_store_lse(p, t, h, m, l);
-}
 
 // Workspace: status word, merge counters (zero between calls), partials
 constexpr size_t kAttnCountersOffset = 64;
 constexpr size_t kAttnZeroBytes = 2048;
 constexpr int kDecMaxRows = 16;
+constexpr size_t kDecPartials = static_cast<size_t>(2) * kDecMaxCtas * kDecMaxRows * (128 + 2);
+constexpr size_t kProPartials = static_cast<size_t>(2) * kProMaxCtas * kProRows * (128 + 2);
 constexpr size_t kAttnWorkspaceBytes =
-    kAttnZeroBytes + sizeof(float) * 2 * kDecMaxCtas * kDecMaxRows * (128 + 2);
-static_assert(kAttnCountersOffset + 4 * kDecMaxCtas <= kAttnZeroBytes, "counters fit");
+    kAttnZeroBytes + sizeof(float) * (kDecPartials > kProPartials ? kDecPartials : kProPartials);
+static_assert(kAttnCountersOffset + 4 * kDecMaxCtas <= kAttnZeroBytes &&
+                  kAttnCountersOffset + 4 * 2 * kProMaxCtas <= kAttnZeroBytes,
+              "counters fit");
 
 constexpr int kDecSmemPerCta = 113 * 1024 - 512;  // two CTAs per SM
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename Kernel>
+int allow_smem(Kernel kernel, int smem, std::atomic<unsigned long long> &ready) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FP8L_ECUDA;
+    if (ready.load(std::memory_order_acquire) >> dev & 1u) return FP8L_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+        return FP8L_ECUDA;
+    ready.fetch_or(1ull << dev, std::memory_order_release);
+    return FP8L_OK;
+}
 
 template <int QDT, int DIM, int ROWS>
 int launch_decode(AttnParams p, int sms, cudaStream_t stream) {
     using Sm = DecSmem<QDT, DIM, ROWS>;
-    int stages = (kDecSmemPerCta - Sm::kFixedBytes) / Sm::kStageBytes;
-    stages = stages < kDecMaxStages ? stages : kDecMaxStages;
-    p.stages = stages;
-    const int smem = stages * Sm::kStageBytes + Sm::kFixedBytes;
+    const int fit = (kDecSmemPerCta - Sm::kFixedBytes) / Sm::kStageBytes;
+    p.stages = fit < kDecMaxStages ? fit : kDecMaxStages;
+    const int smem = p.stages * Sm::kStageBytes + Sm::kFixedBytes;
+    static std::atomic<unsigned long long> ready{0};
     auto kernel = kv_attention_decode_kernel<QDT, DIM, ROWS>;
-    static std::atomic<unsigned> ready{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FP8L_ECUDA;
-    if (!(ready.load(std::memory_order_acquire) >> dev & 1u)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
-            return FP8L_ECUDA;
-        ready.fetch_or(1u << dev, std::memory_order_release);
-    }
+    if (int st = allow_smem(kernel, smem, ready); st != FP8L_OK) return st;
     const int ctas = 2 * sms < kDecMaxCtas ? 2 * sms : kDecMaxCtas;
     return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), kDecThreads, smem, stream, p);
+}
+
+template <int QDT, int DIM>
+int launch_prompt(const AttnParams &p, int sms, cudaStream_t stream) {
+    constexpr int smem = ProSmem<QDT, DIM>::kBytes;
+    static std::atomic<unsigned long long> ready{0};
+    auto kernel = kv_attention_prompt_kernel<QDT, DIM>;
+    if (int st = allow_smem(kernel, smem, ready); st != FP8L_OK) return st;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(sms < kProMaxCtas ? sms : kProMaxCtas)), kProThreads,
+                            smem, stream, p);
 }
 
 template <int QDT, int DIM>
 int launch_attention(const AttnParams &p, int64_t rows, int sms, cudaStream_t stream) {
     if (rows <= 8) return launch_decode<QDT, DIM, 8>(p, sms, stream);
     if (rows <= 16) return launch_decode<QDT, DIM, 16>(p, sms, stream);
-    return launch_dependent(kv_attention_kernel<QDT, DIM>, dim3(static_cast<unsigned>(p.tokens) * p.q_heads),
-                            kAttThreads, 0, stream, p);
+    return launch_prompt<QDT, DIM>(p, sms, stream);
 }
 
 }  // namespace
