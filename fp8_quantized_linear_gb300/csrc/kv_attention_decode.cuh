@@ -174,6 +174,12 @@ __device__ __forceinline__ uint32_t take_part(float &a, float &b) {
     return c;
 }
 
+// Exponent e with 2^7 <= m 2^e < 2^8, at most 120 (rows below 2^-113 lose
+// their last bits) so that 2^-e stays a normal float32; m >= 0
+__device__ __forceinline__ int part_exponent(float m) {
+    return min(134 - static_cast<int>(__float_as_uint(m) >> 23), 120);
+}
+
 // A piece of one request and kv head: key tiles [tile, end) of its [begin, stop)
 struct DecSegment {
     int r, g;
@@ -567,8 +573,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv_attention_decode_kernel(con
                 // of a warp's rows, or the row is a repeat of none)
 #pragma unroll
                 for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o, LANES));
-                // exponent e with 2^7 <= m 2^e < 2^8, kept inside float32
-                const int e = m > 0.0f ? min(7 - (ilogbf(m)), 120) : 0;
+                const int e = part_exponent(m);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] *= up;

@@ -47,25 +47,43 @@ __device__ __forceinline__ void attn_store(const AttnParams &p, int token, int h
     if (p.out_dtype == FP8L_E4M3) {
         const float s = p.out_scale[0];
         uint8_t *y = static_cast<uint8_t *>(p.out) + at;
-        if constexpr (VALS == 1) {
-            *y = code_of(o[0], s);
-        } else {
+        if constexpr (VALS < 4) {
 #pragma unroll
-            for (int i = 0; i < VALS; i += 2)
-                *reinterpret_cast<uint16_t *>(y + i) =
-                    static_cast<uint16_t>(out_e4m3x2(__fdiv_rn(o[i], s), __fdiv_rn(o[i + 1], s)));
+            for (int i = 0; i < VALS; ++i) y[i] = code_of(o[i], s);
+        } else {
+            const Quot d = Quot::make<FP8L_F32>(s);
+            uint32_t c[VALS / 4];
+#pragma unroll
+            for (int i = 0; i < VALS / 4; ++i)
+                c[i] = codes_of_word<FP8L_F32, true>(
+                           make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                                      __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3])), d).x;
+            if constexpr (VALS % 16 == 0) {
+#pragma unroll
+                for (int i = 0; i < VALS / 4; i += 4)
+                    *reinterpret_cast<uint4 *>(y + 4 * i) = make_uint4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VALS / 4; ++i) *reinterpret_cast<uint32_t *>(y + 4 * i) = c[i];
+            }
         }
     } else {
         uint16_t *y = static_cast<uint16_t *>(p.out) + at;
         if constexpr (VALS == 1) {
             *y = static_cast<uint16_t>(pack_out16(o[0], o[0], p.out_dtype) & 0xFFFFu);
-        } else if constexpr (VALS == 2) {
-            *reinterpret_cast<uint32_t *>(y) = pack_out16(o[0], o[1], p.out_dtype);
         } else {
+            uint32_t w[VALS / 2];
 #pragma unroll
-            for (int i = 0; i < VALS; i += 4)
-                *reinterpret_cast<uint2 *>(y + i) =
-                    make_uint2(pack_out16(o[i], o[i + 1], p.out_dtype), pack_out16(o[i + 2], o[i + 3], p.out_dtype));
+            for (int i = 0; i < VALS / 2; ++i) w[i] = pack_out16(o[2 * i], o[2 * i + 1], p.out_dtype);
+            if constexpr (VALS == 2) {
+                *reinterpret_cast<uint32_t *>(y) = w[0];
+            } else if constexpr (VALS == 4) {
+                *reinterpret_cast<uint2 *>(y) = make_uint2(w[0], w[1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VALS / 2; i += 4)
+                    *reinterpret_cast<uint4 *>(y + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            }
         }
     }
 }

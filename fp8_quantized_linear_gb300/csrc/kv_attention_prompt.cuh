@@ -29,10 +29,12 @@
 // into equal pieces for one CTA per SM; row tiles that span pieces are merged
 // by the last CTA to arrive, in CTA order, as in the decode kernel.
 //
-// Roles (448 threads): warps 0-3 and 4-7 softmax of halves 0 and 1 (warp w
+// Roles (512 threads): warps 0-3 and 4-7 softmax of halves 0 and 1 (warp w
 // owns tensor-memory lanes 32 (w mod 4) ..), warps 8-11 queries to parts and V
 // to fp16, warp 12 copies, warp 13 issues the MMAs.
 #pragma once
+
+#include <type_traits>
 
 #include "kv_attention_decode.cuh"
 
@@ -41,12 +43,16 @@ namespace {
 
 constexpr int kProRows = 256;     // query rows per tile, two halves
 constexpr int kProKeys = 128;
-constexpr int kProThreads = 448;
+constexpr int kProThreads = 512;
 constexpr int kProWarps = kProThreads / 32;
 constexpr int kProMaxKStages = 4;
 constexpr int kProMaxVStages = 2;
 constexpr int kProScaleSlots = 8;  // tiles whose page scales are held
+constexpr int kProSegments = 8;    // pieces between the copy warp and the slowest role (stages + 2 at most)
 constexpr int kProMaxCtas = 160;
+// registers per thread of the softmax, converter and other warpgroups after
+// the split: 2 x 184 + 88 + 56 = 4 x 128, what the block starts with
+constexpr int kProSoftmaxRegs = 184, kProConvertRegs = 88, kProOtherRegs = 56;
 constexpr float kProHead = 7.0f;   // reference below the maximum it was set from
 constexpr float kProMove = 15.0f;  // a score this far above moves it
 
@@ -63,21 +69,75 @@ struct ProSmem {
     static constexpr int kVOff = kKOff + kKStages * kTileBytes;
     static constexpr int kV16Off = kVOff + kVStages * kTileBytes;
     static constexpr int kScaleOff = kV16Off + 2 * kV16Bytes;               // [slot][2][8] floats
-    static constexpr int kQfOff = kScaleOff + kProScaleSlots * 16 * 4;      // [2][256] floats
-    static constexpr int kBarOff = kQfOff + 2 * kProRows * 4;
-    static constexpr int kBars = 2 * kProMaxKStages + 2 * kProMaxVStages + kProScaleSlots + 4 + 6 + 4;
+    static constexpr int kFactorOff = kScaleOff + kProScaleSlots * 16 * 4;  // [slot][8] float4
+    static constexpr int kQfOff = kFactorOff + kProScaleSlots * 8 * 16;     // [256] floats
+    static constexpr int kSegOff = kQfOff + kProRows * 4;                   // [kProSegments] ProSegment
+    static constexpr int kBarOff = kSegOff + kProSegments * 64;
+    static constexpr int kBars = 2 * kProMaxKStages + 2 * kProMaxVStages + 2 * kProScaleSlots + kProSegments + 4 + 8 + 3;
     static constexpr int kMiscOff = kBarOff + kBars * 8;
     static constexpr int kBytes = kMiscOff + 16;
-    static_assert(kBytes <= 227 * 1024 - 256, "one CTA's shared memory, beside the static variables");
+    static_assert(kBytes <= 227 * 1024 - 320, "one CTA's shared memory, beside the static variables");
 };
 
-__device__ __forceinline__ void pro_mma_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
+// mbar_wait without a call: the register split does not allow one.
+__device__ __forceinline__ bool pro_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status,
+                                         long long limit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > limit) {
+            *abort_flag = 1;
+            atomicOr(status, kStatusTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+// A wait that ignores the abort flag, while tearing down
+__device__ __forceinline__ void pro_drain(uint32_t bar, uint32_t parity, unsigned *status) {
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (clock64() - t0 > kDefaultWaitCycles) {
+            atomicOr(status, kStatusTimeout);
+            return;
+        }
+    }
+}
+
+// Operand descriptors as two words: the address moves only in the low one,
+// so a step along an operand is one addition (a single thread issues every
+// MMA, and its instructions are the critical path).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+    return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14); }
+
+// D (tensor memory) = or += A B^T, both operands in shared memory, fp8
+template <bool ACC>
+__device__ __forceinline__ void pro_mma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                           uint32_t b_hi, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+
+// The same with A in tensor memory, fp16
+__device__ __forceinline__ void pro_mma_f16(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -107,15 +167,44 @@ __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t 
         : "memory");
 }
 
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// E4M3 codes of two values (a in the low byte) and what they leave over
-__device__ __forceinline__ uint32_t take_part_unscaled(float &a, float &b) {
-    const uint32_t c = take_part(a, b);
-    a *= 0.0625f;
-    b *= 0.0625f;
+// E4M3 codes of two fp16 pairs (in order), which become what the codes leave
+// over (exact: the difference of a value and its rounding to fewer bits)
+__device__ __forceinline__ uint32_t take_part_f16(uint32_t &a, uint32_t &b) {
+    uint32_t c, x, y;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 lo, %3;\n\tcvt.rn.satfinite.e4m3x2.f16x2 hi, %4;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, lo;\n\tcvt.rn.f16x2.e4m3x2 %2, hi;\n\t}"
+        : "=r"(c), "=r"(x), "=r"(y)
+        : "r"(a), "r"(b));
+    const __half2 da = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&x));
+    const __half2 db = __hsub2(*reinterpret_cast<const __half2 *>(&b), *reinterpret_cast<const __half2 *>(&y));
+    a = *reinterpret_cast<const uint32_t *>(&da);
+    b = *reinterpret_cast<const uint32_t *>(&db);
     return c;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ float max16(const uint32_t *v) {
+    float m[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        m[i] = max3(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
+    return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], __uint_as_float(v[15])), __uint_as_float(v[15]));
 }
 
 // A request's rows and keys
@@ -131,8 +220,8 @@ __device__ __forceinline__ ProRequest pro_request(const AttnParams &p, int r) {
     d.keys = static_cast<int64_t>(L) < cap ? L : static_cast<int>(cap);
     d.n = max(b - a, 0);
     d.row0 = a;
-    const int64_t rows = static_cast<int64_t>(d.n) * (p.q_heads / p.kv_heads);
-    d.tiles = static_cast<int>((rows + kProRows - 1) / kProRows);
+    // (rows fit 32 bits: tokens * q_heads does)
+    d.tiles = (d.n * (p.q_heads / p.kv_heads) + kProRows - 1) / kProRows;
     return d;
 }
 
@@ -144,50 +233,61 @@ struct ProKeys {
 
 __device__ __forceinline__ ProKeys pro_keys(const AttnParams &p, const ProRequest &d, int j) {
     const int group = p.q_heads / p.kv_heads;
-    const int64_t lo = static_cast<int64_t>(j) * kProRows;
-    const int64_t all = static_cast<int64_t>(d.n) * group;
-    const int64_t hi = lo + kProRows < all ? lo + kProRows : all;
+    const int lo = j * kProRows;
+    const int hi = min(lo + kProRows, d.n * group);
     const int before = d.keys - d.n;
     ProKeys k;
-    k.last = before + static_cast<int>((hi - 1) / group);
-    k.first = p.window > 0 ? max(0, before + static_cast<int>(lo / group) - p.window + 1) : 0;
+    k.last = before + (hi - 1) / group;
+    k.first = p.window > 0 ? max(0, before + lo / group - p.window + 1) : 0;
     k.begin = k.first / kProKeys;
     k.tiles = k.last < 0 ? 1 : k.last / kProKeys - k.begin + 1;
     return k;
 }
 
+// A piece of one row tile, as the copy warp hands it to the other roles
+// through shared memory (they keep none of it in registers over the tiles)
 struct ProSegment {
-    int r, g, j;
-    ProRequest req;
-    ProKeys keys;
-    int tile, end;  // key tiles of this piece
-    long long at;   // number of `tile` in the line
+    int tile, end;         // key tiles of this piece
+    int begin, stop;       // of the whole row tile
+    int first, last;       // keys seen
+    int g, row0;           // kv head, the request's first token row
+    int row_first, rows;   // first (token, head) row of the tile, how many
+    int before;            // position of the request's first new token
+    int done;              // tiles of the CTA's piece before this one; tile == end: no more
+    int r, pad[3];
 };
 
 struct ProWalk {
-    long long at, left;
+    int done, left;  // tiles of the CTA's piece behind and ahead
     int r, g, j, offset;
     __device__ __forceinline__ bool next(const AttnParams &p, ProSegment &s) {
         if (left <= 0) return false;
-        s.req = pro_request(p, r);
-        while (s.req.tiles == 0) {
+        ProRequest d = pro_request(p, r);
+        while (d.tiles == 0) {
             if (++r >= p.requests) return false;
-            s.req = pro_request(p, r);
+            d = pro_request(p, r);
         }
+        const ProKeys k = pro_keys(p, d, j);
         s.r = r;
         s.g = g;
-        s.j = j;
-        s.keys = pro_keys(p, s.req, j);
-        s.tile = s.keys.begin + offset;
-        const long long take = min(static_cast<long long>(s.keys.tiles - offset), left);
-        s.end = s.tile + static_cast<int>(take);
-        s.at = at;
-        at += take;
+        s.row0 = d.row0;
+        s.row_first = j * kProRows;
+        s.rows = min(d.n * (p.q_heads / p.kv_heads) - s.row_first, kProRows);
+        s.before = d.keys - d.n;
+        s.first = k.first;
+        s.last = k.last;
+        s.begin = k.begin;
+        s.stop = k.begin + k.tiles;
+        s.tile = k.begin + offset;
+        const int take = min(k.tiles - offset, left);
+        s.end = s.tile + take;
+        s.done = done;
+        done += take;
         left -= take;
-        offset += static_cast<int>(take);
-        if (offset == s.keys.tiles) {
+        offset += take;
+        if (offset == k.tiles) {
             offset = 0;
-            if (++j == s.req.tiles) {
+            if (++j == d.tiles) {
                 j = 0;
                 if (++g == p.kv_heads) {
                     g = 0;
@@ -209,19 +309,44 @@ __device__ __forceinline__ long long pro_request_work(const AttnParams &p, int r
     return n;
 }
 
+// One lane of the (converged) warp, always the same
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0u;
+}
+
 __device__ __forceinline__ void half_sync(int half) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
 }
 
+__device__ __forceinline__ bool half_any(int half, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(x ? 1u : 0u), "r"(1 + half)
+        : "memory");
+    return r != 0u;
+}
+
 // Adds the CTAs' partials of one half of a row tile, in CTA order: a warp
-// takes 16 rows at a time, DIM / 32 dimensions per lane.
+// takes 8 rows at a time, DIM / 32 dimensions per lane.
 template <int DIM, typename Partial>
 __device__ __forceinline__ void pro_merge(const AttnParams &p, const ProSegment &s, int half, int rows, int group,
                                           int parts, const Partial &partial) {
-    constexpr int V = DIM / 32, B = 16;
+    constexpr int V = DIM / 32, B = 8;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int b = warp * 32; b < warp * 32 + 32 && b < rows; b += B) {
-        // lanes 0-15 hold the rows' maxima and sums
+        // lanes 0-7 hold the rows' maxima and sums
         const int mine = 128 * half + b + (lane & (B - 1));
         float top = -INFINITY;
         for (int c = 0; c < parts; ++c) top = fmaxf(top, __ldcg(partial(c) + kProRows * DIM + 2 * mine));
@@ -248,18 +373,19 @@ __device__ __forceinline__ void pro_merge(const AttnParams &p, const ProSegment 
                 }
             }
         }
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int i = 0; i < B; ++i) {
-            const float l = __shfl_sync(0xFFFFFFFFu, sum, i);
+            const float scale = __shfl_sync(0xFFFFFFFFu, inv, i);
             if (b + i >= rows) continue;
-            const int row = s.j * kProRows + 128 * half + b + i;
+            const int row = s.row_first + 128 * half + b + i;
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[i][k] = l > 0.0f ? acc[i][k] / l : 0.0f;
-            attn_store<V>(p, s.req.row0 + row / group, s.g * group + row % group, DIM, V * lane, acc[i]);
+            for (int k = 0; k < V; ++k) acc[i][k] *= scale;
+            attn_store<V>(p, s.row0 + row / group, s.g * group + row % group, DIM, V * lane, acc[i]);
         }
         if (lane < B && b + lane < rows && p.lse != nullptr) {
-            const int row = s.j * kProRows + 128 * half + b + lane;
-            attn_store_lse(p, s.req.row0 + row / group, s.g * group + row % group, top, sum);
+            const int row = s.row_first + 128 * half + b + lane;
+            attn_store_lse(p, s.row0 + row / group, s.g * group + row % group, top, sum);
         }
     }
 }
@@ -281,9 +407,10 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
     const uint32_t kfull = take_bars(kProMaxKStages), kempty = take_bars(kProMaxKStages);
     const uint32_t vfull = take_bars(kProMaxVStages), vempty = take_bars(kProMaxVStages);
     const uint32_t scfull = take_bars(kProScaleSlots);
+    const uint32_t fcfull = take_bars(kProScaleSlots), segfull = take_bars(kProSegments);
     const uint32_t v16full = take_bars(2), v16free = take_bars(2);
-    const uint32_t sfull = take_bars(2), wfull = take_bars(2), odone = take_bars(2);
-    const uint32_t qfull = take_bars(2), qfree = take_bars(1), done_bar = take_bars(1);
+    const uint32_t sfull = take_bars(2), wfull = take_bars(4), odone = take_bars(2);
+    const uint32_t qfull = take_bars(2), done_bar = take_bars(1);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pro_smem + Sm::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -293,18 +420,22 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             mbar_init(kfull + 8 * s, 1);
             mbar_init(kempty + 8 * s, 1);
         }
-        for (int s = 0; s < kProScaleSlots; ++s) mbar_init(scfull + 8 * s, 32);
+        for (int s = 0; s < kProSegments; ++s) mbar_init(segfull + 8 * s, 1);
+        for (int s = 0; s < kProScaleSlots; ++s) {
+            mbar_init(scfull + 8 * s, 32);
+            mbar_init(fcfull + 8 * s, 8);
+        }
         for (int s = 0; s < 2; ++s) {
             mbar_init(vfull + 8 * s, 1);
             mbar_init(vempty + 8 * s, 128);
             mbar_init(v16full + 8 * s, 128);
             mbar_init(v16free + 8 * s, 1);
             mbar_init(sfull + 8 * s, 1);
-            mbar_init(wfull + 8 * s, 128);
+            mbar_init(wfull + 16 * s, 128);
+            mbar_init(wfull + 16 * s + 8, 128);
             mbar_init(odone + 8 * s, 1);
             mbar_init(qfull + 8 * s, 128);
         }
-        mbar_init(qfree, 1);
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -374,27 +505,45 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    ProWalk walk{w0, w1 - w0, idle ? 0 : start_r, idle ? 0 : start_g, idle ? 0 : start_j, idle ? 0 : start_offset};
     const int group = p.q_heads / p.kv_heads;
-    auto rows_of = [&](const ProSegment &s) {
-        const int64_t left = static_cast<int64_t>(s.req.n) * group - static_cast<int64_t>(s.j) * kProRows;
-        return static_cast<int>(left < kProRows ? left : kProRows);
+    ProSegment *segs = reinterpret_cast<ProSegment *>(pro_smem + Sm::kSegOff);
+    // piece number n, or nullptr after the last (or a time-out)
+    auto segment_at = [&](int n) -> const ProSegment * {
+        if (!pro_wait(segfull + 8 * (n & (kProSegments - 1)), (n / kProSegments) & 1u, abort_flag, p.status,
+                      p.wait_cycles))
+            return nullptr;
+        const ProSegment *s = segs + (n & (kProSegments - 1));
+        return s->tile < s->end ? s : nullptr;
     };
-    ProSegment s;
 
-    if (warp == 12) {
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProOtherRegs));
+
+      if (warp == 12) {
         // ---------------------------------------------------------- copies
         const int P = 1 << p.page_shift, per_tile = kProKeys >> p.page_shift;
         const int i = lane & 7;
-        int kst = 0, vst = 0, count = 0;
+        int kst = 0, vst = 0, count = 0, segment = 0;
         uint32_t kph = 0, vph = 0, kissued = 0, kpar = 0, vissued = 0, vpar = 0;
         bool ok = true;
-        while (ok && walk.next(p, s)) {
+        ProWalk walk{0, static_cast<int>(w1 - w0), idle ? 0 : start_r, idle ? 0 : start_g, idle ? 0 : start_j,
+                     idle ? 0 : start_offset};
+        ProSegment s;
+        while (ok) {
+            const bool more = walk.next(p, s);
+            if (!more) s.tile = s.end = 0;
+            if (lane == 0) {
+                segs[segment & (kProSegments - 1)] = s;
+                mbar_arrive(segfull + 8 * (segment & (kProSegments - 1)));
+            }
+            __syncwarp();
+            ++segment;
+            if (!more) break;
             const int32_t *table = p.block_table + static_cast<int64_t>(s.r) * p.table_width;
             auto wanted = [&](int tile) {
                 const int64_t b = static_cast<int64_t>(tile) * per_tile + i;
-                return lane < 16 && i < per_tile && (b << p.page_shift) <= s.keys.last &&
-                       ((b + 1) << p.page_shift) > s.keys.first;
+                return lane < 16 && i < per_tile && (b << p.page_shift) <= s.last &&
+                       ((b + 1) << p.page_shift) > s.first;
             };
             int page = wanted(s.tile) ? table[s.tile * per_tile + i] : 0;
             for (int tile = s.tile; tile < s.end; ++tile, ++count) {
@@ -403,7 +552,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 if (tile + 1 < s.end) page = wanted(tile + 1) ? table[(tile + 1) * per_tile + i] : 0;
                 uint32_t bytes = 0;
                 if (mine) {
-                    const int in_page = min(s.keys.last + 1 - ((tile * per_tile + i) << p.page_shift), P);
+                    const int in_page = min(s.last + 1 - ((tile * per_tile + i) << p.page_shift), P);
                     bytes = static_cast<uint32_t>((in_page + 7) / 8 * 8 * DIM);
                 }
                 uint32_t sum = lane < 8 ? bytes : 0u;
@@ -411,7 +560,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
                 // keys, and the scales of keys and values
                 ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(kempty + 8 * kst, kph ^ 1u, abort_flag, p.status, p.wait_cycles));
+                                pro_wait(kempty + 8 * kst, kph ^ 1u, abort_flag, p.status, p.wait_cycles));
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(kfull + 8 * kst, sum);
                 __syncwarp();
@@ -436,7 +585,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 }
                 // values
                 ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(vempty + 8 * vst, vph ^ 1u, abort_flag, p.status, p.wait_cycles));
+                                pro_wait(vempty + 8 * vst, vph ^ 1u, abort_flag, p.status, p.wait_cycles));
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(vfull + 8 * vst, sum);
                 __syncwarp();
@@ -453,152 +602,142 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         for (int x = 0; x < Sm::kKStages; ++x)
-            if (kissued & (1u << x)) mbar_wait_drain(kfull + 8 * x, (kpar >> x) & 1u, p.status);
+            if (kissued & (1u << x)) pro_drain(kfull + 8 * x, (kpar >> x) & 1u, p.status);
         for (int x = 0; x < Sm::kVStages; ++x)
-            if (vissued & (1u << x)) mbar_wait_drain(vfull + 8 * x, (vpar >> x) & 1u, p.status);
-    } else if (warp == 13) {
+            if (vissued & (1u << x)) pro_drain(vfull + 8 * x, (vpar >> x) & 1u, p.status);
+      } else if (warp == 13) {
         // ---------------------------------------------------------- MMAs
-        if (lane == 0) {
+        {
+            const bool leader = elect_one();
+            const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             const uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(kProKeys >> 3) << 17) | (8u << 24);
             const uint32_t idesc_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(DIM >> 3) << 17) | (8u << 24);
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                return mbar_wait_fast(bar, parity & 1u, abort_flag, p.status, p.wait_cycles);
+                return __all_sync(0xFFFFFFFFu, pro_wait(bar, parity & 1u, abort_flag, p.status, p.wait_cycles));
             };
             bool ok = true;
             if (p.stall & kStallMma) ok = wait(done_bar, 0);
             int kst = 0, count = 0, segment = 0;
             uint32_t kph = 0;
-            int uses[2] = {0, 0};  // score tiles of each half so far
-            auto scores = [&](int half) {
-                const uint32_t k = sbase + Sm::kKOff + kst * Sm::kTileBytes;
+            int uses[2] = {0, 0}, segments1 = 0;  // score tiles of each half, pieces of half 1 so far
+            const uint32_t q_lo = desc_lo(sbase, 128), k_lo0 = desc_lo(sbase + Sm::kKOff, 128);
+            const uint32_t v_lo0 = desc_lo(sbase + Sm::kV16Off, 16 * DIM);
+            uint32_t k_lo = k_lo0;
+            auto scores = [&](auto half_c) {
+                constexpr int half = decltype(half_c)::value;
+                if (!leader) return;
 #pragma unroll
                 for (int part = 0; part < Sm::kParts; ++part) {
-                    const uint32_t q = sbase + (half * Sm::kParts + part) * Sm::kQPart;
 #pragma unroll
-                    for (int x = 0; x < DIM / 32; ++x)
-                        dec_mma(tmem + 128u * half, core_desc(q + 256u * x, 128, 8 * DIM),
-                                core_desc(k + 256u * x, 128, 8 * DIM), idesc_s, (part | x) != 0 ? 1u : 0u);
+                    for (int x = 0; x < DIM / 32; ++x) {
+                        const uint32_t a = q_lo + ((half * Sm::kParts + part) * Sm::kQPart + 256 * x) / 16;
+                        const uint32_t b = k_lo + 256 * x / 16;
+                        if (part == 0 && x == 0)
+                            pro_mma_f8<false>(tmem_u + 128u * half, a, desc_hi(8 * DIM), b, desc_hi(8 * DIM), idesc_s);
+                        else
+                            pro_mma_f8<true>(tmem_u + 128u * half, a, desc_hi(8 * DIM), b, desc_hi(8 * DIM), idesc_s);
+                    }
                 }
                 mma_commit(sfull + 8 * half);
             };
             // O += W V of tile number `tile` (its V buffer), use u of the half
-            auto values = [&](int half, int tile, int u, bool first) {
-                if (!wait(wfull + 8 * half, u) || !wait(v16full + 8 * (tile & 1), tile >> 1)) return false;
-                tc_fence_after();
-                const uint32_t v = sbase + Sm::kV16Off + (tile & 1) * Sm::kV16Bytes;
+            auto values = [&](auto half_c, int tile, int u, bool first) {
+                constexpr int half = decltype(half_c)::value;
+                if (!wait(v16full + 8 * (tile & 1), tile >> 1)) return false;
+                const uint32_t v = v_lo0 + ((tile & 1) ? Sm::kV16Bytes / 16 : 0);
 #pragma unroll
-                for (int x = 0; x < kProKeys / 16; ++x)
-                    pro_mma_f16(tmem + 256u + 128u * half, tmem + 128u * half + 8u * x,
-                                core_desc(v + 32u * DIM * x, 16 * DIM, 128), idesc_o, (first && x == 0) ? 0u : 1u);
-                mma_commit(odone + 8 * half);
+                for (int y = 0; y < 2; ++y) {
+                    if (!wait(wfull + 16 * half + 8 * y, u)) return false;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int x = y * kProKeys / 32; x < (y + 1) * kProKeys / 32; ++x)
+                            pro_mma_f16(tmem_u + 256u + 128u * half, tmem_u + 128u * half + 8u * x, v + 32 * DIM * x / 16,
+                                desc_hi(128), idesc_o, x == 0 ? (first ? 0u : 1u) : 1u);
+                    }
+                }
+                if (leader) mma_commit(odone + 8 * half);
                 return true;
             };
-            while (ok && walk.next(p, s)) {
-                const bool two = rows_of(s) > 128;
+            using Half0 = std::integral_constant<int, 0>;
+            using Half1 = std::integral_constant<int, 1>;
+            while (ok) {
+                const ProSegment *s = segment_at(segment);
+                if (__any_sync(0xFFFFFFFFu, s == nullptr)) break;
+                const bool two = s->rows > 128;
+                const int tiles = s->end - s->tile;
                 bool pending = false;  // half 1 of the tile before
-                ok = wait(qfull + 8 * (segment & 1), segment >> 1);
-                for (int tile = s.tile; ok && tile < s.end; ++tile, ++count) {
+                ok = wait(qfull, segment);
+                for (int tile = 0; ok && tile < tiles; ++tile, ++count) {
                     ok = wait(kfull + 8 * kst, kph);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(0);
+                    scores(Half0{});
                     if (pending) {
-                        ok = values(1, count - 1, uses[1] - 1, tile - 1 == s.tile);
+                        ok = values(Half1{}, count - 1, uses[1] - 1, tile == 1);
                         if (!ok) break;
-                        mma_commit(v16free + 8 * ((count - 1) & 1));
+                        if (leader) mma_commit(v16free + 8 * ((count - 1) & 1));
                     }
                     if (two) {
-                        scores(1);
+                        if (tile == 0) {
+                            ok = wait(qfull + 8, segments1++);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        scores(Half1{});
                         ++uses[1];
                     }
-                    mma_commit(kempty + 8 * kst);
-                    if (tile + 1 == s.end) mma_commit(qfree);
-                    ok = values(0, count, uses[0], tile == s.tile);
+                    if (leader) mma_commit(kempty + 8 * kst);
+                    ok = values(Half0{}, count, uses[0], tile == 0);
                     if (!ok) break;
                     ++uses[0];
-                    if (!two) mma_commit(v16free + 8 * (count & 1));
+                    if (leader && !two) mma_commit(v16free + 8 * (count & 1));
                     pending = two;
+                    k_lo += Sm::kTileBytes / 16;
                     if (++kst == Sm::kKStages) {
                         kst = 0;
                         kph ^= 1u;
+                        k_lo = k_lo0;
                     }
                 }
                 if (ok && pending) {
-                    ok = values(1, count - 1, uses[1] - 1, s.end - 1 == s.tile);
-                    if (ok) mma_commit(v16free + 8 * ((count - 1) & 1));
+                    ok = values(Half1{}, count - 1, uses[1] - 1, tiles == 1);
+                    if (ok && leader) mma_commit(v16free + 8 * ((count - 1) & 1));
                 }
                 ++segment;
             }
-            mma_commit(done_bar);
+            if (leader) mma_commit(done_bar);
         }
         __syncwarp();
+      }
     } else if (warp >= 8) {
-        // ------------------------------------- queries to parts, V to fp16
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProConvertRegs));
+
+        // ------------------------------------- V to fp16, the scales' factors
         const int tid = static_cast<int>(threadIdx.x) - 256;
-        float *qf = reinterpret_cast<float *>(pro_smem + Sm::kQfOff);
         int vst = 0, count = 0, segment = 0;
         uint32_t vph = 0;
         bool ok = true;
-        while (walk.next(p, s)) {
-            const int rows = rows_of(s);
-            ok = ok && (segment == 0 ||
-                        mbar_wait(qfree, (segment - 1) & 1u, abort_flag, p.status, p.wait_cycles));
-            constexpr int LANES = DIM / 8, AT_ONCE = 128 / LANES, BATCH = 8;
-            const int l = tid % LANES;
-            for (int b = 0; b < rows; b += AT_ONCE * BATCH) {
-                uint4 u[BATCH];
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int row = b + k * AT_ONCE + tid / LANES;
-                    u[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < rows) {
-                        const int64_t at = static_cast<int64_t>(s.j) * kProRows + row;
-                        const int token = s.req.row0 + static_cast<int>(at / group);
-                        const int head = s.g * group + static_cast<int>(at % group);
-                        u[k] = *reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(token) * p.q_stride +
-                                                                head * DIM + 8 * l);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int row = b + k * AT_ONCE + tid / LANES;  // rows past the last are zeros, below 256
-                    float x[8];
-                    const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t f = widen16<QDT>(w[i]);
-                        x[2 * i] = __uint_as_float(static_cast<uint32_t>(f));
-                        x[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(f >> 32));
-                    }
-                    float m = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-                    for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o, LANES));
-                    const int e = m > 0.0f ? min(7 - ilogbf(m), 120) : 0;
-                    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= up;
-                    if (l == 0)
-                        qf[(segment & 1) * kProRows + row] =
-                            p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-                    for (int part = 0; part < Sm::kParts; ++part) {
-                        uint32_t c[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) c[i] = take_part_unscaled(x[2 * i], x[2 * i + 1]);
-                        uint8_t *dst = pro_smem + ((row >> 7) * Sm::kParts + part) * Sm::kQPart +
-                                       ((row & 127) >> 3) * 8 * DIM + (l >> 1) * 128 + (row & 7) * 16 + 8 * (l & 1);
-                        *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-                    }
-                }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(qfull + 8 * (segment & 1));
+        while (const ProSegment *sp = segment_at(segment)) {
+            const int first = sp->first, last = sp->last, end = sp->end;
             ++segment;
-            for (int tile = s.tile; tile < s.end; ++tile, ++count) {
+            for (int tile = sp->tile; tile < end; ++tile, ++count) {
+                if (tid < 8) {
+                    // factors of the 16 keys from 16 tid on: their page's
+                    // scales; a page without a seen key was not copied
+                    const int slot = count & (kProScaleSlots - 1), pg = (16 * tid) >> p.page_shift;
+                    const int key = tile * kProKeys + 16 * tid;
+                    ok = ok && pro_wait(scfull + 8 * slot, (count / kProScaleSlots) & 1u, abort_flag, p.status,
+                                              p.wait_cycles);
+                    const float *sc = reinterpret_cast<const float *>(pro_smem + Sm::kScaleOff) + slot * 16;
+                    const bool there = key <= last && key + 15 >= first;
+                    const float ks = there ? sc[pg] : 0.0f, vs = there ? sc[8 + pg] : 1.0f;
+                    reinterpret_cast<float4 *>(pro_smem + Sm::kFactorOff)[slot * 8 + tid] =
+                        make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.0f);
+                    mbar_arrive(fcfull + 8 * slot);
+                }
                 constexpr int PIECES = kProKeys * DIM / 16 / 128;  // 16-byte pieces per thread
-                ok = ok && mbar_wait_fast(vfull + 8 * vst, vph, abort_flag, p.status, p.wait_cycles);
+                ok = ok && pro_wait(vfull + 8 * vst, vph, abort_flag, p.status, p.wait_cycles);
                 const uint8_t *src = pro_smem + Sm::kVOff + vst * Sm::kTileBytes;
                 uint4 u[PIECES];
 #pragma unroll
@@ -608,7 +747,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     u[k] = *reinterpret_cast<const uint4 *>(src + 16 * piece);
                     // keys that are not there: whatever the stage holds (NaN
                     // codes too) must not meet their zero weights
-                    if (key < s.keys.first || key > s.keys.last) u[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (key < first || key > last) u[k] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 mbar_arrive(vempty + 8 * vst);
                 if (++vst == Sm::kVStages) {
@@ -616,7 +755,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     vph ^= 1u;
                 }
                 const int b = count & 1;
-                ok = ok && mbar_wait_fast(v16free + 8 * b, ((count >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                ok = ok && pro_wait(v16free + 8 * b, ((count >> 1) & 1u) ^ 1u, abort_flag, p.status,
                                           p.wait_cycles);
                 uint8_t *dst = pro_smem + Sm::kV16Off + b * Sm::kV16Bytes;
 #pragma unroll
@@ -641,75 +780,152 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             }
         }
     } else {
+
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProSoftmaxRegs));
         // ---------------------------------------------------------- softmax
         const int half = warp >> 2, tid = static_cast<int>(threadIdx.x) & 127;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_addr + 128u * half, o_tmem = tmem + lane_addr + 256u + 128u * half;
-        const float *qf = reinterpret_cast<const float *>(pro_smem + Sm::kQfOff);
-        const float *scales = reinterpret_cast<const float *>(pro_smem + Sm::kScaleOff);
+        float *qf = reinterpret_cast<float *>(pro_smem + Sm::kQfOff) + 128 * half;
+        const float4 *factors = reinterpret_cast<const float4 *>(pro_smem + Sm::kFactorOff);
         int count = 0, segment = 0, uses = 0;
         bool ok = true;
-        while (walk.next(p, s)) {
-            const int rows = rows_of(s) - 128 * half;  // valid rows of this half
+        for (;;) {
+            const ProSegment *s = segment_at(segment);
+            // one answer for the half's threads, whose barriers below need all
+            // of them (a wait can give up in one thread and not in another)
+            if (half_any(half, s == nullptr)) break;
+            const int rows = s->rows - 128 * half;  // valid rows of this half
+            const int end = s->end, begin = s->tile;
             if (rows <= 0) {
-                count += s.end - s.tile;
+                count += end - begin;
                 ++segment;
                 continue;
             }
             const bool warp_on = (tid & ~31) < rows;
-            const int64_t row = static_cast<int64_t>(s.j) * kProRows + 128 * half + tid;
-            const int before = s.req.keys - s.req.n;
-            const int pos = before + static_cast<int>(row / group);
+            const int pos = s->before + (s->row_first + 128 * half + tid) / group;
             // positions of the warp's first and last valid row
-            const int64_t row_lo = row - lane;
-            const int64_t row_hi = min(row_lo + 31, static_cast<int64_t>(s.j) * kProRows + 128 * half + rows - 1);
-            const int pos_lo = before + static_cast<int>(row_lo / group), pos_hi = before + static_cast<int>(row_hi / group);
-            ok = ok && mbar_wait_fast(qfull + 8 * (segment & 1), (segment >> 1) & 1u, abort_flag, p.status,
-                                      p.wait_cycles);
-            const float f = qf[(segment & 1) * kProRows + 128 * half + tid];
+            const int pos_lo = __shfl_sync(0xFFFFFFFFu, pos, 0);
+            const int pos_hi = __shfl_sync(0xFFFFFFFFu, pos, min(31, max(rows - 1 - (tid & ~31), 0)));
+            // this half's queries as E4M3 parts, and each row's factor: LANES
+            // lanes hold a row, eight dimensions each, all loads in flight at
+            // once.  (The half's earlier score MMAs have retired: it has read
+            // their results.)
+            {
+                constexpr int LANES = DIM / 8, AT_ONCE = 128 / LANES, BATCH = 4;
+                const int l = tid % LANES;
+                const int row_first = s->row_first + 128 * half + tid / LANES;
+                int token = row_first / group, member = row_first % group;
+                const int token_step = AT_ONCE / group, member_step = AT_ONCE % group;
+                const uint16_t *q0 = p.q + static_cast<int64_t>(s->row0) * p.q_stride + s->g * group * DIM + 8 * l;
+                uint4 next[BATCH];
+                auto load = [&](int row0) {
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        next[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row0 + k * AT_ONCE + tid / LANES < rows)
+                            next[k] = *reinterpret_cast<const uint4 *>(q0 + static_cast<int64_t>(token) * p.q_stride +
+                                                                       member * DIM);
+                        token += token_step;
+                        member += member_step;
+                        if (member >= group) {
+                            member -= group;
+                            ++token;
+                        }
+                    }
+                };
+                load(0);
+                const int full = min((rows + AT_ONCE * BATCH - 1) / (AT_ONCE * BATCH), 128 / (AT_ONCE * BATCH));
+#pragma unroll 1
+                for (int b = 0; b < full; ++b) {
+                    uint4 u[BATCH];
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) u[k] = next[k];
+                    load((b + 1) * AT_ONCE * BATCH);  // (none past the last row)
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int row = (b * BATCH + k) * AT_ONCE + tid / LANES;
+                        uint32_t mag = fold_mag<QDT>(word_mag_max<QDT>(u[k], 0u));
+#pragma unroll
+                        for (int o = LANES / 2; o > 0; o >>= 1)
+                            mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o, LANES));
+                        const int e = part_exponent(mag_bits_to_float<QDT>(mag));
+                        const uint32_t up = static_cast<uint32_t>(127 + e) << 23;
+                        if (l == 0) qf[row] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                        uint32_t h[4];  // the scaled row in fp16: exact from 2^-22 of its largest element on
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint64_t x2 = f2_mul(widen16<QDT>(w[i]), f2_pack(up, up));
+                            const __half2 x = __floats2half2_rn(__uint_as_float(static_cast<uint32_t>(x2)),
+                                                                __uint_as_float(static_cast<uint32_t>(x2 >> 32)));
+                            h[i] = *reinterpret_cast<const uint32_t *>(&x);
+                        }
+                        uint8_t *dst = pro_smem + half * Sm::kParts * Sm::kQPart + (row >> 3) * 8 * DIM +
+                                       (l >> 1) * 128 + (row & 7) * 16 + 8 * (l & 1);
+#pragma unroll
+                        for (int part = 0; part < Sm::kParts; ++part) {
+                            const uint32_t c0 = take_part_f16(h[0], h[1]), c1 = take_part_f16(h[2], h[3]);
+                            *reinterpret_cast<uint2 *>(dst + part * Sm::kQPart) = make_uint2(c0, c1);
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(qfull + 8 * half);
+                half_sync(half);  // the row factors are written
+            }
+            const float f = qf[tid];
             ++segment;
             float m = -INFINITY, l = 0.0f;
-            for (int tile = s.tile; tile < s.end; ++tile, ++count, ++uses) {
+            for (int tile = begin; tile < end; ++tile, ++count, ++uses) {
                 // (a barrier per slot, not the key stage's, which may be
                 // filled again while this half is still in an epilogue)
-                ok = ok && mbar_wait_fast(scfull + 8 * (count & (kProScaleSlots - 1)), (count / kProScaleSlots) & 1u,
+                ok = ok && pro_wait(fcfull + 8 * (count & (kProScaleSlots - 1)), (count / kProScaleSlots) & 1u,
                                           abort_flag, p.status, p.wait_cycles);
-                ok = ok && mbar_wait_fast(sfull + 8 * half, uses & 1u, abort_flag, p.status, p.wait_cycles);
+                ok = ok && pro_wait(sfull + 8 * half, uses & 1u, abort_flag, p.status, p.wait_cycles);
                 tc_fence_after();
                 if (warp_on) {
-                    const float *sc = scales + (count & (kProScaleSlots - 1)) * 16;
+                    const float4 *fc = factors + (count & (kProScaleSlots - 1)) * 8;
                     const int key0 = tile * kProKeys;
-                    const bool plain = key0 + kProKeys - 1 <= pos_lo && (p.window == 0 || key0 > pos_hi - p.window);
-                    // columns [lo, hi) of this row are seen
-                    const int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0, hi = pos + 1 - key0;
-                    // factors of the 16 columns from 16 x on: the page's
-                    // scales; a page without a seen key was not copied
-                    auto factors = [&](int x, float &c, float &lv, float &rv) {
-                        const int pg = (16 * x) >> p.page_shift;
-                        const bool there = key0 + 16 * x <= s.keys.last && key0 + 16 * x + 15 >= s.keys.first;
-                        c = there ? f * sc[pg] : 0.0f;
-                        const float vs = there ? sc[8 + pg] : 1.0f;
-                        lv = __log2f(vs);
-                        rv = __frcp_rn(vs);
+                    // 64 columns at a time, read twice (maximum, weights): a
+                    // row of 128 scores does not fit the registers, and the
+                    // loops are kept rolled: their code fits the instruction
+                    // cache beside the other roles'
+                    uint32_t v[2][32];
+                    const bool masked =
+                        !(key0 + kProKeys - 1 <= pos_lo && (p.window == 0 || key0 > pos_hi - p.window));
+                    auto load = [&](int x) {
+                        tmem_ld32_nowait(s_tmem + 64 * x, v[0]);
+                        tmem_ld32_nowait(s_tmem + 64 * x + 32, v[1]);
+                        tmem_wait_ld();
                     };
                     float top = -INFINITY;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        load(x);
+                        if (masked) {
+                            // columns [lo, hi) are seen by this row; 32 that
+                            // all rows of the warp see are left alone, the
+                            // others go back masked for the second reading
+                            const int c0 = key0 + 64 * x;
+                            const int lo = p.window > 0 ? pos - p.window + 1 - c0 : 0, hi = pos + 1 - c0;
+                            const int lo_all = p.window > 0 ? pos_hi - p.window + 1 - c0 : 0, hi_all = pos_lo + 1 - c0;
 #pragma unroll
-                    for (int x = 0; x < kProKeys / 32; ++x) {
-                        uint32_t v[32];
-                        tmem_ld32_nowait(s_tmem + 32 * x, v);
-                        tmem_wait_ld();
+                            for (int y = 0; y < 2; ++y) {
+                                if (32 * y >= lo_all && 32 * y + 32 <= hi_all) continue;
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float c, lv, rv;
-                            factors(2 * x + y, c, lv, rv);
-                            float raw = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int col = 32 * x + 16 * y + i;
-                                const float sv = __uint_as_float(v[16 * y + i]);
-                                raw = fmaxf(raw, plain || (col >= lo && col < hi) ? sv : -INFINITY);
+                                for (int i = 0; i < 32; ++i)
+                                    if (32 * y + i < lo || 32 * y + i >= hi) v[y][i] = 0xFF800000u;  // -inf
+                                tmem_st32_nowait(s_tmem + 64 * x + 32 * y, v[y]);
                             }
-                            if (raw > -INFINITY) top = fmaxf(top, fmaf(raw, c, lv));
+                            tmem_wait_st();
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float raw = max16(v[y / 2] + 16 * (y & 1));
+                            const float4 k = fc[4 * x + y];
+                            // (-inf where the row sees none of the 16 keys)
+                            top = fmaxf(top, raw == -INFINITY ? raw : fmaf(raw, f * k.x, k.y));
                         }
                     }
                     const bool move = top > m + kProMove;
@@ -718,91 +934,93 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                         const float keep = to == -INFINITY ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - to));
                         l *= keep;
                         m = to;
-                        if (tile != s.tile) {
-                            ok = ok && mbar_wait_fast(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status,
-                                                      p.wait_cycles);
+                        if (tile != begin) {
+                            ok = ok && pro_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status,
+                                                p.wait_cycles);
                             tc_fence_after();
-#pragma unroll
-                            for (int x = 0; x < DIM / 32; ++x) {
-                                uint32_t v[32];
-                                tmem_ld32_nowait(o_tmem + 32 * x, v);
+#pragma unroll 1
+                            for (int x = 0; x < DIM / 16; ++x) {
+                                uint32_t o[16];
+                                tmem_ld_n(o_tmem + 16 * x, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
-                                tmem_st32_nowait(o_tmem + 32 * x, v);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                tmem_st_n(o_tmem + 16 * x, o);
                             }
                         }
                     }
                     const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        load(x);
+                        uint32_t w[32];
 #pragma unroll
-                    for (int x = 0; x < kProKeys / 32; ++x) {
-                        uint32_t v[32], w[16];
-                        tmem_ld32_nowait(s_tmem + 32 * x, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float c, lv, rv;
-                            factors(2 * x + y, c, lv, rv);
-                            const float b = lv - mu;
-                            float sum = 0.0f;
+                        for (int y = 0; y < 4; ++y) {
+                            const float4 k = fc[4 * x + y];
+                            // (positive, so that -inf stays -inf where the
+                            // factor is 0: a page that was not copied)
+                            const float a = fmaxf(f * k.x, 1e-37f), b = k.y - mu;
+                            const uint64_t a2 = f2_pack(__float_as_uint(a), __float_as_uint(a));
+                            const uint64_t b2 = f2_pack(__float_as_uint(b), __float_as_uint(b));
+                            uint64_t sum[2] = {0, 0};
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                float a[2];
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int col = 32 * x + 16 * y + i + k;
-                                    const float t = fmaf(__uint_as_float(v[16 * y + i + k]), c, b);
-                                    a[k] = plain || (col >= lo && col < hi) ? ex2(t) : 0.0f;
-                                    sum += a[k];
-                                }
-                                const __half2 h = __floats2half2_rn(a[0], a[1]);
+                                const uint32_t *c = v[y / 2] + 16 * (y & 1) + i;
+                                const uint64_t t = f2_fma(f2_pack(c[0], c[1]), a2, b2);
+                                const float w0 = ex2(__uint_as_float(static_cast<uint32_t>(t)));
+                                const float w1 = ex2(__uint_as_float(static_cast<uint32_t>(t >> 32)));
+                                sum[(i >> 1) & 1] =
+                                    f2_add(sum[(i >> 1) & 1], f2_pack(__float_as_uint(w0), __float_as_uint(w1)));
+                                const __half2 h = __floats2half2_rn(w0, w1);
                                 w[8 * y + i / 2] = *reinterpret_cast<const uint32_t *>(&h);
                             }
-                            l = fmaf(sum, rv, l);
+                            const uint64_t both = f2_add(sum[0], sum[1]);
+                            l = fmaf(__uint_as_float(static_cast<uint32_t>(both)) +
+                                         __uint_as_float(static_cast<uint32_t>(both >> 32)), k.z, l);
                         }
-                        tmem_st_n(s_tmem + 16 * x, w);  // below the columns still to be read
+                        tmem_st32_nowait(s_tmem + 32 * x, w);  // below the columns still to be read
+                        // these keys can be multiplied
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(wfull + 16 * half + 8 * x);
                     }
-                    tmem_wait_st();
+                } else {
+                    tc_fence_before();
+                    mbar_arrive(wfull + 16 * half);
+                    mbar_arrive(wfull + 16 * half + 8);
                 }
-                tc_fence_before();
-                mbar_arrive(wfull + 8 * half);
             }
 
             // ------------------------------------------------------ epilogue
-            ok = ok && mbar_wait_fast(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status, p.wait_cycles);
+            ok = ok && pro_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status, p.wait_cycles);
             tc_fence_after();
-            const bool whole = s.tile == s.keys.begin && s.end == s.keys.begin + s.keys.tiles;
+            const bool whole = begin == s->begin && end == s->stop;
             const bool valid = tid < rows;
-            const int token = s.req.row0 + static_cast<int>(row / group), head = s.g * group + static_cast<int>(row % group);
+            const int row = s->row_first + 128 * half + tid;
+            const int out_token = s->row0 + row / group, head = s->g * group + row % group;
             if (whole) {
                 if (warp_on) {
                     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < DIM / 32; ++x) {
                         uint32_t v[32];
                         tmem_ld32_nowait(o_tmem + 32 * x, v);
                         tmem_wait_ld();
-                        if (valid) {
+                        float o[32];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                float o[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    o[i] = l > 0.0f ? __uint_as_float(v[8 * y + i]) * inv : 0.0f;
-                                attn_store<8>(p, token, head, DIM, 32 * x + 8 * y, o);
-                            }
-                        }
+                        for (int i = 0; i < 32; ++i) o[i] = l > 0.0f ? __uint_as_float(v[i]) * inv : 0.0f;
+                        if (valid) attn_store<32>(p, out_token, head, DIM, 32 * x, o);
                     }
-                    if (valid && p.lse != nullptr) attn_store_lse(p, token, head, m, l);
+                    if (valid && p.lse != nullptr) attn_store_lse(p, out_token, head, m, l);
                 }
                 tc_fence_before();
             } else {
-                const long long seg0 = s.at - (s.tile - s.keys.begin), seg1 = seg0 + s.keys.tiles;
+                const long long seg0 = w0 + s->done - (begin - s->begin), seg1 = seg0 + (s->stop - s->begin);
                 const long long c0 = ((seg0 + 1) * ctas - 1) / total, c1 = (seg1 * ctas - 1) / total;
                 constexpr long long kPart = kProRows * (DIM + 2);
-                float *part = p.partials + (cta * 2 + (s.tile != s.keys.begin || seg0 == w0 ? 0 : 1)) * kPart;
+                float *part = p.partials + (cta * 2 + (begin != s->begin || seg0 == w0 ? 0 : 1)) * kPart;
                 if (warp_on) {
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < DIM / 32; ++x) {
                         uint32_t v[32];
                         tmem_ld32_nowait(o_tmem + 32 * x, v);
@@ -824,7 +1042,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 }
                 half_sync(half);
                 if (merge_now[half]) {
-                    pro_merge<DIM>(p, s, half, rows, group, static_cast<int>(c1 - c0 + 1), [&](int c) {
+                    pro_merge<DIM>(p, *s, half, rows, group, static_cast<int>(c1 - c0 + 1), [&](int c) {
                         const int slot = c == 0 && seg0 != total * c0 / ctas ? 1 : 0;
                         return p.partials + ((c0 + c) * 2 + slot) * kPart;
                     });
@@ -834,7 +1052,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
         }
     }
 
-    mbar_wait_drain(done_bar, 0, p.status);
+    pro_drain(done_bar, 0, p.status);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
