@@ -155,8 +155,13 @@ def workspace(device=None) -> torch.Tensor:
 
 
 def fp8l_read_status(ws: torch.Tensor) -> int:
+    lib = load()
     with torch.cuda.device(ws.device):
-        return int(load().fp8l_read_status(ws.data_ptr(), _stream(ws.device)))
+        st = int(lib.fp8l_read_status(ws.data_ptr(), _stream(ws.device)))
+        if st == ETIMEOUT and ws.numel() == lib.fp8_kv_attention_workspace_bytes():
+            # an attention call that gave up may leave its merge counters mid-way
+            ws[: lib.fp8_kv_attention_workspace_zero_bytes()].zero_()
+    return st
 
 
 STALL_MMA = 1
@@ -452,6 +457,11 @@ def fp8_w8a16_mm(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     return y
 
 
+# The functions of the paged cache run once per layer and step in front of
+# kernels of a few microseconds, so their checks are written to cost little:
+# one pass of plain attribute tests, the stream's handle without a Stream
+# object, no device switch when the device is current already.
+
 KV_PAGE_SIZES = (16, 32, 64, 128)
 KV_MIN_SCALE = 2.0 ** -64  # FP8L_KV_MIN_SCALE
 
@@ -502,28 +512,76 @@ def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, devic
     return KvCache(*codes, *scales)
 
 
-def _kv_check_cache(cache: KvCache):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream_handle(index: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _kv_call(f, index: int, *args) -> int:
+    """f(*args, current stream of device `index`) with that device current."""
+    with torch.cuda.device(index):
+        return f(*args, _stream_handle(index))
+
+
+def _kv_refuse(index: int, *ts):
+    """Says what is wrong with tensors that _kv_placed did not accept."""
+    for t in ts:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("expected CUDA tensors")
+        if t.get_device() != index:
+            raise ValueError("tensors are on different devices")
+        if not t.is_contiguous():
+            raise ValueError("expected contiguous tensors")
+
+
+def _kv_placed(index: int, ts) -> bool:
+    """Whether the tensors (or None) are contiguous and on device `index`."""
+    try:
+        for t in ts:
+            if t is not None and (t.get_device() != index or not t.is_contiguous()):
+                return False
+    except AttributeError:
+        return False
+    return True
+
+
+def _kv_device(t) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("expected CUDA tensors")
+    return t.get_device()
+
+
+def _kv_cache_shape(cache: KvCache):
+    """(num_pages, kv_heads, page_size, head_dim) of a well-formed cache."""
     k, v, ks, vs = cache
-    _need_cuda(k, v, ks, vs)
-    if k.dim() != 6 or k.shape[4:] != (8, 16) or v.shape != k.shape or \
-            ks.shape != k.shape[:2] or vs.shape != ks.shape:
+    shape = k.shape
+    if len(shape) != 6 or shape[4] != 8 or shape[5] != 16 or v.shape != shape or \
+            ks.shape != shape[:2] or vs.shape != shape[:2]:
         raise ValueError("cache codes are [num_pages, kv_heads, page_size / 8, head_dim / 16, 8, "
                          "16] and scales [num_pages, kv_heads]")
-    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or ks.dtype != torch.float32 or \
-            vs.dtype != torch.float32:
+    if k.dtype is not _U8 or v.dtype is not _U8 or ks.dtype is not _F32 or vs.dtype is not _F32:
         raise ValueError("cache codes are uint8, scales float32")
+    return shape[0], shape[1], shape[2] * 8, shape[3] * 16
 
 
-def _need_int32(**ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
-
-
-def _same_device(first: torch.Tensor, *ts):
-    for t in ts:
-        if t is not None and t.device != first.device:
-            raise ValueError("tensors are on different devices")
+def _rows(x: torch.Tensor) -> int:
+    """Row stride of a token tensor whose rows are dense (any row stride)."""
+    want = 1
+    for d in range(x.dim() - 1, 0, -1):
+        if x.shape[d] > 1 and x.stride(d) != want:
+            raise ValueError("expected dense rows (only the row stride may differ)")
+        want *= x.shape[d]
+    return x.stride(0) if x.shape[0] > 1 else want
 
 
 def fp8_kv_plan(q_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
@@ -536,41 +594,42 @@ def fp8_kv_plan(q_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.
     (q_offsets [R + 1], kv_lens after the step [R], positions and slots
     [tokens], used [2]: pages taken, tokens without a page), in `plan`'s
     tensors when given."""
-    _need_cuda(q_lens, kv_lens, block_table, free_pages, *(plan or ()))
-    _need_int32(q_lens=q_lens, kv_lens=kv_lens, block_table=block_table, free_pages=free_pages)
+    index = _kv_device(q_lens)
+    given = (q_lens, kv_lens, block_table, free_pages)
+    if not _kv_placed(index, given):
+        _kv_refuse(index, *given)
+    if q_lens.dtype is not _I32 or kv_lens.dtype is not _I32 or \
+            block_table.dtype is not _I32 or free_pages.dtype is not _I32:
+        raise ValueError("q_lens, kv_lens, block_table and free_pages must be int32")
     if block_table.dim() != 2:
         raise ValueError("block_table is [requests, table_width]")
     R, W = block_table.shape
     if q_lens.shape != (R,) or kv_lens.shape != (R,):
         raise ValueError("q_lens and kv_lens have one entry per row of block_table")
-    tokens, device = int(tokens), q_lens.device
-    _same_device(q_lens, kv_lens, block_table, free_pages, *(plan or ()))
+    tokens = int(tokens)
     if plan is None:
         # one allocation, 4-byte aligned parts
-        buf = torch.empty(2 * R + 3 + 2 * max(tokens, 0), dtype=torch.int32, device=device)
-        plan = KvPlan(*buf.split([R + 1, R, max(tokens, 0), max(tokens, 0), 2]))
+        n = tokens if tokens > 0 else 0
+        buf = torch.empty(2 * R + 3 + 2 * n, dtype=_I32, device=q_lens.device)
+        plan = KvPlan(*torch.unsafe_split_with_sizes(buf, (R + 1, R, n, n, 2)))
+        at = buf.data_ptr()
+        ptrs = (at, at + 4 * (R + 1), at + 4 * (2 * R + 1), at + 4 * (2 * R + 1 + n),
+                at + 4 * (2 * R + 1 + 2 * n))
     else:
-        _need_int32(**plan._asdict())
-        if [t.shape for t in plan] != [(R + 1,), (R,), (tokens,), (tokens,), (2,)]:
-            raise ValueError("plan tensors are [R + 1], [R], [tokens], [tokens], [2]")
-    with torch.cuda.device(device):
-        st = load().fp8_kv_plan(
-            q_lens.data_ptr(), kv_lens.data_ptr(), R, tokens, page_size, block_table.data_ptr(),
-            W, free_pages.data_ptr(), free_pages.numel(), plan.q_offsets.data_ptr(),
-            plan.kv_lens.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(),
-            plan.used.data_ptr(), _stream(device))
-    _check(st, "fp8_kv_plan")
+        if not _kv_placed(index, plan):
+            _kv_refuse(index, *plan)
+        if [t.shape for t in plan] != [(R + 1,), (R,), (tokens,), (tokens,), (2,)] or \
+                any(t.dtype is not _I32 for t in plan):
+            raise ValueError("plan tensors are int32 [R + 1], [R], [tokens], [tokens], [2]")
+        ptrs = tuple(t.data_ptr() for t in plan)
+    args = (q_lens.data_ptr(), kv_lens.data_ptr(), R, tokens, page_size, block_table.data_ptr(), W,
+            free_pages.data_ptr(), free_pages.numel(), *ptrs)
+    f = (_lib or load()).fp8_kv_plan
+    st = (f(*args, _stream_handle(index)) if _current_device() == index
+          else _kv_call(f, index, *args))
+    if st:
+        _check(st, "fp8_kv_plan")
     return plan
-
-
-def _rows(x: torch.Tensor) -> int:
-    """Row stride of a token tensor whose rows are dense (any row stride)."""
-    want = 1
-    for d in range(x.dim() - 1, 0, -1):
-        if x.shape[d] > 1 and x.stride(d) != want:
-            raise ValueError("expected dense rows (only the row stride may differ)")
-        want *= x.shape[d]
-    return x.stride(0) if x.shape[0] > 1 else want
 
 
 def fp8_qk_norm_rope_append(qkv: torch.Tensor, cache: KvCache, positions: torch.Tensor,
@@ -585,39 +644,44 @@ def fp8_qk_norm_rope_append(qkv: torch.Tensor, cache: KvCache, positions: torch.
     positions, slots: int32 [tokens] (fp8_kv_plan); cos_sin: float32
     [max_positions, rot] or None (no rotation); q_gamma, k_gamma: [head_dim]
     or None (no norm).  Returns q [tokens, q_heads, head_dim]."""
-    _kv_check_cache(cache)
-    _need_cuda(positions, slots, cos_sin, q_gamma, k_gamma, q)
-    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
-        raise TypeError("expected CUDA tensors")
-    _need_int32(positions=positions, slots=slots)
-    hkv, dim = cache.kv_heads, cache.head_dim
+    index = _kv_device(qkv)
+    k, v, ks, vs = cache
+    given = (k, v, ks, vs, positions, slots, cos_sin, q_gamma, k_gamma, q)
+    if not _kv_placed(index, given):
+        _kv_refuse(index, *given)
+    pages, hkv, page, dim = _kv_cache_shape(cache)
     if qkv.dim() != 2 or qkv.shape[1] % dim != 0:
         raise ValueError("qkv is [tokens, (q_heads + 2 kv_heads) * head_dim]")
-    T, heads = qkv.shape[0], qkv.shape[1] // dim - 2 * hkv
-    if positions.shape != (T,) or slots.shape != (T,):
-        raise ValueError("positions and slots have one entry per token")
-    if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32):
-        raise ValueError("cos_sin is float32 [max_positions, rot]")
-    for gamma in (q_gamma, k_gamma):
-        if gamma is not None and (gamma.shape != (dim,) or gamma.dtype != qkv.dtype):
-            raise ValueError("q_gamma and k_gamma are [head_dim] of qkv's dtype")
+    T, width = qkv.shape
+    dtype, heads = qkv.dtype, width // dim - 2 * hkv
+    if positions.shape != (T,) or slots.shape != (T,) or positions.dtype is not _I32 or \
+            slots.dtype is not _I32:
+        raise ValueError("positions and slots are int32, one entry per token")
+    angles, limit, rot = None, 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype is not _F32:
+            raise ValueError("cos_sin is float32 [max_positions, rot]")
+        angles, (limit, rot) = cos_sin.data_ptr(), cos_sin.shape
+    gammas = [None, None]
+    for i, gamma in enumerate((q_gamma, k_gamma)):
+        if gamma is not None:
+            if gamma.shape != (dim,) or gamma.dtype is not dtype:
+                raise ValueError("q_gamma and k_gamma are [head_dim] of qkv's dtype")
+            gammas[i] = gamma.data_ptr()
     if q is None:
-        q = torch.empty((T, max(heads, 0), dim), dtype=qkv.dtype, device=qkv.device)
-    elif q.shape != (T, heads, dim) or q.dtype != qkv.dtype:
+        q = torch.empty((T, heads if heads > 0 else 0, dim), dtype=dtype, device=qkv.device)
+    elif q.shape != (T, heads, dim) or q.dtype is not dtype:
         raise ValueError("q is [tokens, q_heads, head_dim] of qkv's dtype")
-    _same_device(qkv, *cache, positions, slots, cos_sin, q_gamma, k_gamma, q)
-    with torch.cuda.device(qkv.device):
-        st = load().fp8_qk_norm_rope_append(
-            qkv.data_ptr(), _DTYPE_CODE.get(qkv.dtype, -1), T, _rows(qkv), heads, hkv, dim,
-            q_gamma.data_ptr() if q_gamma is not None else None,
-            k_gamma.data_ptr() if k_gamma is not None else None, float(eps),
-            cos_sin.data_ptr() if cos_sin is not None else None,
-            cos_sin.shape[0] if cos_sin is not None else 0,
-            cos_sin.shape[1] if cos_sin is not None else 0, 1 if interleaved else 0,
-            positions.data_ptr(), slots.data_ptr(), q.data_ptr(), cache.k.data_ptr(),
-            cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
-            cache.num_pages, cache.page_size, _stream(qkv.device))
-    _check(st, "fp8_qk_norm_rope_append")
+    args = (qkv.data_ptr(), _DTYPE_CODE.get(dtype, -1), T,
+            width if qkv.is_contiguous() else _rows(qkv), heads, hkv, dim, gammas[0], gammas[1],
+            eps, angles, limit, rot, 1 if interleaved else 0, positions.data_ptr(),
+            slots.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+            vs.data_ptr(), pages, page)
+    f = (_lib or load()).fp8_qk_norm_rope_append
+    st = (f(*args, _stream_handle(index)) if _current_device() == index
+          else _kv_call(f, index, *args))
+    if st:
+        _check(st, "fp8_qk_norm_rope_append")
     return q
 
 
@@ -629,13 +693,16 @@ def fp8_kv_attention_workspace(device=None) -> torch.Tensor:
     allocated once per stream and reused (its counters zeroed), so calls on
     different streams do not share one.  During a graph capture without such
     a workspace the graph gets its own, zeroed at every replay."""
-    device = torch.device("cuda", torch.cuda.current_device() if device is None
-                          else torch.device(device).index or 0)
-    key = (device, _stream(device))
+    if isinstance(device, int):
+        index = device
+    else:
+        index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    key = (index, _stream_handle(index))
     ws = _attention_workspaces.get(key)
     if ws is None:
         lib = load()
-        ws = torch.empty(lib.fp8_kv_attention_workspace_bytes(), dtype=torch.uint8, device=device)
+        ws = torch.empty(lib.fp8_kv_attention_workspace_bytes(), dtype=_U8,
+                         device=torch.device("cuda", index))
         ws[: lib.fp8_kv_attention_workspace_zero_bytes()].zero_()
         if not torch.cuda.is_current_stream_capturing():
             _attention_workspaces[key] = ws
@@ -655,45 +722,54 @@ def fp8_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
     request's new tokens.  sm_scale defaults to head_dim ** -0.5; window > 0
     limits each row to its last `window` keys; out_dtype: q's (default) or
     uint8 (E4M3 codes of out / out_scale).  Returns (out, lse or None)."""
-    _kv_check_cache(cache)
-    _need_cuda(block_table, q_offsets, kv_lens, out_scale, out, lse, ws)
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("expected CUDA tensors")
-    _need_int32(block_table=block_table, q_offsets=q_offsets, kv_lens=kv_lens)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+    index = _kv_device(q)
+    k, v, ks, vs = cache
+    if ws is None:
+        ws = fp8_kv_attention_workspace(index)
+    elif ws.dtype is not _U8 or ws.numel() < load().fp8_kv_attention_workspace_bytes():
+        raise ValueError("ws is a uint8 tensor of fp8_kv_attention_workspace_bytes() elements")
+    given = (k, v, ks, vs, block_table, q_offsets, kv_lens, out_scale, out, lse, ws)
+    if not _kv_placed(index, given):
+        _kv_refuse(index, *given)
+    pages, hkv, page, dim = _kv_cache_shape(cache)
+    if block_table.dtype is not _I32 or q_offsets.dtype is not _I32 or kv_lens.dtype is not _I32:
+        raise ValueError("block_table, q_offsets and kv_lens must be int32")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != dim:
         raise ValueError("q is [tokens, q_heads, head_dim]")
     if block_table.dim() != 2:
         raise ValueError("block_table is [requests, table_width]")
     R, W = block_table.shape
     if q_offsets.shape != (R + 1,) or kv_lens.shape != (R,):
         raise ValueError("q_offsets is [requests + 1], kv_lens [requests]")
-    T, heads, dim = q.shape
     if out_dtype is None:
         out_dtype = q.dtype if out is None else out.dtype
-    if out_dtype == torch.float8_e4m3fn:
-        out_dtype = torch.uint8
+    if out_dtype is torch.float8_e4m3fn:
+        out_dtype = _U8
     if out is None:
-        out = torch.empty((T, heads, dim), dtype=out_dtype, device=q.device)
-    elif out.shape != q.shape or _codes(out).dtype != out_dtype:
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    elif out.shape != shape or _codes(out).dtype is not out_dtype:
         raise ValueError("out is [tokens, q_heads, head_dim] of out_dtype")
-    if out_scale is not None and (out_scale.dtype != torch.float32 or out_scale.numel() != 1):
-        raise ValueError("out_scale is one float32")
-    if lse is None and want_lse:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    elif lse is not None and (lse.shape != (T, heads) or lse.dtype != torch.float32):
-        raise ValueError("lse is float32 [tokens, q_heads]")
-    if ws is None:
-        ws = fp8_kv_attention_workspace(q.device)
-    _same_device(q, *cache, block_table, q_offsets, kv_lens, out_scale, out, lse, ws)
-    with torch.cuda.device(q.device):
-        st = load().fp8_kv_attention(
-            q.data_ptr(), _DTYPE_CODE.get(q.dtype, -1), T, _rows(q), heads, cache.kv_heads, dim,
-            cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-            cache.v_scale.data_ptr(), cache.num_pages, cache.page_size, block_table.data_ptr(), W,
-            q_offsets.data_ptr(), kv_lens.data_ptr(), R, int(max_q_len),
-            float(dim ** -0.5 if sm_scale is None else sm_scale), int(window),
-            out_scale.data_ptr() if out_scale is not None else None, out.data_ptr(),
-            _DTYPE_CODE.get(out_dtype, -1), lse.data_ptr() if lse is not None else None,
-            ws.data_ptr(), _stream(q.device))
-    _check(st, "fp8_kv_attention")
+    scale_ptr = lse_ptr = None
+    if out_scale is not None:
+        if out_scale.dtype is not _F32 or out_scale.numel() != 1:
+            raise ValueError("out_scale is one float32")
+        scale_ptr = out_scale.data_ptr()
+    if want_lse and lse is None:
+        lse = torch.empty(shape[:2], dtype=_F32, device=q.device)
+    if lse is not None:
+        if lse.shape != shape[:2] or lse.dtype is not _F32:
+            raise ValueError("lse is float32 [tokens, q_heads]")
+        lse_ptr = lse.data_ptr()
+    args = (q.data_ptr(), _DTYPE_CODE.get(q.dtype, -1), shape[0],
+            shape[1] * dim if q.is_contiguous() else _rows(q), shape[1], hkv, dim, k.data_ptr(),
+            v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page, block_table.data_ptr(), W,
+            q_offsets.data_ptr(), kv_lens.data_ptr(), R, max_q_len,
+            dim ** -0.5 if sm_scale is None else sm_scale, window, scale_ptr, out.data_ptr(),
+            _DTYPE_CODE.get(out_dtype, -1), lse_ptr, ws.data_ptr())
+    f = (_lib or load()).fp8_kv_attention
+    st = (f(*args, _stream_handle(index)) if _current_device() == index
+          else _kv_call(f, index, *args))
+    if st:
+        _check(st, "fp8_kv_attention")
     return out, lse
