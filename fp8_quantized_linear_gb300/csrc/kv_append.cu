@@ -18,8 +18,8 @@
 // the chunk are found from the slots alone (ballots of "first slot of a run"
 // and "continues a run"), so no list of pages has to be built first.  Runs of
 // one or two tokens (decode) go to one group each; longer runs (prompts) are
-// spread over the whole block, the rows staying in registers between the
-// maximum and the cast.  Tokens that a page already holds are re-cast by the
+// spread over the whole block, which reads them twice (maximum, cast), the
+// second time from L1.  Tokens that a page already holds are re-cast by the
 // whole block when the scale grew: a group alone would read up to 127 rows
 // one after the other.
 #include "kv_device.cuh"
@@ -29,9 +29,8 @@ namespace fp8l {
 namespace {
 
 constexpr int kAppThreads = 256;
-constexpr int kAppMaxPage = 128;
 constexpr int kAppMaxChunk = 64;    // tokens whose runs one block starts
-constexpr int kAppHeadsPerGroup = 4;  // query heads of a token per group: loads in flight
+constexpr int kAppHeadsPerGroup = 8;  // query heads of a token per group: loads in flight
 
 struct AppendParams {
     const uint16_t *qkv;
@@ -55,101 +54,157 @@ struct AppendParams {
 // The pages' blocks of a scale: values are never quantized with less
 constexpr float kKvMinScale = FP8L_KV_MIN_SCALE;
 
+// One row (a token's head) in a group of DIM / 8 lanes, eight dimensions each
+// as float pairs.  kSplit: a lane holds dimensions 4 l .. 4 l + 3 and
+// DIM / 2 + 4 l .. + 3, so that a rotation over the whole head in halves has
+// both dimensions of a pair in one thread; otherwise 8 l .. 8 l + 7.
+enum Layout { kContiguous = 0, kSplit = 1 };
+
 struct Row {
-    float x[8];
+    uint64_t p[4];
 };
 
-template <int DT>
-__device__ __forceinline__ Row widen_row(const uint4 &u) {
-    Row r;
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint64_t f = widen16<DT>(w[i]);
-        r.x[2 * i] = __uint_as_float(static_cast<uint32_t>(f));
-        r.x[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(f >> 32));
+struct Raw {
+    uint32_t w[4];
+};
+
+template <int DIM, int LAYOUT>
+__device__ __forceinline__ Raw load_raw(const uint16_t *row, int l) {
+    Raw r;
+    if constexpr (LAYOUT == kSplit) {
+        const uint2 a = *reinterpret_cast<const uint2 *>(row + 4 * l);
+        const uint2 b = *reinterpret_cast<const uint2 *>(row + DIM / 2 + 4 * l);
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = b.x, r.w[3] = b.y;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4 *>(row + 8 * l);
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
     }
     return r;
 }
 
 template <int DT>
-__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+__device__ __forceinline__ Row widen_row(const Raw &u) {
+    Row r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = widen16<DT>(u.w[i]);
+    return r;
+}
+
+__device__ __forceinline__ float lo_f(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float hi_f(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
+__device__ __forceinline__ uint64_t pair_of(float a, float b) { return f2_pack(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ uint64_t f2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
+
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(uint64_t p) {
     if constexpr (DT == FP8L_BF16) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo_f(p), hi_f(p));
         return *reinterpret_cast<uint32_t *>(&h);
     } else {
-        __half2 h = __floats2half2_rn(a, b);
+        __half2 h = __floats2half2_rn(lo_f(p), hi_f(p));
         return *reinterpret_cast<uint32_t *>(&h);
     }
 }
 
-// cosines and sines of a token for the eight dimensions [8 l, 8 l + 8) of a
-// lane (four pairs in c[0..3], s[0..3] when interleaved)
+template <int DT, int DIM, int LAYOUT>
+__device__ __forceinline__ void store_row16(uint16_t *row, int l, const Row &r) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = narrow2<DT>(r.p[i]);
+    if constexpr (LAYOUT == kSplit) {
+        *reinterpret_cast<uint2 *>(row + 4 * l) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(row + DIM / 2 + 4 * l) = make_uint2(w[2], w[3]);
+    } else {
+        *reinterpret_cast<uint4 *>(row + 8 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Cosines and sines of a token for a lane's rotation pairs: the float pairs
+// of its four (kSplit: dimensions 4 l .. of the first half; interleaved:
+// pairs 4 l ..) or eight (a partner lane holds the other dimension) angles.
+template <int LAYOUT>
 struct Turn {
-    float c[8], s[8];
-    int half8;  // rot / 16: lanes of the rotated first half
+    static constexpr int kPairs = LAYOUT == kSplit ? 2 : 4;
+    uint64_t c[kPairs], s[kPairs];
+    int half8;  // rot / 16: lanes of the rotated first half (contiguous)
     bool on;    // this lane's dimensions rotate
 };
 
-__device__ __forceinline__ Turn load_turn(const AppendParams &p, int token, int l) {
-    Turn t;
+template <int LAYOUT>
+__device__ __forceinline__ Turn<LAYOUT> load_turn(const AppendParams &p, int token, int l) {
+    Turn<LAYOUT> t;
     t.half8 = p.rot >> 4;
-    t.on = 8 * l < p.rot;
+    t.on = 8 * l < p.rot || (LAYOUT == kSplit && p.rot > 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        t.c[i] = 1.0f;
-        t.s[i] = 0.0f;
+    for (int i = 0; i < Turn<LAYOUT>::kPairs; ++i) {
+        t.c[i] = pair_of(1.0f, 1.0f);
+        t.s[i] = 0;
     }
     if (t.on) {
         const int pos = min(max(p.positions[token], 0), p.max_positions - 1);
         const float *row = p.cos_sin + static_cast<int64_t>(pos) * p.rot;
-        const int half = p.rot >> 1;
-        const int i0 = p.interleaved ? 4 * l : 8 * (l < t.half8 ? l : l - t.half8);
+        const float *sin = row + (p.rot >> 1);
+        const int i0 = LAYOUT == kSplit || p.interleaved ? 4 * l : 8 * (l < t.half8 ? l : l - t.half8);
         const float4 c0 = *reinterpret_cast<const float4 *>(row + i0);
-        const float4 s0 = *reinterpret_cast<const float4 *>(row + half + i0);
-        t.c[0] = c0.x, t.c[1] = c0.y, t.c[2] = c0.z, t.c[3] = c0.w;
-        t.s[0] = s0.x, t.s[1] = s0.y, t.s[2] = s0.z, t.s[3] = s0.w;
-        if (!p.interleaved) {
-            const float4 c1 = *reinterpret_cast<const float4 *>(row + i0 + 4);
-            const float4 s1 = *reinterpret_cast<const float4 *>(row + half + i0 + 4);
-            t.c[4] = c1.x, t.c[5] = c1.y, t.c[6] = c1.z, t.c[7] = c1.w;
-            t.s[4] = s1.x, t.s[5] = s1.y, t.s[6] = s1.z, t.s[7] = s1.w;
+        const float4 s0 = *reinterpret_cast<const float4 *>(sin + i0);
+        t.c[0] = pair_of(c0.x, c0.y), t.c[1] = pair_of(c0.z, c0.w);
+        t.s[0] = pair_of(s0.x, s0.y), t.s[1] = pair_of(s0.z, s0.w);
+        if constexpr (LAYOUT == kContiguous) {
+            if (!p.interleaved) {
+                const float4 c1 = *reinterpret_cast<const float4 *>(row + i0 + 4);
+                const float4 s1 = *reinterpret_cast<const float4 *>(sin + i0 + 4);
+                t.c[2] = pair_of(c1.x, c1.y), t.c[3] = pair_of(c1.z, c1.w);
+                t.s[2] = pair_of(s1.x, s1.y), t.s[3] = pair_of(s1.z, s1.w);
+            }
         }
     }
     return t;
 }
 
-// The norm (when `gamma`) and the rotation of one row held by the LANES
-// lanes of `mask`
+// 1 / sqrt(mean of squares + eps) of the row held by the lanes of `mask`
 template <int LANES>
-__device__ __forceinline__ void norm_rotate(Row &r, bool norm, const Row &gamma, float eps, const Turn &t,
-                                            bool interleaved, int l, uint32_t mask) {
-    if (norm) {
-        float ss = 0.0f;
+__device__ __forceinline__ float row_rms(const Row &r, float eps, uint32_t mask) {
+    const uint64_t a = f2_fma(r.p[1], r.p[1], f2_mul(r.p[0], r.p[0]));
+    const uint64_t b = f2_fma(r.p[3], r.p[3], f2_mul(r.p[2], r.p[2]));
+    float ss = (lo_f(a) + hi_f(a)) + (lo_f(b) + hi_f(b));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(r.x[i], r.x[i], ss);
+    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o, LANES);
+    return rsqrtf(ss * (1.0f / (8 * LANES)) + eps);
+}
+
+__device__ __forceinline__ void scale_row(Row &r, float inv, const Row &gamma) {
+    const uint64_t i2 = pair_of(inv, inv);
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o, LANES);
-        const float inv = __fdiv_rn(1.0f, __fsqrt_rn(ss * (1.0f / (8 * LANES)) + eps));
+    for (int i = 0; i < 4; ++i) r.p[i] = f2_mul(f2_mul(r.p[i], i2), gamma.p[i]);
+}
+
+// (a, b) <- (a cos - b sin, b cos + a sin)
+template <int LANES, int LAYOUT>
+__device__ __forceinline__ void rotate_row(Row &r, const Turn<LAYOUT> &t, bool interleaved, int l, uint32_t mask) {
+    if constexpr (LAYOUT == kSplit) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r.x[i] = (r.x[i] * inv) * gamma.x[i];
-    }
-    if (interleaved) {
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t a = r.p[i], b = r.p[i + 2];
+            r.p[i] = f2_fma(f2_neg(b), t.s[i], f2_mul(a, t.c[i]));
+            r.p[i + 2] = f2_fma(a, t.s[i], f2_mul(b, t.c[i]));
+        }
+    } else if (interleaved) {
         if (t.on) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float a = r.x[2 * i], b = r.x[2 * i + 1];
-                r.x[2 * i] = a * t.c[i] - b * t.s[i];
-                r.x[2 * i + 1] = b * t.c[i] + a * t.s[i];
+                const float a = lo_f(r.p[i]), b = hi_f(r.p[i]);
+                const float c = i & 1 ? hi_f(t.c[i >> 1]) : lo_f(t.c[i >> 1]);
+                const float s = i & 1 ? hi_f(t.s[i >> 1]) : lo_f(t.s[i >> 1]);
+                r.p[i] = pair_of(a * c - b * s, b * c + a * s);
             }
         }
     } else {
         const bool low = l < t.half8;
         const int partner = !t.on ? l : (low ? l + t.half8 : l - t.half8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float other = __shfl_sync(mask, r.x[i], partner, LANES);
-            if (t.on) r.x[i] = low ? r.x[i] * t.c[i] - other * t.s[i] : r.x[i] * t.c[i] + other * t.s[i];
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t other = __shfl_sync(mask, r.p[i], partner, LANES);
+            if (t.on) r.p[i] = f2_fma(low ? f2_neg(other) : other, t.s[i], f2_mul(r.p[i], t.c[i]));
         }
     }
 }
@@ -157,15 +212,16 @@ __device__ __forceinline__ void norm_rotate(Row &r, bool norm, const Row &gamma,
 __device__ __forceinline__ uint32_t row_mag(const Row &r) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(r.x[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 4; ++i)
+        m = max(m, max(static_cast<uint32_t>(r.p[i]) & 0x7FFFFFFFu, static_cast<uint32_t>(r.p[i] >> 32) & 0x7FFFFFFFu));
     return m;
 }
 
 __device__ __forceinline__ uint2 row_codes(const Row &r, const Quot &d) {
-    const uint4 a = make_uint4(__float_as_uint(r.x[0]), __float_as_uint(r.x[1]), __float_as_uint(r.x[2]),
-                               __float_as_uint(r.x[3]));
-    const uint4 b = make_uint4(__float_as_uint(r.x[4]), __float_as_uint(r.x[5]), __float_as_uint(r.x[6]),
-                               __float_as_uint(r.x[7]));
+    const uint4 a = make_uint4(static_cast<uint32_t>(r.p[0]), static_cast<uint32_t>(r.p[0] >> 32),
+                               static_cast<uint32_t>(r.p[1]), static_cast<uint32_t>(r.p[1] >> 32));
+    const uint4 b = make_uint4(static_cast<uint32_t>(r.p[2]), static_cast<uint32_t>(r.p[2] >> 32),
+                               static_cast<uint32_t>(r.p[3]), static_cast<uint32_t>(r.p[3] >> 32));
     return make_uint2(codes_of_word<FP8L_F32, false>(a, d).x, codes_of_word<FP8L_F32, false>(b, d).x);
 }
 
@@ -208,9 +264,9 @@ __device__ void recast_block(uint8_t *cache, const Recast &job, int page_size) {
     }
 }
 
-template <int DT, int DIM>
+template <int DT, int DIM, int LAYOUT>
 __device__ void append_unit(const AppendParams &p, int unit) {
-    constexpr int LANES = DIM / 8, GROUPS = kAppThreads / LANES, ROWS = kAppMaxPage / GROUPS;
+    constexpr int LANES = DIM / 8, GROUPS = kAppThreads / LANES, BATCH = 2;
     __shared__ uint32_t lead[8], cont[8];
     __shared__ uint32_t red[33];
     __shared__ Recast jobs[kAppMaxChunk];
@@ -259,17 +315,28 @@ __device__ void append_unit(const AppendParams &p, int unit) {
 
     uint8_t *cache = values ? p.v_cache : p.k_cache;
     float *scales = values ? p.v_scale : p.k_scale;
-    const uint16_t *src = p.qkv + (p.q_heads + (values ? p.kv_heads : 0) + head) * DIM + 8 * l;
+    const uint16_t *src = p.qkv + (p.q_heads + (values ? p.kv_heads : 0) + head) * DIM;
     const bool norm = !values && p.k_gamma != nullptr;
     Row gamma = {};
-    if (norm) gamma = widen_row<DT>(*reinterpret_cast<const uint4 *>(p.k_gamma + 8 * l));
-    auto load = [&](int t, uint32_t m) {
-        Row r = widen_row<DT>(*reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(t) * p.stride));
-        if (!values) norm_rotate<LANES>(r, norm, gamma, p.eps, load_turn(p, t, l), p.interleaved != 0, l, m);
+    if (norm) gamma = widen_row<DT>(load_raw<DIM, LAYOUT>(p.k_gamma, l));
+    auto load = [&](int t) { return load_raw<DIM, LAYOUT>(src + static_cast<int64_t>(t) * p.stride, l); };
+    // the float32 row of a token
+    auto finish = [&](const Raw &u, const Turn<LAYOUT> &turn) {
+        Row r = widen_row<DT>(u);
+        if (norm) scale_row(r, row_rms<LANES>(r, p.eps, mask), gamma);
+        if (!values && p.rot > 0) rotate_row<LANES, LAYOUT>(r, turn, p.interleaved != 0, l, mask);
         return r;
     };
+    const Turn<LAYOUT> none = {};
     auto store = [&](const Row &r, int64_t ph, int o, const Quot &d) {
-        *reinterpret_cast<uint2 *>(cache + kv_chunk_offset(ph, P, DIM, o, l >> 1) + 8 * (l & 1)) = row_codes(r, d);
+        const uint2 c = row_codes(r, d);
+        if constexpr (LAYOUT == kSplit) {
+            uint8_t *at = cache + kv_chunk_offset(ph, P, DIM, o, l >> 2) + 4 * (l & 3);
+            *reinterpret_cast<uint32_t *>(at) = c.x;
+            *reinterpret_cast<uint32_t *>(at + DIM / 32 * 128) = c.y;
+        } else {
+            *reinterpret_cast<uint2 *>(cache + kv_chunk_offset(ph, P, DIM, o, l >> 1) + 8 * (l & 1)) = c;
+        }
     };
 
     // runs of one or two tokens: one group each
@@ -280,8 +347,8 @@ __device__ void append_unit(const AppendParams &p, int unit) {
         const int t = t0 + i, slot = p.slots[t], o = slot & (P - 1);
         const int64_t ph = static_cast<int64_t>(slot >> p.page_shift) * p.kv_heads + head;
         const float old = o > 0 ? scales[ph] : 0.0f;
-        Row a = load(t, mask), b = a;
-        if (n == 2) b = load(t + 1, mask);
+        const Row a = finish(load(t), values ? none : load_turn<LAYOUT>(p, t, l));
+        const Row b = n == 2 ? finish(load(t + 1), values ? none : load_turn<LAYOUT>(p, t + 1, l)) : a;
         uint32_t m = max(row_mag(a), row_mag(b));
 #pragma unroll
         for (int x = LANES / 2; x > 0; x >>= 1) m = max(m, __shfl_xor_sync(mask, m, x, LANES));
@@ -303,21 +370,29 @@ __device__ void append_unit(const AppendParams &p, int unit) {
             const int t = t0 + i, slot = p.slots[t], o = slot & (P - 1);
             const int64_t ph = static_cast<int64_t>(slot >> p.page_shift) * p.kv_heads + head;
             const float old = o > 0 ? scales[ph] : 0.0f;
-            Row x[ROWS];
-            uint32_t m = 0;
+            // rows in batches, twice: the second reading finds them in L1 (a
+            // page's rows of a head are 32 KB at most), and few registers
+            // leave room for the blocks of queries on the SM
+            auto each_row = [&](auto &&use) {
+#pragma unroll 1
+                for (int j0 = g; j0 < n; j0 += BATCH * GROUPS) {
+                    Raw u[BATCH];
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                if (g + j * GROUPS < n) {
-                    x[j] = load(t + g + j * GROUPS, mask);
-                    m = max(m, row_mag(x[j]));
+                    for (int j = 0; j < BATCH; ++j)
+                        if (j0 + j * GROUPS < n) u[j] = load(t + j0 + j * GROUPS);
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) {
+                        const int i = j0 + j * GROUPS;
+                        if (i < n) use(finish(u[j], values ? none : load_turn<LAYOUT>(p, t + i, l)), i);
+                    }
                 }
-            }
+            };
+            uint32_t m = 0;
+            each_row([&](const Row &r, int) { m = max(m, row_mag(r)); });
             m = block_max_u32(m, red);
             const float s = fmaxf(block_scale(m), old);
             const Quot d = Quot::make<FP8L_F32>(s);
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j)
-                if (g + j * GROUPS < n) store(x[j], ph, o + g + j * GROUPS, d);
+            each_row([&](const Row &r, int i) { store(r, ph, o + i, d); });
             if (o > 0 && s > old) recast_block<DIM>(cache, Recast{ph, o, old, s}, P);
             __syncthreads();  // every thread has read the old scale and the block maximum
             if (tid == 0) scales[ph] = s;
@@ -327,7 +402,7 @@ __device__ void append_unit(const AppendParams &p, int unit) {
     for (int j = 0; j < num_jobs; ++j) recast_block<DIM>(cache, jobs[j], P);
 }
 
-template <int DT, int DIM>
+template <int DT, int DIM, int LAYOUT>
 __device__ void query_rows(const AppendParams &p, int block) {
     constexpr int LANES = DIM / 8, GROUPS = kAppThreads / LANES;
     const int tid = static_cast<int>(threadIdx.x);
@@ -337,37 +412,44 @@ __device__ void query_rows(const AppendParams &p, int block) {
     const int64_t t64 = item / p.head_groups;
     if (t64 >= p.tokens) return;
     const int t = static_cast<int>(t64);
-    const int h0 = static_cast<int>(item % p.head_groups) * kAppHeadsPerGroup;
+    const int h0 = static_cast<int>(item - t64 * p.head_groups) * kAppHeadsPerGroup;
     const int n = min(kAppHeadsPerGroup, p.q_heads - h0);
-    const uint16_t *src = p.qkv + static_cast<int64_t>(t) * p.stride + h0 * DIM + 8 * l;
-    uint4 u[kAppHeadsPerGroup];
+    const uint16_t *src = p.qkv + static_cast<int64_t>(t) * p.stride + h0 * DIM;
+    Raw u[kAppHeadsPerGroup];
 #pragma unroll
-    for (int h = 0; h < kAppHeadsPerGroup; ++h)
-        u[h] = h < n ? *reinterpret_cast<const uint4 *>(src + h * DIM) : make_uint4(0u, 0u, 0u, 0u);
+    for (int h = 0; h < kAppHeadsPerGroup; ++h) u[h] = load_raw<DIM, LAYOUT>(src + (h < n ? h : 0) * DIM, l);
     const bool norm = p.q_gamma != nullptr;
     Row gamma = {};
-    if (norm) gamma = widen_row<DT>(*reinterpret_cast<const uint4 *>(p.q_gamma + 8 * l));
-    const Turn turn = load_turn(p, t, l);
-    uint16_t *dst = p.q_out + (static_cast<int64_t>(t) * p.q_heads + h0) * DIM + 8 * l;
+    if (norm) gamma = widen_row<DT>(load_raw<DIM, LAYOUT>(p.q_gamma, l));
+    Turn<LAYOUT> turn;
+    if (p.rot > 0) turn = load_turn<LAYOUT>(p, t, l);
+    uint16_t *dst = p.q_out + (static_cast<int64_t>(t) * p.q_heads + h0) * DIM;
 #pragma unroll
     for (int h = 0; h < kAppHeadsPerGroup; ++h) {
         Row r = widen_row<DT>(u[h]);
-        norm_rotate<LANES>(r, norm, gamma, p.eps, turn, p.interleaved != 0, l, mask);
-        if (h < n)
-            *reinterpret_cast<uint4 *>(dst + h * DIM) =
-                make_uint4(narrow2<DT>(r.x[0], r.x[1]), narrow2<DT>(r.x[2], r.x[3]),
-                           narrow2<DT>(r.x[4], r.x[5]), narrow2<DT>(r.x[6], r.x[7]));
+        if (norm) scale_row(r, row_rms<LANES>(r, p.eps, mask), gamma);
+        if (p.rot > 0) rotate_row<LANES, LAYOUT>(r, turn, p.interleaved != 0, l, mask);
+        if (h < n) store_row16<DT, DIM, LAYOUT>(dst + h * DIM, l, r);
     }
 }
 
-template <int DT, int DIM>
-__global__ void __launch_bounds__(kAppThreads) qk_norm_rope_append_kernel(const AppendParams p) {
+template <int DT, int DIM, int LAYOUT>
+__global__ void __launch_bounds__(kAppThreads, 4) qk_norm_rope_append_kernel(const AppendParams p) {
     grid_dependency_sync();
     const int b = static_cast<int>(blockIdx.x);
     if (b < p.kv_blocks)
-        append_unit<DT, DIM>(p, b);
+        append_unit<DT, DIM, LAYOUT>(p, b);
     else
-        query_rows<DT, DIM>(p, b - p.kv_blocks);
+        query_rows<DT, DIM, LAYOUT>(p, b - p.kv_blocks);
+}
+
+template <int DT, int DIM>
+int launch_append(const AppendParams &p, dim3 grid, cudaStream_t stream) {
+    // both dimensions of a rotation pair in one thread, where the halves of
+    // the whole head rotate against each other (the usual case)
+    if (p.rot == DIM && !p.interleaved)
+        return launch_dependent(qk_norm_rope_append_kernel<DT, DIM, kSplit>, grid, kAppThreads, 0, stream, p);
+    return launch_dependent(qk_norm_rope_append_kernel<DT, DIM, kContiguous>, grid, kAppThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -430,9 +512,8 @@ extern "C" int fp8_qk_norm_rope_append(const void *qkv, int dtype, int64_t token
     if (kv_blocks + q_blocks > INT32_MAX) return FP8L_ESHAPE;
     p.kv_blocks = static_cast<int>(kv_blocks);
     const dim3 grid(static_cast<unsigned>(kv_blocks + q_blocks));
-    auto kernel = dtype == FP8L_BF16 ? (head_dim == 128 ? qk_norm_rope_append_kernel<FP8L_BF16, 128>
-                                                        : qk_norm_rope_append_kernel<FP8L_BF16, 64>)
-                                     : (head_dim == 128 ? qk_norm_rope_append_kernel<FP8L_F16, 128>
-                                                        : qk_norm_rope_append_kernel<FP8L_F16, 64>);
-    return launch_dependent(kernel, grid, kAppThreads, 0, as_stream(stream), p);
+    const cudaStream_t st = as_stream(stream);
+    if (dtype == FP8L_BF16)
+        return head_dim == 128 ? launch_append<FP8L_BF16, 128>(p, grid, st) : launch_append<FP8L_BF16, 64>(p, grid, st);
+    return head_dim == 128 ? launch_append<FP8L_F16, 128>(p, grid, st) : launch_append<FP8L_F16, 64>(p, grid, st);
 }
