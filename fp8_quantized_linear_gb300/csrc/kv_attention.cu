@@ -17,17 +17,17 @@ namespace {
 
 // Workspace: status word, merge counters (zero between calls), partials
 constexpr size_t kAttnCountersOffset = 64;
-constexpr size_t kAttnZeroBytes = 2048;
-constexpr int kDecMaxRows = 16;
-constexpr size_t kDecPartials = static_cast<size_t>(2) * kDecMaxCtas * kDecMaxRows * (128 + 2);
+constexpr size_t kAttnZeroBytes = 16384;
+constexpr size_t kDecPartials = static_cast<size_t>(2) * kDecMaxCtas * 16 * (128 + 2);  // or half the CTAs, 32 rows
 constexpr size_t kProPartials = static_cast<size_t>(2) * kProMaxCtas * kProRows * (128 + 2);
 constexpr size_t kAttnWorkspaceBytes =
     kAttnZeroBytes + sizeof(float) * (kDecPartials > kProPartials ? kDecPartials : kProPartials);
-static_assert(kAttnCountersOffset + 4 * kDecMaxCtas <= kAttnZeroBytes &&
+// decode: per merge level, two pieces of a CTA, two softmax groups (four of half the CTAs)
+static_assert(kAttnCountersOffset + 4 * kDecLevels * 2 * 2 * kDecMaxCtas <= kAttnZeroBytes &&
                   kAttnCountersOffset + 4 * 2 * kProMaxCtas <= kAttnZeroBytes,
               "counters fit");
 
-constexpr int kDecSmemPerCta = 113 * 1024 - 512;  // two CTAs per SM
+constexpr int kSmemPerSm = 227 * 1024;  // what the CTAs of an SM can ask for, each with 1 KB of its own
 
 // Raises a kernel's shared-memory limit once per device.
 template <typename Kernel>
@@ -42,17 +42,20 @@ int allow_smem(Kernel kernel, int smem, std::atomic<unsigned long long> &ready) 
     return FP8L_OK;
 }
 
-template <int QDT, int DIM, int ROWS>
+template <int QDT, int DIM, int GROUPS>
 int launch_decode(AttnParams p, int sms, cudaStream_t stream) {
-    using Sm = DecSmem<QDT, DIM, ROWS>;
-    const int fit = (kDecSmemPerCta - Sm::kFixedBytes) / Sm::kStageBytes;
-    p.stages = fit < kDecMaxStages ? fit : kDecMaxStages;
-    const int smem = p.stages * Sm::kStageBytes + Sm::kFixedBytes;
+    using Sh = DecShape<QDT, DIM, GROUPS>;
+    constexpr int kBudget = kSmemPerSm / Sh::kCtasPerSm - 1024;
+    constexpr int kFit = (kBudget - Sh::kFixedBytes) / Sh::kStageBytes;
+    static_assert(kFit >= 2, "two stages at least");
+    p.stages = kFit < kDecMaxStages ? kFit : kDecMaxStages;
+    const int smem = p.stages * Sh::kStageBytes + Sh::kFixedBytes;
     static std::atomic<unsigned long long> ready{0};
-    auto kernel = kv_attention_decode_kernel<QDT, DIM, ROWS>;
+    auto kernel = kv_attention_decode_kernel<QDT, DIM, GROUPS>;
     if (int st = allow_smem(kernel, smem, ready); st != FP8L_OK) return st;
-    const int ctas = 2 * sms < kDecMaxCtas ? 2 * sms : kDecMaxCtas;
-    return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), kDecThreads, smem, stream, p);
+    const int most = kDecMaxCtas / 2 * Sh::kCtasPerSm, ctas = Sh::kCtasPerSm * sms;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), Sh::kThreads, smem, stream,
+                            p);
 }
 
 template <int QDT, int DIM>
@@ -67,8 +70,9 @@ int launch_prompt(const AttnParams &p, int sms, cudaStream_t stream) {
 
 template <int QDT, int DIM>
 int launch_attention(const AttnParams &p, int64_t rows, int sms, cudaStream_t stream) {
-    if (rows <= 8) return launch_decode<QDT, DIM, 8>(p, sms, stream);
-    if (rows <= 16) return launch_decode<QDT, DIM, 16>(p, sms, stream);
+    if (rows <= 8) return launch_decode<QDT, DIM, 1>(p, sms, stream);
+    if (rows <= 16) return launch_decode<QDT, DIM, 2>(p, sms, stream);
+    if (rows <= 32) return launch_decode<QDT, DIM, 4>(p, sms, stream);
     return launch_prompt<QDT, DIM>(p, sms, stream);
 }
 

@@ -33,10 +33,13 @@
 // leaves its partial (m, l, O) in the workspace and the last CTA to arrive
 // adds the partials in CTA order, so the result does not depend on timing.
 //
-// Roles (192 threads, two CTAs per SM): warps 0-3 softmax and epilogue (warp
-// w owns tensor-memory lanes 32 w ..), warp 4 copies (one untiled bulk copy
-// per page, keys and values; the page's scales by cp.async), warp 5 issues the
-// MMAs, the next tile's scores before this tile's values.
+// Roles: per eight rows a softmax group of four warps (warp w of a group owns
+// tensor-memory lanes 32 w ..: a thread is a key, and in the epilogue a
+// dimension), independent of the other groups; one warp for copies (one
+// untiled bulk copy per page, keys and values; the page's scales by cp.async),
+// which also hands the pieces of the line to the others through shared memory;
+// one warp that issues the MMAs, the next tile's scores before this tile's
+// values.  Two CTAs per SM up to 16 rows, one with 32.
 #pragma once
 
 #include "kv_attention_params.cuh"
@@ -45,119 +48,48 @@ namespace fp8l {
 namespace {
 
 constexpr int kDecTile = 128;      // keys per tile = MMA M
-constexpr int kDecThreads = 192;
 constexpr int kDecMaxStages = 6;
 constexpr int kDecMinTiles = 2;    // tiles per CTA below which fewer CTAs run
 constexpr int kDecMaxCtas = 2 * 160;
+constexpr int kDecFan = 16;        // partials added by one CTA
+constexpr int kDecLevels = 3;      // 16^3 CTAs and more
+constexpr int kDecSegments = 16;   // pieces between the copy warp and the slowest role (stages + 3 at most)
 
-template <int QDT, int ROWS>
+// GROUPS softmax groups of eight rows
+template <int QDT, int DIM, int GROUPS>
 struct DecShape {
+    static constexpr int kRows = 8 * GROUPS;
+    static constexpr int kCtasPerSm = GROUPS <= 2 ? 2 : 1;
+    static constexpr int kThreads = 128 * GROUPS + 64;
     static constexpr int kQParts = QDT == FP8L_BF16 ? 2 : 3;
-    static constexpr int kWParts = 3;
-    static constexpr int kSCols = (ROWS * kQParts + 15) / 16 * 16;
-    static constexpr int kOCols = (ROWS * kWParts + 15) / 16 * 16;
-    // two score buffers, one when they would not fit half the tensor memory
-    static constexpr int kSBufs = 2 * kSCols + kOCols <= 256 ? 2 : 1;
-    static constexpr int kUsedCols = kSBufs * kSCols + kOCols;
-    static constexpr int kTmemCols = kUsedCols <= 64 ? 64 : (kUsedCols <= 128 ? 128 : 256);
-    static_assert(kUsedCols <= 256, "two CTAs share an SM's tensor memory");
-};
-
-// Shared memory after the stages
-template <int QDT, int DIM, int ROWS>
-struct DecSmem {
-    using Sh = DecShape<QDT, ROWS>;
+    static constexpr int kSCols = (kRows * kQParts + 15) / 16 * 16;
+    static constexpr int kOCols = (kRows * 3 + 15) / 16 * 16;
+    static constexpr int kUsedCols = 2 * kSCols + kOCols;
+    static constexpr int kTmemCols = kUsedCols <= 64 ? 64 : (kUsedCols <= 128 ? 128 : (kUsedCols <= 256 ? 256 : 512));
+    static_assert(kUsedCols <= 512 / kCtasPerSm, "the SM's CTAs share its tensor memory");
+    // shared memory after the stages; columns that no row uses hold whatever
+    // is there: their products land in columns that nobody reads
     static constexpr int kStageBytes = 2 * kDecTile * DIM;  // keys, values
-    static constexpr int kQBytes = Sh::kSCols * DIM;        // per buffer
-    static constexpr int kWBytes = kDecTile * Sh::kOCols;   // per buffer
+    static constexpr int kQBytes = kSCols * DIM;            // per buffer
+    static constexpr int kWBytes = kDecTile * kOCols;       // per buffer
     static constexpr int kQOff = 0;
     static constexpr int kWOff = kQOff + 2 * kQBytes;
-    static constexpr int kScaleOff = kWOff + 2 * kWBytes;                  // [stage][2][8] floats
-    static constexpr int kQfOff = kScaleOff + kDecMaxStages * 16 * 4;      // [2][ROWS] floats
-    static constexpr int kRedOff = kQfOff + 2 * ROWS * 4;                  // [4][ROWS] floats
-    static constexpr int kRefOff = kRedOff + 4 * ROWS * 4;                 // [2][ROWS] floats: m, l
-    static constexpr int kBarOff = (kRefOff + 2 * ROWS * 4 + 15) / 16 * 16;
-    static constexpr int kBars = 2 * kDecMaxStages + 4 + 4 + 2 + 1;
+    // the epilogue's rows in float32: in the weights' buffers where one group
+    // owns them (its weights have been multiplied by then)
+    static constexpr int kRowsOff = GROUPS == 1 ? kWOff : kWOff + 2 * kWBytes;
+    static constexpr int kScaleOff = kWOff + 2 * kWBytes + (GROUPS == 1 ? 0 : kRows * DIM * 4);  // [stage][2][8]
+    static constexpr int kQfOff = kScaleOff + kDecMaxStages * 16 * 4;   // [2][kRows] floats
+    static constexpr int kRedOff = kQfOff + 2 * kRows * 4;              // [4][kRows] floats
+    static constexpr int kRefOff = kRedOff + 4 * kRows * 4;             // [kRows] floats
+    static constexpr int kSegOff = (kRefOff + kRows * 4 + 15) / 16 * 16;  // [kDecSegments] DecSegment
+    static constexpr int kBarOff = kSegOff + kDecSegments * 64;
+    static constexpr int kBars = 2 * kDecMaxStages + 10 + kDecSegments + 1;
     static constexpr int kMiscOff = kBarOff + kBars * 8;
-    static constexpr int kFixedBytes = kMiscOff + 64;
+    static constexpr int kFixedBytes = kMiscOff + 16;
+    static_assert(kRows * DIM * 4 <= 2 * kWBytes || GROUPS > 1, "the rows fit the weights' buffers");
     // the M-side read of a 64-dimension V covers 512 bytes past the last stage
     static_assert(2 * kQBytes >= 512, "reads past the last stage stay inside");
 };
-
-__device__ __forceinline__ uint64_t core_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-           (static_cast<uint64_t>(sbo >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
-}
-
-__device__ __forceinline__ void dec_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// COLS columns of this thread's lane
-template <int COLS>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[COLS]) {
-    static_assert(COLS % 16 == 0, "");
-    uint32_t r[COLS / 16][16];
-#pragma unroll
-    for (int c = 0; c < COLS / 16; ++c) tmem_ld_n(taddr + 16 * c, r[c]);
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int c = 0; c < COLS; ++c) v[c] = __uint_as_float(r[c / 16][c % 16]);
-}
-
-// barrier over the 128 softmax threads
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-
-__device__ __forceinline__ bool softmax_any(bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(x ? 1u : 0u)
-        : "memory");
-    return r != 0u;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // E4M3 codes of two values (a in the low byte) and what they leave over,
 // times 16
@@ -174,19 +106,38 @@ __device__ __forceinline__ uint32_t take_part(float &a, float &b) {
     return c;
 }
 
-// Exponent e with 2^7 <= m 2^e < 2^8, at most 120 (rows below 2^-113 lose
-// their last bits) so that 2^-e stays a normal float32; m >= 0
-__device__ __forceinline__ int part_exponent(float m) {
-    return min(134 - static_cast<int>(__float_as_uint(m) >> 23), 120);
+// Sums (or maxima) of eight values over the warp in 3 + 2 steps: each step of
+// the first three halves the values a lane keeps.  Lanes with the same
+// lane / 4 return value number (bits 4, 3, 2 of the lane).
+template <bool MAX>
+__device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
+    auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+    float a[4], b[2];
+    const bool h4 = lane & 16, h3 = lane & 8, h2 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, h4 ? v[i] : v[i + 4], 16);
+        a[i] = op(h4 ? v[i + 4] : v[i], other);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, h3 ? a[i] : a[i + 2], 8);
+        b[i] = op(h3 ? a[i + 2] : a[i], other);
+    }
+    float c = op(h2 ? b[1] : b[0], __shfl_xor_sync(0xFFFFFFFFu, h2 ? b[0] : b[1], 4));
+    c = op(c, __shfl_xor_sync(0xFFFFFFFFu, c, 2));
+    return op(c, __shfl_xor_sync(0xFFFFFFFFu, c, 1));
 }
 
-// A piece of one request and kv head: key tiles [tile, end) of its [begin, stop)
+// A piece of one request and kv head: key tiles [tile, end) of its [begin,
+// stop).  tile == end: there are no more.
 struct DecSegment {
     int r, g;
     int n, row0;        // the request's new tokens, their first row
     int first, keys;    // first visible key, end of the keys
     int tile, end, begin, stop;
-    long long at;       // number of `tile` in the line of tiles
+    int done;           // tiles of the CTA's piece of the line before this one
+    int pad[5];
 };
 
 struct DecRange {
@@ -210,10 +161,10 @@ __device__ __forceinline__ DecRange dec_range(const AttnParams &p, int r) {
     return d;
 }
 
-// Walks the segments of a CTA's piece [at, end) of the line of tiles.
+// Walks the pieces of a CTA's part of the line of tiles.
 struct DecWalk {
-    long long at, left;  // number of the next tile, tiles still to hand out
-    int r, g, offset;    // next tile: offset in request r, head g
+    int done, left;    // tiles handed out, still to hand out
+    int r, g, offset;  // next tile: offset in request r, head g
     __device__ __forceinline__ bool next(const AttnParams &p, DecSegment &s) {
         if (left <= 0) return false;
         DecRange d = dec_range(p, r);
@@ -230,18 +181,17 @@ struct DecWalk {
         s.begin = d.begin;
         s.stop = d.begin + d.tiles;
         s.tile = d.begin + offset;
-        const long long take = min(static_cast<long long>(d.tiles - offset), left);
-        s.end = s.tile + static_cast<int>(take);
-        s.at = at;
-        at += take;
+        const int take = min(d.tiles - offset, left);
+        s.end = s.tile + take;
+        s.done = done;
+        done += take;
         left -= take;
-        offset += static_cast<int>(take);
+        offset += take;
         if (offset == d.tiles) {
             offset = 0;
             if (++g == p.kv_heads) {
                 g = 0;
-                ++r;
-                if (r >= p.requests) left = 0;
+                if (++r >= p.requests) left = 0;
             }
         }
         return true;
@@ -249,6 +199,7 @@ struct DecWalk {
 };
 
 // Exclusive prefix (plus the block's total in *total) of one value per thread
+template <int THREADS>
 __device__ __forceinline__ long long dec_scan(long long v, long long *red, long long *total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     long long inc = v;
@@ -262,7 +213,7 @@ __device__ __forceinline__ long long dec_scan(long long v, long long *red, long 
     __syncthreads();
     long long before = 0, sum = 0;
 #pragma unroll
-    for (int w = 0; w < kDecThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += red[w];
         sum += red[w];
     }
@@ -270,202 +221,166 @@ __device__ __forceinline__ long long dec_scan(long long v, long long *red, long 
     return before + inc - v;
 }
 
-// out and lse of a request and head from its CTAs' partials c0 .. c1, in CTA
-// order: a warp per row, DIM / 32 dimensions per lane, 32 partials' factors
-// at a time in the lanes.
-template <int DIM, int ROWS, typename Partial>
-__device__ __forceinline__ void merge_partials(const AttnParams &p, const DecSegment &s, int rows, int group,
-                                               long long c0, long long c1, const Partial &partial) {
-    constexpr int V = DIM / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = static_cast<int>(c1 - c0 + 1);
-    for (int r = warp; r < rows; r += 4) {
-        float top = -INFINITY;
-        for (int c = lane; c < parts; c += 32) top = fmaxf(top, __ldcg(partial(c0 + c) + ROWS * DIM + 2 * r));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        float sum = 0.0f, acc[V] = {};
-        for (int b = 0; b < parts; b += 32) {
-            float e = 0.0f;
-            if (b + lane < parts) {
-                const float *q = partial(c0 + b + lane) + ROWS * DIM + 2 * r;
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q));
-                e = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
-                sum = fmaf(ml.y, e, sum);
-            }
-            const int n = min(32, parts - b);
-#pragma unroll 8
-            for (int k = 0; k < n; ++k) {
-                const float ek = __shfl_sync(0xFFFFFFFFu, e, k);
-                const float *q = partial(c0 + b + k) + r * DIM + V * lane;
-                if constexpr (V == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(q));
-                    acc[0] = fmaf(v.x, ek, acc[0]);
-                    acc[1] = fmaf(v.y, ek, acc[1]);
-                    acc[2] = fmaf(v.z, ek, acc[2]);
-                    acc[3] = fmaf(v.w, ek, acc[3]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(q));
-                    acc[0] = fmaf(v.x, ek, acc[0]);
-                    acc[1] = fmaf(v.y, ek, acc[1]);
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const int token = s.row0 + r / group, head = s.g * group + r % group;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = sum > 0.0f ? acc[i] / sum : 0.0f;
-        attn_store<V>(p, token, head, DIM, V * lane, acc);
-        if (lane == 0 && p.lse != nullptr) attn_store_lse(p, token, head, top, sum);
-    }
-}
-
-template <int QDT, int DIM, int ROWS>
-__global__ void __launch_bounds__(kDecThreads, 2) kv_attention_decode_kernel(const AttnParams p) {
-    using Sh = DecShape<QDT, ROWS>;
-    using Sm = DecSmem<QDT, DIM, ROWS>;
+template <int QDT, int DIM, int GROUPS>
+__global__ void __launch_bounds__(DecShape<QDT, DIM, GROUPS>::kThreads, DecShape<QDT, DIM, GROUPS>::kCtasPerSm)
+kv_attention_decode_kernel(const AttnParams p) {
+    using Sh = DecShape<QDT, DIM, GROUPS>;
+    constexpr int ROWS = Sh::kRows;
     extern __shared__ __align__(128) uint8_t dec_smem[];
-    __shared__ long long scan_red[kDecThreads / 32];
-    __shared__ long long start_left;
-    __shared__ int start_r, start_g, start_offset, merge_now;
+    __shared__ long long scan_red[Sh::kThreads / 32];
+    __shared__ int start_r, start_g, start_offset, merge_now[GROUPS];
     const uint32_t sbase = smem_u32(dec_smem);
     const int S = p.stages;
-    const uint32_t fixed = sbase + static_cast<uint32_t>(S) * Sm::kStageBytes;
-    uint8_t *fixed_ptr = dec_smem + static_cast<size_t>(S) * Sm::kStageBytes;
-    const uint32_t bars = fixed + Sm::kBarOff;
-    auto full_bar = [&](int s) { return bars + 8u * s; };
-    auto empty_bar = [&](int s) { return bars + 8u * (kDecMaxStages + s); };
-    auto sfull_bar = [&](int b) { return bars + 8u * (2 * kDecMaxStages + b); };
-    auto sempty_bar = [&](int b) { return bars + 8u * (2 * kDecMaxStages + 2 + b); };
-    auto wfull_bar = [&](int b) { return bars + 8u * (2 * kDecMaxStages + 4 + b); };
-    auto wfree_bar = [&](int b) { return bars + 8u * (2 * kDecMaxStages + 6 + b); };
-    auto qfull_bar = [&](int b) { return bars + 8u * (2 * kDecMaxStages + 8 + b); };
-    const uint32_t done_bar = bars + 8u * (2 * kDecMaxStages + 10);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fixed_ptr + Sm::kMiscOff);
+    const uint32_t fixed = sbase + static_cast<uint32_t>(S) * Sh::kStageBytes;
+    uint8_t *fixed_ptr = dec_smem + static_cast<size_t>(S) * Sh::kStageBytes;
+    const uint32_t full = fixed + Sh::kBarOff, empty = full + 8 * kDecMaxStages;
+    const uint32_t sfull = empty + 8 * kDecMaxStages, sempty = sfull + 16, wfull = sempty + 16, wfree = wfull + 16;
+    const uint32_t qfull = wfree + 16, segfull = qfull + 16, done_bar = segfull + 8 * kDecSegments;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fixed_ptr + Sh::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kCopyWarp = 4 * GROUPS, kMmaWarp = kCopyWarp + 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1 + 32);  // expected bytes, and the lanes' scale copies
-            mbar_init(empty_bar(s), 1);
+            mbar_init(full + 8 * s, 1 + 32);  // expected bytes, and the lanes' scale copies
+            mbar_init(empty + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(sfull_bar(b), 1);
-            mbar_init(sempty_bar(b), 128);
-            mbar_init(wfull_bar(b), 128);
-            mbar_init(wfree_bar(b), 1);
-            mbar_init(qfull_bar(b), 128);
+            mbar_init(sfull + 8 * b, 1);
+            mbar_init(sempty + 8 * b, 128 * GROUPS);
+            mbar_init(wfull + 8 * b, 128 * GROUPS);
+            mbar_init(wfree + 8 * b, 1);
+            mbar_init(qfull + 8 * b, 128 * GROUPS);
         }
+        for (int s = 0; s < kDecSegments; ++s) mbar_init(segfull + 8 * s, 1);
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    // columns that no row uses stay zero: queries and weights
-    for (int i = static_cast<int>(threadIdx.x); i < (2 * Sm::kQBytes + 2 * Sm::kWBytes) / 16; i += kDecThreads)
-        reinterpret_cast<uint4 *>(fixed_ptr)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(tmem_slot)),
                      "r"(Sh::kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     grid_dependency_sync();
 
-    // the line of tiles, and this CTA's piece of it
-    long long total = 0;
-    {
-        long long mine = 0;
-        for (int r = static_cast<int>(threadIdx.x); r < p.requests; r += kDecThreads)
-            mine += static_cast<long long>(dec_range(p, r).tiles) * p.kv_heads;
-        dec_scan(mine, scan_red, &total);
+    // the line of tiles, and this CTA's piece of it: requests in rounds of
+    // one per thread, the first round's values kept for the second reading
+    const int mine0 = static_cast<int>(threadIdx.x) < p.requests ? dec_range(p, threadIdx.x).tiles : 0;
+    long long total = 0, before0 = 0;
+    for (int r0 = 0; r0 < p.requests; r0 += Sh::kThreads) {
+        const int r = r0 + static_cast<int>(threadIdx.x);
+        const int tiles = r0 == 0 ? mine0 : (r < p.requests ? dec_range(p, r).tiles : 0);
+        long long sum;
+        const long long before = dec_scan<Sh::kThreads>(static_cast<long long>(tiles) * p.kv_heads, scan_red, &sum);
+        if (r0 == 0) before0 = before;
+        total += sum;
     }
     // fewer CTAs when each would get less than kDecMinTiles
     const long long ctas = max(min(static_cast<long long>(gridDim.x), total / kDecMinTiles),
                                min(static_cast<long long>(gridDim.x), min(total, 1LL)));
     const long long cta = static_cast<long long>(blockIdx.x);
     const bool idle = cta >= ctas;
-    const long long w0 = idle ? 0 : total * cta / ctas, w1 = idle ? 0 : total * (cta + 1) / ctas;
+    const long long w0 = idle ? 0 : piece_begin(total, cta, ctas), w1 = idle ? 0 : piece_begin(total, cta + 1, ctas);
     if (!idle) {
         long long carry = 0;
-        for (int r0 = 0; r0 < p.requests; r0 += kDecThreads) {
+        for (int r0 = 0; r0 < p.requests; r0 += Sh::kThreads) {
             const int r = r0 + static_cast<int>(threadIdx.x);
-            const int tiles = r < p.requests ? dec_range(p, r).tiles : 0;
-            long long sum;
+            const int tiles = r0 == 0 ? mine0 : (r < p.requests ? dec_range(p, r).tiles : 0);
             const long long n = static_cast<long long>(tiles) * p.kv_heads;
-            const long long before = carry + dec_scan(n, scan_red, &sum);
+            long long sum = 0, before = before0;
+            if (p.requests > Sh::kThreads) before = carry + dec_scan<Sh::kThreads>(n, scan_red, &sum);
             if (n > 0 && before <= w0 && w0 < before + n) {
                 start_r = r;
-                start_g = static_cast<int>((w0 - before) / tiles);
-                start_offset = static_cast<int>((w0 - before) % tiles);
-                start_left = w1 - w0;
+                const unsigned rest = static_cast<unsigned>(w0 - before);  // below tiles * kv_heads
+                start_g = static_cast<int>(rest / static_cast<unsigned>(tiles));
+                start_offset = static_cast<int>(rest % static_cast<unsigned>(tiles));
             }
             carry += sum;
             if (carry > w0) break;
         }
-    } else if (threadIdx.x == 0) {
-        start_r = start_g = start_offset = 0;
-        start_left = 0;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t o_tmem = tmem + Sh::kSBufs * Sh::kSCols;
-    DecWalk walk{w0, start_left, start_r, start_g, start_offset};
+    const uint32_t o_col = 2 * Sh::kSCols;
     const int P = 1 << p.page_shift;
     const int group = p.q_heads / p.kv_heads;
+    DecSegment *segs = reinterpret_cast<DecSegment *>(fixed_ptr + Sh::kSegOff);
+    // piece number n, or nullptr after the last (or a time-out)
+    auto segment_at = [&](int n) -> const DecSegment * {
+        if (!kv_wait(segfull + 8 * (n & (kDecSegments - 1)), (n / kDecSegments) & 1u, abort_flag, p.status,
+                     p.wait_cycles))
+            return nullptr;
+        const DecSegment *s = segs + (n & (kDecSegments - 1));
+        return s->tile < s->end ? s : nullptr;
+    };
 
-    if (warp == 4) {
+    if (warp == kCopyWarp) {
         // ---------------------------------------------------------- copies
-        int stage = 0;
+        int stage = 0, published = 0;
         uint32_t phase = 0, issued = 0, issued_parity = 0;
         const int per_tile = kDecTile >> p.page_shift;  // pages of a tile, at most 8
-        DecSegment s;
-        bool ok = true;
-        while (ok && walk.next(p, s)) {
+        DecWalk walk{0, static_cast<int>(w1 - w0), idle ? 0 : start_r, idle ? 0 : start_g, idle ? 0 : start_offset};
+        bool ok = true, more = true;
+        // hands out the next piece (or the end)
+        auto publish = [&](DecSegment &s) {
+            more = more && walk.next(p, s);
+            if (!more) s.tile = s.end = 0;
+            if (lane == 0) {
+                segs[published & (kDecSegments - 1)] = s;
+                mbar_arrive(segfull + 8 * (published & (kDecSegments - 1)));
+            }
+            __syncwarp();
+            ++published;
+            return more;
+        };
+        DecSegment s, ahead;
+        bool have = publish(s);
+        while (ok && have) {
+            // one piece ahead: its queries are prepared under this one's tiles
+            const bool have_ahead = publish(ahead);
             const int32_t *table = p.block_table + static_cast<int64_t>(s.r) * p.table_width;
             // lanes 0-7 keys of page lane, lanes 8-15 values of page lane - 8
             const int i = lane & 7;
-            auto block_of = [&](int tile) { return tile * per_tile + i; };
             auto wanted = [&](int tile) {
-                const int b = block_of(tile);
-                return lane < 16 && i < per_tile && (static_cast<int64_t>(b) << p.page_shift) < s.keys &&
-                       (static_cast<int64_t>(b + 1) << p.page_shift) > s.first;
+                const int64_t b = static_cast<int64_t>(tile) * per_tile + i;
+                return lane < 16 && i < per_tile && (b << p.page_shift) < s.keys &&
+                       ((b + 1) << p.page_shift) > s.first;
             };
-            int page = wanted(s.tile) ? table[block_of(s.tile)] : 0;
+            int page = wanted(s.tile) ? table[s.tile * per_tile + i] : 0;
             for (int tile = s.tile; tile < s.end; ++tile) {
                 const bool mine = wanted(tile);
                 const int64_t ph = static_cast<int64_t>(min(max(page, 0), p.num_pages - 1)) * p.kv_heads + s.g;
                 // the next tile's pages, while this one waits for its stage
-                if (tile + 1 < s.end) page = wanted(tile + 1) ? table[block_of(tile + 1)] : 0;
+                if (tile + 1 < s.end) page = wanted(tile + 1) ? table[(tile + 1) * per_tile + i] : 0;
                 uint32_t bytes = 0;
                 if (mine) {
-                    const int in_page = min(s.keys - (block_of(tile) << p.page_shift), P);
+                    const int in_page = min(s.keys - ((tile * per_tile + i) << p.page_shift), P);
                     bytes = static_cast<uint32_t>((in_page + 7) / 8 * 8 * DIM);
                 }
-                uint32_t sum = bytes;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                ok = mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.wait_cycles);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, bytes);
+                ok = __all_sync(0xFFFFFFFFu,
+                                kv_wait(empty + 8 * stage, phase ^ 1u, abort_flag, p.status, p.wait_cycles));
                 if (!ok) break;
-                const uint32_t dst = sbase + static_cast<uint32_t>(stage) * Sm::kStageBytes +
+                const uint32_t dst = sbase + static_cast<uint32_t>(stage) * Sh::kStageBytes +
                                      (lane >= 8 ? kDecTile * DIM : 0) + static_cast<uint32_t>(i * P * DIM);
-                if (lane == 0) mbar_expect_tx(full_bar(stage), sum);
+                if (lane == 0) mbar_expect_tx(full + 8 * stage, sum);
                 __syncwarp();
                 if (mine) {
-                    bulk_copy(dst, (lane < 8 ? p.k_cache : p.v_cache) + ph * P * DIM, bytes, full_bar(stage));
+                    bulk_copy(dst, (lane < 8 ? p.k_cache : p.v_cache) + ph * P * DIM, bytes, full + 8 * stage);
                     const float *scale = (lane < 8 ? p.k_scale : p.v_scale) + ph;
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                                     fixed + Sm::kScaleOff + static_cast<uint32_t>((stage * 16 + lane) * 4)),
+                                     fixed + Sh::kScaleOff + static_cast<uint32_t>((stage * 16 + lane) * 4)),
                                  "l"(scale)
                                  : "memory");
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full_bar(stage))
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full + 8 * stage)
                              : "memory");
                 issued |= 1u << stage;
                 issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -474,90 +389,101 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv_attention_decode_kernel(con
                     phase ^= 1u;
                 }
             }
+            s = ahead;
+            have = have_ahead;
         }
         // every copy lands before the CTA exits
-        for (int s2 = 0; s2 < S; ++s2)
-            if (issued & (1u << s2)) mbar_wait_drain(full_bar(s2), (issued_parity >> s2) & 1u, p.status);
-    } else if (warp == 5) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int x = 0; x < S; ++x)
+            if (issued & (1u << x)) kv_drain(full + 8 * x, (issued_parity >> x) & 1u, p.status);
+    } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMAs
-        if (lane == 0) {
-            const uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(Sh::kSCols >> 3) << 17) | (8u << 24);
-            const uint32_t idesc_o = (1u << 4) | (1u << 15) | (1u << 16) |
-                                     (static_cast<uint32_t>(Sh::kOCols >> 3) << 17) | (8u << 24);
-            bool ok = true;
-            if (p.stall & kStallMma) ok = mbar_wait(done_bar, 0, abort_flag, p.status, p.wait_cycles);
-            int stage = 0, prev_stage = 0, i = 0, segment = 0;
-            uint32_t phase = 0;
-            bool prev_first = false;
-            auto values = [&](int k) {  // O += V^T W^T of tile number k
-                const int b = k & 1;
-                if (!mbar_wait_fast(wfull_bar(b), (k >> 1) & 1u, abort_flag, p.status, p.wait_cycles)) return false;
-                tc_fence_after();
-                const uint32_t v = sbase + static_cast<uint32_t>(prev_stage) * Sm::kStageBytes + kDecTile * DIM;
-                const uint32_t w = fixed + Sm::kWOff + static_cast<uint32_t>(b) * Sm::kWBytes;
+        const bool leader = elect_one();
+        const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(Sh::kSCols >> 3) << 17) | (8u << 24);
+        const uint32_t idesc_o = (1u << 4) | (1u << 15) | (1u << 16) |
+                                 (static_cast<uint32_t>(Sh::kOCols >> 3) << 17) | (8u << 24);
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, kv_wait(bar, parity & 1u, abort_flag, p.status, p.wait_cycles));
+        };
+        bool ok = true;
+        if (p.stall & kStallMma) ok = wait(done_bar, 0);
+        int stage = 0, prev_stage = 0, i = 0, segment = 0;
+        uint32_t phase = 0;
+        bool prev_first = false;
+        auto values = [&](int k) {  // O += V^T W^T of tile number k
+            const int b = k & 1;
+            if (!wait(wfull + 8 * b, k >> 1)) return false;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t v = desc_lo(sbase + static_cast<uint32_t>(prev_stage) * Sh::kStageBytes + kDecTile * DIM,
+                                           8 * DIM);
+                const uint32_t w = desc_lo(fixed + Sh::kWOff + static_cast<uint32_t>(b) * Sh::kWBytes, 8 * Sh::kOCols);
 #pragma unroll
                 for (int j = 0; j < kDecTile / 32; ++j)
-                    dec_mma(o_tmem, core_desc(v + 32u * DIM * j, 8 * DIM, 128),
-                            core_desc(w + 32u * Sh::kOCols * j, 8 * Sh::kOCols, 128), idesc_o,
-                            (prev_first && j == 0) ? 0u : 1u);
-                mma_commit(wfree_bar(b));
-                mma_commit(empty_bar(prev_stage));
-                return true;
-            };
-            DecSegment s;
-            while (ok && walk.next(p, s)) {
-                const int qb = segment & 1;
-                ok = mbar_wait_fast(qfull_bar(qb), (segment >> 1) & 1u, abort_flag, p.status, p.wait_cycles);
-                for (int tile = s.tile; ok && tile < s.end; ++tile, ++i) {
-                    const int b = Sh::kSBufs == 2 ? (i & 1) : 0;
-                    const uint32_t use = static_cast<uint32_t>(Sh::kSBufs == 2 ? i >> 1 : i);
-                    ok = mbar_wait_fast(full_bar(stage), phase, abort_flag, p.status, p.wait_cycles) &&
-                         mbar_wait_fast(sempty_bar(b), (use & 1u) ^ 1u, abort_flag, p.status, p.wait_cycles);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t k = sbase + static_cast<uint32_t>(stage) * Sm::kStageBytes;
-                    const uint32_t q = fixed + Sm::kQOff + static_cast<uint32_t>(qb) * Sm::kQBytes;
+                    mma_f8_desc(tmem_u + o_col, v + 2 * DIM * j, desc_hi(128), w + 2 * Sh::kOCols * j, desc_hi(128),
+                                idesc_o, (prev_first && j == 0) ? 0u : 1u);
+                mma_commit(wfree + 8 * b);
+                mma_commit(empty + 8 * prev_stage);
+            }
+            return true;
+        };
+        while (ok) {
+            const DecSegment *s = segment_at(segment);
+            if (__any_sync(0xFFFFFFFFu, s == nullptr)) break;
+            const int qb = segment & 1, tiles = s->end - s->tile;
+            ok = wait(qfull + 8 * qb, segment >> 1);
+            for (int tile = 0; ok && tile < tiles; ++tile, ++i) {
+                const int b = i & 1;
+                ok = wait(full + 8 * stage, phase) && wait(sempty + 8 * b, (i >> 1) + 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t k = desc_lo(sbase + static_cast<uint32_t>(stage) * Sh::kStageBytes, 128);
+                    const uint32_t q = desc_lo(fixed + Sh::kQOff + static_cast<uint32_t>(qb) * Sh::kQBytes, 128);
 #pragma unroll
                     for (int j = 0; j < DIM / 32; ++j)
-                        dec_mma(tmem + static_cast<uint32_t>(b * Sh::kSCols), core_desc(k + 256u * j, 128, 8 * DIM),
-                                core_desc(q + 256u * j, 128, 8 * DIM), idesc_s, j == 0 ? 0u : 1u);
-                    mma_commit(sfull_bar(b));
-                    if (i > 0) ok = values(i - 1);
-                    prev_stage = stage;
-                    prev_first = tile == s.tile;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                        mma_f8_desc(tmem_u + static_cast<uint32_t>(b * Sh::kSCols), k + 16 * j, desc_hi(8 * DIM),
+                                    q + 16 * j, desc_hi(8 * DIM), idesc_s, j == 0 ? 0u : 1u);
+                    mma_commit(sfull + 8 * b);
                 }
-                ++segment;
+                if (i > 0) ok = values(i - 1);
+                prev_stage = stage;
+                prev_first = tile == 0;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            if (ok && i > 0) values(i - 1);
-            mma_commit(done_bar);
+            ++segment;
         }
+        if (ok && i > 0) values(i - 1);
+        if (leader) mma_commit(done_bar);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax
-        const int tid = static_cast<int>(threadIdx.x);
-        const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-        float *qf = reinterpret_cast<float *>(fixed_ptr + Sm::kQfOff);
-        float *red = reinterpret_cast<float *>(fixed_ptr + Sm::kRedOff);
-        float *ref = reinterpret_cast<float *>(fixed_ptr + Sm::kRefOff);
-        const float *scales = reinterpret_cast<const float *>(fixed_ptr + Sm::kScaleOff);
+        const int grp = warp >> 2, bar_id = 1 + grp, tid = static_cast<int>(threadIdx.x) & 127;
+        const int row_base = 8 * grp;  // the group's rows of the unit
+        const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_tmem = tmem + lane_addr + row_base, o_tmem = tmem + lane_addr + o_col + row_base;
+        float *qf = reinterpret_cast<float *>(fixed_ptr + Sh::kQfOff) + row_base;
+        float *red = reinterpret_cast<float *>(fixed_ptr + Sh::kRedOff) + row_base;
+        float *ref = reinterpret_cast<float *>(fixed_ptr + Sh::kRefOff) + row_base;
+        const float *scales = reinterpret_cast<const float *>(fixed_ptr + Sh::kScaleOff);
         bool ok = true;
 
-        // The segment's queries as E4M3 parts in buffer b, and the factor of
+        // The piece's queries as E4M3 parts in buffer b, and the factor of
         // each row's scores: LANES lanes hold a row, eight dimensions each.
         auto load_queries = [&](const DecSegment &s, int b) {
-            constexpr int LANES = DIM / 8, AT_ONCE = 128 / LANES;
-            const int l = tid % LANES;
-            const int rows = min(s.n * group, ROWS);
-            for (int row = tid / LANES; row < ROWS; row += AT_ONCE) {
+            constexpr int LANES = DIM / 8;
+            const int l = tid % LANES, row = tid / LANES;
+            if (row < 8) {  // (whole warps)
+                const int unit_row = row_base + row, token = unit_row / group;
                 float x[8] = {};
-                if (row < rows) {
-                    const int token = s.row0 + row / group, head = s.g * group + row % group;
+                if (token < s.n) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(
-                        p.q + static_cast<int64_t>(token) * p.q_stride + head * DIM + 8 * l);
+                        p.q + static_cast<int64_t>(s.row0 + token) * p.q_stride +
+                        (s.g * group + unit_row - token * group) * DIM + 8 * l);
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -569,88 +495,89 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv_attention_decode_kernel(con
                 float m = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-                // (every lane of the warp is in the loop: ROWS is a multiple
-                // of a warp's rows, or the row is a repeat of none)
 #pragma unroll
                 for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o, LANES));
                 const int e = part_exponent(m);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] *= up;
-                if (l == 0) qf[b * ROWS + row] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                if (l == 0)
+                    qf[b * ROWS + row] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
                 for (int part = 0; part < Sh::kQParts; ++part) {
                     uint32_t c[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) c[i] = take_part(x[2 * i], x[2 * i + 1]);
-                    const int col = part * ROWS + row;
-                    uint8_t *dst = fixed_ptr + Sm::kQOff + b * Sm::kQBytes + (col >> 3) * 8 * DIM + (l >> 1) * 128 +
+                    const int col = part * ROWS + unit_row;
+                    uint8_t *dst = fixed_ptr + Sh::kQOff + b * Sh::kQBytes + (col >> 3) * 8 * DIM + (l >> 1) * 128 +
                                    (col & 7) * 16 + 8 * (l & 1);
                     *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(qfull_bar(b));
+            mbar_arrive(qfull + 8 * b);
         };
 
         int stage = 0, i = 0, segment = 0;
         uint32_t phase = 0;
-        DecSegment s, next;
-        bool more = walk.next(p, s);
-        if (more) load_queries(s, 0);
+        const DecSegment *s = segment_at(0);
+        // one answer for the group's threads, whose barriers need all of them
+        // (a wait can give up in one thread and not in another)
+        bool more = !group_any(bar_id, s == nullptr);
+        if (more) load_queries(*s, 0);
         while (more) {
             const int qb = segment & 1;
-            const int rows = min(s.n * group, ROWS);
-            float l[ROWS], m[ROWS], f[ROWS];
-            softmax_sync();  // the row factors of this segment are written
+            const int begin = s->tile, end = s->end, first = s->first, keys = s->keys;
+            const int pos0 = keys - s->n;  // position of the first row's token
+            float l[8], m[8];
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
+            for (int r = 0; r < 8; ++r) {
                 l[r] = 0.0f;
                 m[r] = -INFINITY;
-                f[r] = qf[qb * ROWS + r];
             }
-            bool have_next = false;
-            for (int tile = s.tile; tile < s.end; ++tile, ++i) {
-                const int sb = Sh::kSBufs == 2 ? (i & 1) : 0;
-                const uint32_t use = static_cast<uint32_t>(Sh::kSBufs == 2 ? i >> 1 : i);
-                const int wb = i & 1;
+            group_sync(bar_id);  // the row factors of this piece are written
+            const DecSegment *next = nullptr;
+            for (int tile = begin; tile < end; ++tile, ++i) {
+                const int b = i & 1;
                 const int key = tile * kDecTile + tid;
                 // scales and codes of the stage, then the scores
-                ok = ok && mbar_wait_fast(full_bar(stage), phase, abort_flag, p.status, p.wait_cycles);
+                ok = ok && kv_wait(full + 8 * stage, phase, abort_flag, p.status, p.wait_cycles);
                 const int pg = tid >> p.page_shift;
-                const bool exists = key >= s.first && key < s.keys;
+                const bool exists = key >= first && key < keys;
                 const float ks = exists ? scales[stage * 16 + pg] : 0.0f;
                 const float vs = exists ? scales[stage * 16 + 8 + pg] : 1.0f;
                 const float lv = __log2f(vs), rv = __frcp_rn(vs);
-                ok = ok && mbar_wait_fast(sfull_bar(sb), use & 1u, abort_flag, p.status, p.wait_cycles);
+                const float4 f0 = *reinterpret_cast<const float4 *>(qf + qb * ROWS);
+                const float4 f1 = *reinterpret_cast<const float4 *>(qf + qb * ROWS + 4);
+                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                ok = ok && kv_wait(sfull + 8 * b, (i >> 1) & 1u, abort_flag, p.status, p.wait_cycles);
                 tc_fence_after();
-                float t[ROWS];
+                float t[8];
                 {
-                    float c[Sh::kSCols];
-                    tmem_ld_cols<Sh::kSCols>(tmem + lane_addr + static_cast<uint32_t>(sb * Sh::kSCols), c);
-                    tc_fence_before();
-                    mbar_arrive(sempty_bar(sb));
+                    uint32_t c[Sh::kQParts][8];
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
-                        float x = c[r];
-                        if (Sh::kQParts == 3)
-                            x = fmaf(fmaf(c[2 * ROWS + r], 0.0625f, c[ROWS + r]), 0.0625f, x);
-                        else
-                            x = fmaf(c[ROWS + r], 0.0625f, x);
+                    for (int part = 0; part < Sh::kQParts; ++part)
+                        tmem_ld8(s_tmem + static_cast<uint32_t>(b * Sh::kSCols + part * ROWS), c[part]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    mbar_arrive(sempty + 8 * b);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        float x = __uint_as_float(c[Sh::kQParts - 1][r]);
+#pragma unroll
+                        for (int part = Sh::kQParts - 2; part >= 0; --part)
+                            x = fmaf(x, 0.0625f, __uint_as_float(c[part][r]));
                         t[r] = fmaf(x, f[r] * ks, lv);
                     }
                 }
                 // rows see keys up to their position; tiles below every row's
                 // need no test (nor above the last row's window)
-                const int pos0 = s.keys - s.n;
-                const bool plain = tile * kDecTile + kDecTile - 1 <= pos0 && tile * kDecTile >= s.first &&
-                                   (p.window == 0 || tile * kDecTile > s.keys - 1 - p.window);
-                if (!plain) {
-                    int pos = pos0, j = 0;
+                if (!(tile * kDecTile + kDecTile - 1 <= pos0 && tile * kDecTile >= first &&
+                      (p.window == 0 || tile * kDecTile > keys - 1 - p.window))) {
+                    int pos = pos0 + row_base / group, j = row_base % group;
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
-                        const bool seen = exists && key <= pos && (p.window == 0 || key > pos - p.window);
-                        if (!seen) t[r] = -INFINITY;
+                    for (int r = 0; r < 8; ++r) {
+                        if (!(exists && key <= pos && (p.window == 0 || key > pos - p.window))) t[r] = -INFINITY;
                         if (++j == group) {
                             j = 0;
                             ++pos;
@@ -659,173 +586,219 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv_attention_decode_kernel(con
                 }
                 bool past = false;
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r) past |= r < rows && t[r] > m[r] + 1.0f;
-                if (softmax_any(past)) {
+                for (int r = 0; r < 8; ++r) past |= t[r] > m[r] + 1.0f;
+                if (group_any(bar_id, past)) {
                     // new references: the tile's maxima
+                    const float top = reduce8<true>(t, lane);
+                    if ((lane & 3) == 0) red[(warp & 3) * ROWS + (lane >> 2)] = top;
+                    group_sync(bar_id);
+                    float keep[8];
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
-                        float x = t[r];
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-                        if (lane == 0) red[warp * ROWS + r] = x;
-                    }
-                    softmax_sync();
-                    float keep[ROWS];
-#pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
+                    for (int r = 0; r < 8; ++r) {
                         const float x = fmaxf(fmaxf(red[r], red[ROWS + r]), fmaxf(red[2 * ROWS + r], red[3 * ROWS + r]));
                         const float to = fmaxf(m[r], x);
                         keep[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - to);
                         l[r] *= keep[r];
                         m[r] = to;
                     }
-                    if (tile != s.tile) {
+                    if (tile != begin) {
                         // the accumulator holds tiles up to the previous one
-                        ok = ok && mbar_wait_fast(wfree_bar((i - 1) & 1), ((i - 1) >> 1) & 1u, abort_flag, p.status,
-                                                  p.wait_cycles);
+                        ok = ok && kv_wait(wfree + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1u, abort_flag, p.status,
+                                           p.wait_cycles);
                         tc_fence_after();
-                        float o[Sh::kOCols];
-                        tmem_ld_cols<Sh::kOCols>(o_tmem + lane_addr, o);
-                        uint32_t u[Sh::kOCols / 16][16];
+#pragma unroll 1
+                        for (int part = 0; part < 3; ++part) {
+                            uint32_t o[8];
+                            tmem_ld8(o_tmem + static_cast<uint32_t>(part * ROWS), o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < Sh::kOCols; ++c)
-                            u[c / 16][c % 16] = __float_as_uint(c < 3 * ROWS ? o[c] * keep[c % ROWS] : 0.0f);
-#pragma unroll
-                        for (int c = 0; c < Sh::kOCols / 16; ++c) tmem_st_n(o_tmem + lane_addr + 16 * c, u[c]);
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                            for (int r = 0; r < 8; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * keep[r]);
+                            tmem_st8(o_tmem + static_cast<uint32_t>(part * ROWS), o);
+                        }
+                        tmem_wait_st();
                         tc_fence_before();
                     }
                 }
                 // weights, their sums, and their parts
-                float w[ROWS];
+                float w[8];
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r) {
+                for (int r = 0; r < 8; ++r) {
                     w[r] = ex2(t[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
                     l[r] = fmaf(w[r], rv, l[r]);
                     w[r] *= 128.0f;
                 }
-                ok = ok && mbar_wait_fast(wfree_bar(wb), ((i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.wait_cycles);
-                uint8_t *wrow = fixed_ptr + Sm::kWOff + wb * Sm::kWBytes + (tid >> 3) * 8 * Sh::kOCols + (tid & 7) * 16;
+                ok = ok && kv_wait(wfree + 8 * b, ((i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.wait_cycles);
+                uint8_t *wrow = fixed_ptr + Sh::kWOff + b * Sh::kWBytes + (tid >> 3) * 8 * Sh::kOCols + (tid & 7) * 16;
 #pragma unroll
                 for (int part = 0; part < 3; ++part) {
+                    uint32_t c[4];
 #pragma unroll
-                    for (int r = 0; r < ROWS; r += 4) {
-                        const uint32_t lo = take_part(w[r], w[r + 1]), hi = take_part(w[r + 2], w[r + 3]);
-                        const int col = part * ROWS + r;
-                        *reinterpret_cast<uint32_t *>(wrow + (col >> 4) * 128 + (col & 15)) = lo | (hi << 16);
-                    }
+                    for (int r = 0; r < 4; ++r) c[r] = take_part(w[2 * r], w[2 * r + 1]);
+                    const int col = part * ROWS + row_base;
+                    *reinterpret_cast<uint2 *>(wrow + (col >> 4) * 128 + (col & 15)) =
+                        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
                 }
-                if (!exists) {
+                if (grp == 0 && !exists) {
                     // keys that are not there: whatever the stage holds
                     // (NaN codes too) must not meet their zero weights
-                    uint8_t *v = dec_smem + static_cast<size_t>(stage) * Sm::kStageBytes + kDecTile * DIM +
+                    uint8_t *v = dec_smem + static_cast<size_t>(stage) * Sh::kStageBytes + kDecTile * DIM +
                                  (tid >> 3) * 8 * DIM + (tid & 7) * 16;
 #pragma unroll
                     for (int c = 0; c < DIM / 16; ++c)
                         *reinterpret_cast<uint4 *>(v + c * 128) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(wfull_bar(wb));
+                mbar_arrive(wfull + 8 * b);
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1u;
                 }
-                if (tile == s.tile) {
-                    // the next segment's queries, so that its scores need not
+                if (tile == begin) {
+                    // the next piece's queries, so that its scores need not
                     // wait for this one's epilogue
-                    have_next = walk.next(p, next);
-                    if (have_next) load_queries(next, qb ^ 1);
+                    next = segment_at(segment + 1);
+                    if (group_any(bar_id, next == nullptr)) next = nullptr;
+                    if (next != nullptr) load_queries(*next, qb ^ 1);
                 }
             }
             ++segment;
 
             // ------------------------------------------------------ epilogue
-            ok = ok && mbar_wait_fast(wfree_bar((i - 1) & 1), ((i - 1) >> 1) & 1u, abort_flag, p.status, p.wait_cycles);
+            // sums over the keys, and the accumulator turned from a dimension
+            // per thread into rows of shared memory
+            const float sum = reduce8<false>(l, lane);
+            if ((lane & 3) == 0) red[(warp & 3) * ROWS + (lane >> 2)] = sum;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (tid == r) ref[r] = m[r];
+            ok = ok && kv_wait(wfree + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1u, abort_flag, p.status, p.wait_cycles);
             tc_fence_after();
+            float *rows = reinterpret_cast<float *>(fixed_ptr + Sh::kRowsOff) + row_base * DIM;
+            {
+                uint32_t o[3][8];
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                float x = l[r];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-                l[r] = x;
-            }
-            softmax_sync();  // the maxima in `red` have been read
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                if (lane == 0) red[warp * ROWS + r] = l[r];
-            softmax_sync();
-            float o[Sh::kOCols];
-            tmem_ld_cols<Sh::kOCols>(o_tmem + lane_addr, o);
-            tc_fence_before();
-            const bool whole = s.tile == s.begin && s.end == s.stop;
-            float *part = nullptr;
-            long long c0 = 0, c1 = 0, seg0 = 0;
-            if (!whole) {
-                // the CTAs that share this request and head
-                seg0 = s.at - (s.tile - s.begin);
-                const long long seg1 = seg0 + (s.stop - s.begin);
-                c0 = ((seg0 + 1) * ctas - 1) / total;
-                c1 = (seg1 * ctas - 1) / total;
-                const int slot = s.tile != s.begin || seg0 == w0 ? 0 : 1;
-                part = p.partials + (cta * 2 + slot) * static_cast<long long>(ROWS * (DIM + 2));
-            }
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                l[r] = (red[r] + red[ROWS + r]) + (red[2 * ROWS + r] + red[3 * ROWS + r]);
-                o[r] = fmaf(fmaf(o[2 * ROWS + r], 0.0625f, o[ROWS + r]), 0.0625f, o[r]) * (1.0f / 128.0f);
-            }
-            if (whole) {
+                for (int part = 0; part < 3; ++part) tmem_ld8(o_tmem + static_cast<uint32_t>(part * ROWS), o[part]);
+                tmem_wait_ld();
+                tc_fence_before();
                 if (tid < DIM) {
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
-                        const float x[1] = {l[r] > 0.0f ? o[r] / l[r] : 0.0f};
-                        if (r < rows) attn_store<1>(p, s.row0 + r / group, s.g * group + r % group, DIM, tid, x);
-                    }
-                }
-                if (p.lse != nullptr) {
-#pragma unroll
-                    for (int r = 0; r < ROWS; ++r)
-                        if (tid == r && r < rows)
-                            attn_store_lse(p, s.row0 + r / group, s.g * group + r % group, m[r], l[r]);
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < ROWS; ++r) {
-                    if (r < rows) {
-                        if (tid < DIM) part[r * DIM + tid] = o[r];
-                        if (tid == r) {
-                            part[ROWS * DIM + 2 * r] = m[r];
-                            part[ROWS * DIM + 2 * r + 1] = l[r];
-                        }
-                    }
-                }
-                __threadfence();
-                softmax_sync();
-                if (tid == 0) {
-                    const unsigned parts = static_cast<unsigned>(c1 - c0 + 1);
-                    merge_now = atomicInc(p.counters + c0, parts - 1) == parts - 1;  // wraps to 0
-                    __threadfence();
-                }
-                softmax_sync();
-                if (merge_now) {
-                    auto partial = [&](long long c) {
-                        const int slot = c == c0 && seg0 != total * c0 / ctas ? 1 : 0;
-                        return p.partials + (c * 2 + slot) * static_cast<long long>(ROWS * (DIM + 2));
-                    };
-                    merge_partials<DIM, ROWS>(p, s, rows, group, c0, c1, partial);
+                    for (int r = 0; r < 8; ++r)
+                        rows[r * DIM + tid] = fmaf(fmaf(__uint_as_float(o[2][r]), 0.0625f, __uint_as_float(o[1][r])),
+                                                   0.0625f, __uint_as_float(o[0][r])) * (1.0f / 128.0f);
                 }
             }
-            more = have_next;
+            group_sync(bar_id);
+            // a row in 16 threads, V dimensions each
+            constexpr int V = DIM / 16;
+            const int row = tid >> 4, at = (tid & 15) * V;
+            const int unit_row = row_base + row, token = unit_row / group, head = s->g * group + unit_row - token * group;
+            const bool valid = token < s->n;
+            float acc[V], mm = ref[row];
+            float ll = (red[row] + red[ROWS + row]) + (red[2 * ROWS + row] + red[3 * ROWS + row]);
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(rows + row * DIM + at + v);
+                acc[v] = x.x, acc[v + 1] = x.y, acc[v + 2] = x.z, acc[v + 3] = x.w;
+            }
+            bool write = begin == s->begin && end == s->stop;
+            if (!write) {
+                // the CTAs that share this request and head, and their partials
+                constexpr long long kPart = ROWS * (DIM + 2);
+                const long long seg0 = w0 + s->done - (begin - s->begin), seg1 = seg0 + (s->stop - s->begin);
+                const int c0 = piece_of(total, seg0, ctas), c1 = piece_of(total, seg1 - 1, ctas);
+                const int parts = c1 - c0 + 1;
+                auto slot_of = [&](int c) {
+                    return (c0 + c) * 2 + (c == 0 && seg0 != piece_begin(total, c0, ctas) ? 1 : 0);
+                };
+                auto partial = [&](int c) { return p.partials + slot_of(c) * kPart; };
+                auto put = [&](float *to) {
+#pragma unroll
+                    for (int v = 0; v < V; v += 4)
+                        *reinterpret_cast<float4 *>(to + unit_row * DIM + at + v) =
+                            make_float4(acc[v], acc[v + 1], acc[v + 2], acc[v + 3]);
+                    if ((tid & 15) == 0)
+                        *reinterpret_cast<float2 *>(to + ROWS * DIM + 2 * unit_row) = make_float2(mm, ll);
+                };
+                // whether this CTA is the last of `parts` to count here
+                auto last_of = [&](unsigned *counter, int parts) {
+                    __threadfence();
+                    group_sync(bar_id);
+                    if (tid == 0) {
+                        merge_now[grp] = atomicInc(counter, static_cast<unsigned>(parts - 1)) ==
+                                         static_cast<unsigned>(parts - 1);  // wraps to 0
+                        __threadfence();
+                    }
+                    group_sync(bar_id);
+                    return merge_now[grp] != 0;
+                };
+                // partials c0, c0 + step, ... added in this order: up to
+                // kDecFan factors in a row's 16 threads
+                auto merge = [&](int first_c, int step, int n) {
+                    const int c = tid & 15;
+                    const float2 ml = c < n ? __ldcg(reinterpret_cast<const float2 *>(
+                                                  partial(first_c + c * step) + ROWS * DIM + 2 * unit_row))
+                                            : make_float2(-INFINITY, 0.0f);
+                    mm = ml.x;
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o, 16));
+                    const float e = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mm);
+                    ll = ml.y * e;
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, o, 16);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+#pragma unroll 4
+                    for (int k = 0; k < n; ++k) {
+                        const float ek = __shfl_sync(0xFFFFFFFFu, e, k, 16);
+                        const float *q = partial(first_c + k * step) + unit_row * DIM + at;
+#pragma unroll
+                        for (int v = 0; v < V; v += 4) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(q + v));
+                            acc[v] = fmaf(x.x, ek, acc[v]);
+                            acc[v + 1] = fmaf(x.y, ek, acc[v + 1]);
+                            acc[v + 2] = fmaf(x.z, ek, acc[v + 2]);
+                            acc[v + 3] = fmaf(x.w, ek, acc[v + 3]);
+                        }
+                    }
+                };
+                // a tree of fan-in kDecFan, one level where the parts are few:
+                // a single CTA reads its partials at one SM's rate
+                int index = static_cast<int>(cta) - c0, step = 1, n = parts;
+                unsigned *counters = p.counters;
+                put(partial(index));
+                for (;;) {
+                    const int node = index / kDecFan * kDecFan, members = min(kDecFan, n - node);
+                    write = last_of(counters + slot_of(node * step) * GROUPS + grp, members);
+                    if (!write) break;
+                    merge(node * step, step, members);
+                    if (n <= kDecFan) break;
+                    put(partial(node * step));
+                    index = node / kDecFan;
+                    step *= kDecFan;
+                    n = (n + kDecFan - 1) / kDecFan;
+                    counters += 2 * kDecMaxCtas * 2;
+                    group_sync(bar_id);  // merge_now has been read
+                }
+            }
+            if (write && valid) {
+                const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[v] = ll > 0.0f ? acc[v] * inv : 0.0f;
+                attn_store<V>(p, s->row0 + token, head, DIM, at, acc);
+                if ((tid & 15) == 0 && p.lse != nullptr) attn_store_lse(p, s->row0 + token, head, mm, ll);
+            }
+            group_sync(bar_id);  // rows, sums and references have been read
             s = next;
+            more = next != nullptr;
         }
     }
 
     // MMAs retired, tensor memory free
-    mbar_wait_drain(done_bar, 0, p.status);
+    kv_drain(done_bar, 0, p.status);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kTmemCols));
 }
 

@@ -36,7 +36,7 @@
 
 #include <type_traits>
 
-#include "kv_attention_decode.cuh"
+#include "kv_attention_params.cuh"
 
 namespace fp8l {
 namespace {
@@ -79,58 +79,8 @@ struct ProSmem {
     static_assert(kBytes <= 227 * 1024 - 320, "one CTA's shared memory, beside the static variables");
 };
 
-// mbar_wait without a call: the register split does not allow one.
-__device__ __forceinline__ bool pro_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status,
-                                         long long limit) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return false;
-        if (clock64() - t0 > limit) {
-            *abort_flag = 1;
-            atomicOr(status, kStatusTimeout);
-            return false;
-        }
-    }
-    return true;
-}
-
-// A wait that ignores the abort flag, while tearing down
-__device__ __forceinline__ void pro_drain(uint32_t bar, uint32_t parity, unsigned *status) {
-    const long long t0 = clock64();
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (clock64() - t0 > kDefaultWaitCycles) {
-            atomicOr(status, kStatusTimeout);
-            return;
-        }
-    }
-}
-
-// Operand descriptors as two words: the address moves only in the low one,
-// so a step along an operand is one addition (a single thread issues every
-// MMA, and its instructions are the critical path).
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
-    return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
-}
-constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14); }
-
-// D (tensor memory) = or += A B^T, both operands in shared memory, fp8
-template <bool ACC>
-__device__ __forceinline__ void pro_mma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
-                                           uint32_t b_hi, uint32_t idesc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
-        : "memory");
-}
-
 // The same with A in tensor memory, fp16
-__device__ __forceinline__ void pro_mma_f16(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+__device__ __forceinline__ void mma_f16_desc(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
                                             uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
@@ -140,41 +90,6 @@ __device__ __forceinline__ void pro_mma_f16(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-
-__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // E4M3 codes of two fp16 pairs (in order), which become what the codes leave
 // over (exact: the difference of a value and its rounding to fewer bits)
@@ -307,34 +222,6 @@ __device__ __forceinline__ long long pro_request_work(const AttnParams &p, int r
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
     return n;
-}
-
-// One lane of the (converged) warp, always the same
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xFFFFFFFF;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0u;
-}
-
-__device__ __forceinline__ void half_sync(int half) {
-    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
-}
-
-__device__ __forceinline__ bool half_any(int half, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(x ? 1u : 0u), "r"(1 + half)
-        : "memory");
-    return r != 0u;
 }
 
 // Adds the CTAs' partials of one half of a row tile, in CTA order: a warp
@@ -509,7 +396,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
     ProSegment *segs = reinterpret_cast<ProSegment *>(pro_smem + Sm::kSegOff);
     // piece number n, or nullptr after the last (or a time-out)
     auto segment_at = [&](int n) -> const ProSegment * {
-        if (!pro_wait(segfull + 8 * (n & (kProSegments - 1)), (n / kProSegments) & 1u, abort_flag, p.status,
+        if (!kv_wait(segfull + 8 * (n & (kProSegments - 1)), (n / kProSegments) & 1u, abort_flag, p.status,
                       p.wait_cycles))
             return nullptr;
         const ProSegment *s = segs + (n & (kProSegments - 1));
@@ -560,7 +447,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
                 // keys, and the scales of keys and values
                 ok = __all_sync(0xFFFFFFFFu,
-                                pro_wait(kempty + 8 * kst, kph ^ 1u, abort_flag, p.status, p.wait_cycles));
+                                kv_wait(kempty + 8 * kst, kph ^ 1u, abort_flag, p.status, p.wait_cycles));
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(kfull + 8 * kst, sum);
                 __syncwarp();
@@ -585,7 +472,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 }
                 // values
                 ok = __all_sync(0xFFFFFFFFu,
-                                pro_wait(vempty + 8 * vst, vph ^ 1u, abort_flag, p.status, p.wait_cycles));
+                                kv_wait(vempty + 8 * vst, vph ^ 1u, abort_flag, p.status, p.wait_cycles));
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(vfull + 8 * vst, sum);
                 __syncwarp();
@@ -602,9 +489,9 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         for (int x = 0; x < Sm::kKStages; ++x)
-            if (kissued & (1u << x)) pro_drain(kfull + 8 * x, (kpar >> x) & 1u, p.status);
+            if (kissued & (1u << x)) kv_drain(kfull + 8 * x, (kpar >> x) & 1u, p.status);
         for (int x = 0; x < Sm::kVStages; ++x)
-            if (vissued & (1u << x)) pro_drain(vfull + 8 * x, (vpar >> x) & 1u, p.status);
+            if (vissued & (1u << x)) kv_drain(vfull + 8 * x, (vpar >> x) & 1u, p.status);
       } else if (warp == 13) {
         // ---------------------------------------------------------- MMAs
         {
@@ -613,7 +500,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             const uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(kProKeys >> 3) << 17) | (8u << 24);
             const uint32_t idesc_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(DIM >> 3) << 17) | (8u << 24);
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                return __all_sync(0xFFFFFFFFu, pro_wait(bar, parity & 1u, abort_flag, p.status, p.wait_cycles));
+                return __all_sync(0xFFFFFFFFu, kv_wait(bar, parity & 1u, abort_flag, p.status, p.wait_cycles));
             };
             bool ok = true;
             if (p.stall & kStallMma) ok = wait(done_bar, 0);
@@ -632,10 +519,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     for (int x = 0; x < DIM / 32; ++x) {
                         const uint32_t a = q_lo + ((half * Sm::kParts + part) * Sm::kQPart + 256 * x) / 16;
                         const uint32_t b = k_lo + 256 * x / 16;
-                        if (part == 0 && x == 0)
-                            pro_mma_f8<false>(tmem_u + 128u * half, a, desc_hi(8 * DIM), b, desc_hi(8 * DIM), idesc_s);
-                        else
-                            pro_mma_f8<true>(tmem_u + 128u * half, a, desc_hi(8 * DIM), b, desc_hi(8 * DIM), idesc_s);
+                        mma_f8_desc(tmem_u + 128u * half, a, desc_hi(8 * DIM), b, desc_hi(8 * DIM), idesc_s, (part | x) != 0 ? 1u : 0u);
                     }
                 }
                 mma_commit(sfull + 8 * half);
@@ -652,7 +536,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     if (leader) {
 #pragma unroll
                         for (int x = y * kProKeys / 32; x < (y + 1) * kProKeys / 32; ++x)
-                            pro_mma_f16(tmem_u + 256u + 128u * half, tmem_u + 128u * half + 8u * x, v + 32 * DIM * x / 16,
+                            mma_f16_desc(tmem_u + 256u + 128u * half, tmem_u + 128u * half + 8u * x, v + 32 * DIM * x / 16,
                                 desc_hi(128), idesc_o, x == 0 ? (first ? 0u : 1u) : 1u);
                     }
                 }
@@ -727,7 +611,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     // scales; a page without a seen key was not copied
                     const int slot = count & (kProScaleSlots - 1), pg = (16 * tid) >> p.page_shift;
                     const int key = tile * kProKeys + 16 * tid;
-                    ok = ok && pro_wait(scfull + 8 * slot, (count / kProScaleSlots) & 1u, abort_flag, p.status,
+                    ok = ok && kv_wait(scfull + 8 * slot, (count / kProScaleSlots) & 1u, abort_flag, p.status,
                                               p.wait_cycles);
                     const float *sc = reinterpret_cast<const float *>(pro_smem + Sm::kScaleOff) + slot * 16;
                     const bool there = key <= last && key + 15 >= first;
@@ -737,7 +621,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     mbar_arrive(fcfull + 8 * slot);
                 }
                 constexpr int PIECES = kProKeys * DIM / 16 / 128;  // 16-byte pieces per thread
-                ok = ok && pro_wait(vfull + 8 * vst, vph, abort_flag, p.status, p.wait_cycles);
+                ok = ok && kv_wait(vfull + 8 * vst, vph, abort_flag, p.status, p.wait_cycles);
                 const uint8_t *src = pro_smem + Sm::kVOff + vst * Sm::kTileBytes;
                 uint4 u[PIECES];
 #pragma unroll
@@ -755,7 +639,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     vph ^= 1u;
                 }
                 const int b = count & 1;
-                ok = ok && pro_wait(v16free + 8 * b, ((count >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                ok = ok && kv_wait(v16free + 8 * b, ((count >> 1) & 1u) ^ 1u, abort_flag, p.status,
                                           p.wait_cycles);
                 uint8_t *dst = pro_smem + Sm::kV16Off + b * Sm::kV16Bytes;
 #pragma unroll
@@ -794,7 +678,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             const ProSegment *s = segment_at(segment);
             // one answer for the half's threads, whose barriers below need all
             // of them (a wait can give up in one thread and not in another)
-            if (half_any(half, s == nullptr)) break;
+            if (group_any(1 + half, s == nullptr)) break;
             const int rows = s->rows - 128 * half;  // valid rows of this half
             const int end = s->end, begin = s->tile;
             if (rows <= 0) {
@@ -872,7 +756,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(qfull + 8 * half);
-                half_sync(half);  // the row factors are written
+                group_sync(1 + half);  // the row factors are written
             }
             const float f = qf[tid];
             ++segment;
@@ -880,9 +764,9 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             for (int tile = begin; tile < end; ++tile, ++count, ++uses) {
                 // (a barrier per slot, not the key stage's, which may be
                 // filled again while this half is still in an epilogue)
-                ok = ok && pro_wait(fcfull + 8 * (count & (kProScaleSlots - 1)), (count / kProScaleSlots) & 1u,
+                ok = ok && kv_wait(fcfull + 8 * (count & (kProScaleSlots - 1)), (count / kProScaleSlots) & 1u,
                                           abort_flag, p.status, p.wait_cycles);
-                ok = ok && pro_wait(sfull + 8 * half, uses & 1u, abort_flag, p.status, p.wait_cycles);
+                ok = ok && kv_wait(sfull + 8 * half, uses & 1u, abort_flag, p.status, p.wait_cycles);
                 tc_fence_after();
                 if (warp_on) {
                     const float4 *fc = factors + (count & (kProScaleSlots - 1)) * 8;
@@ -935,17 +819,17 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                         l *= keep;
                         m = to;
                         if (tile != begin) {
-                            ok = ok && pro_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status,
+                            ok = ok && kv_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status,
                                                 p.wait_cycles);
                             tc_fence_after();
 #pragma unroll 1
                             for (int x = 0; x < DIM / 16; ++x) {
                                 uint32_t o[16];
-                                tmem_ld_n(o_tmem + 16 * x, o);
+                                tmem_ld16_nowait(o_tmem + 16 * x, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                                tmem_st_n(o_tmem + 16 * x, o);
+                                tmem_st16_nowait(o_tmem + 16 * x, o);
                             }
                         }
                     }
@@ -992,7 +876,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             }
 
             // ------------------------------------------------------ epilogue
-            ok = ok && pro_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status, p.wait_cycles);
+            ok = ok && kv_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status, p.wait_cycles);
             tc_fence_after();
             const bool whole = begin == s->begin && end == s->stop;
             const bool valid = tid < rows;
@@ -1034,25 +918,25 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 }
                 tc_fence_before();
                 __threadfence();
-                half_sync(half);
+                group_sync(1 + half);
                 if (tid == 0) {
                     const unsigned parts = static_cast<unsigned>(c1 - c0 + 1);
                     merge_now[half] = atomicInc(p.counters + 2 * c0 + half, parts - 1) == parts - 1;  // wraps to 0
                     __threadfence();
                 }
-                half_sync(half);
+                group_sync(1 + half);
                 if (merge_now[half]) {
                     pro_merge<DIM>(p, *s, half, rows, group, static_cast<int>(c1 - c0 + 1), [&](int c) {
                         const int slot = c == 0 && seg0 != total * c0 / ctas ? 1 : 0;
                         return p.partials + ((c0 + c) * 2 + slot) * kPart;
                     });
                 }
-                half_sync(half);  // merge_now has been read
+                group_sync(1 + half);  // merge_now has been read
             }
         }
     }
 
-    pro_drain(done_bar, 0, p.status);
+    kv_drain(done_bar, 0, p.status);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
