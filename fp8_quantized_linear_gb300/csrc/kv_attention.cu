@@ -24,7 +24,7 @@ constexpr size_t kAttnWorkspaceBytes =
     kAttnZeroBytes + sizeof(float) * (kDecPartials > kProPartials ? kDecPartials : kProPartials);
 // decode: per merge level, two pieces of a CTA, two softmax groups (four of half the CTAs)
 static_assert(kAttnCountersOffset + 4 * kDecLevels * 2 * 2 * kDecMaxCtas <= kAttnZeroBytes &&
-                  kAttnCountersOffset + 4 * 2 * kProMaxCtas <= kAttnZeroBytes,
+                  kAttnCountersOffset + 4 * kProLevels * 2 * 2 * kProMaxCtas <= kAttnZeroBytes,
               "counters fit");
 
 constexpr int kSmemPerSm = 227 * 1024;  // what the CTAs of an SM can ask for, each with 1 KB of its own

@@ -40,10 +40,12 @@ namespace {
 
 // ---------------------------------------------------------------- waits, barriers, tensor memory, MMAs
 
-// mbar_wait inline (a register split between warpgroups does not allow a
-// call).
+// A wait for the phase of parity `parity` without a call (a register split
+// between warpgroups does not allow one).  Warps that wait share issue slots
+// with the ones that work, so a failed try sleeps before the next.
+template <int SLEEP = 20>
 __device__ __forceinline__ bool kv_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status,
-                                         long long limit) {
+                                        long long limit) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
 #pragma unroll 1
@@ -54,6 +56,7 @@ __device__ __forceinline__ bool kv_wait(uint32_t bar, uint32_t parity, volatile 
             atomicOr(status, kStatusTimeout);
             return false;
         }
+        if (SLEEP > 0) __nanosleep(SLEEP);
     }
     return true;
 }
@@ -81,24 +84,28 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0u;
 }
 
-// Barrier `id` over the 128 threads of a group of four warps
-__device__ __forceinline__ void group_sync(int id) {
-    asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+// Barrier `id` over `threads` threads of the block
+__device__ __forceinline__ void wide_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // The same, with whether any of them says so
-__device__ __forceinline__ bool group_any(int id, bool x) {
+__device__ __forceinline__ bool wide_any(int id, int threads, bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(x ? 1u : 0u), "r"(id)
+        : "r"(x ? 1u : 0u), "r"(id), "r"(threads)
         : "memory");
     return r != 0u;
 }
+
+// Those of a group of four warps
+__device__ __forceinline__ void group_sync(int id) { wide_sync(id, 128); }
+__device__ __forceinline__ bool group_any(int id, bool x) { return wide_any(id, 128, x); }
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile(

@@ -53,6 +53,8 @@ constexpr int kProMaxCtas = 160;
 // registers per thread of the softmax, converter and other warpgroups after
 // the split: 2 x 184 + 88 + 56 = 4 x 128, what the block starts with
 constexpr int kProSoftmaxRegs = 184, kProConvertRegs = 88, kProOtherRegs = 56;
+constexpr int kProFan = 8;         // partials added by one CTA
+constexpr int kProLevels = 3;      // 8^3 CTAs and more
 constexpr float kProHead = 7.0f;   // reference below the maximum it was set from
 constexpr float kProMove = 15.0f;  // a score this far above moves it
 
@@ -224,59 +226,6 @@ __device__ __forceinline__ long long pro_request_work(const AttnParams &p, int r
     return n;
 }
 
-// Adds the CTAs' partials of one half of a row tile, in CTA order: a warp
-// takes 8 rows at a time, DIM / 32 dimensions per lane.
-template <int DIM, typename Partial>
-__device__ __forceinline__ void pro_merge(const AttnParams &p, const ProSegment &s, int half, int rows, int group,
-                                          int parts, const Partial &partial) {
-    constexpr int V = DIM / 32, B = 8;
-    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-#pragma unroll 1
-    for (int b = warp * 32; b < warp * 32 + 32 && b < rows; b += B) {
-        // lanes 0-7 hold the rows' maxima and sums
-        const int mine = 128 * half + b + (lane & (B - 1));
-        float top = -INFINITY;
-        for (int c = 0; c < parts; ++c) top = fmaxf(top, __ldcg(partial(c) + kProRows * DIM + 2 * mine));
-        float sum = 0.0f, acc[B][V] = {};
-        for (int c = 0; c < parts; ++c) {
-            const float *q = partial(c);
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q + kProRows * DIM + 2 * mine));
-            const float e = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
-            sum = fmaf(ml.y, e, sum);
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const float ei = __shfl_sync(0xFFFFFFFFu, e, i);
-                const float *row = q + (128 * half + b + i) * DIM + V * lane;
-                if constexpr (V == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(row));
-                    acc[i][0] = fmaf(v.x, ei, acc[i][0]);
-                    acc[i][1] = fmaf(v.y, ei, acc[i][1]);
-                    acc[i][2] = fmaf(v.z, ei, acc[i][2]);
-                    acc[i][3] = fmaf(v.w, ei, acc[i][3]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(row));
-                    acc[i][0] = fmaf(v.x, ei, acc[i][0]);
-                    acc[i][1] = fmaf(v.y, ei, acc[i][1]);
-                }
-            }
-        }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const float scale = __shfl_sync(0xFFFFFFFFu, inv, i);
-            if (b + i >= rows) continue;
-            const int row = s.row_first + 128 * half + b + i;
-#pragma unroll
-            for (int k = 0; k < V; ++k) acc[i][k] *= scale;
-            attn_store<V>(p, s.row0 + row / group, s.g * group + row % group, DIM, V * lane, acc[i]);
-        }
-        if (lane < B && b + lane < rows && p.lse != nullptr) {
-            const int row = s.row_first + 128 * half + b + lane;
-            attn_store_lse(p, s.row0 + row / group, s.g * group + row % group, top, sum);
-        }
-    }
-}
-
 template <int QDT, int DIM>
 __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(const AttnParams p) {
     using Sm = ProSmem<QDT, DIM>;
@@ -354,7 +303,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
     const long long ctas = min(static_cast<long long>(gridDim.x), total);
     const long long cta = static_cast<long long>(blockIdx.x);
     const bool idle = cta >= ctas;
-    const long long w0 = idle ? 0 : total * cta / ctas, w1 = idle ? 0 : total * (cta + 1) / ctas;
+    const long long w0 = idle ? 0 : piece_begin(total, cta, ctas), w1 = idle ? 0 : piece_begin(total, cta + 1, ctas);
     if (!idle && before <= w0 && w0 < before + warp_work[warp]) {
         long long rest = w0 - before;
         for (int r = r_begin; r < r_end; ++r) {
@@ -627,11 +576,17 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
 #pragma unroll
                 for (int k = 0; k < PIECES; ++k) {
                     const int piece = tid + 128 * k;
-                    const int key = tile * kProKeys + piece / (DIM / 2) * 8 + (piece & 7);
                     u[k] = *reinterpret_cast<const uint4 *>(src + 16 * piece);
+                }
+                if (tile * kProKeys < first || tile * kProKeys + kProKeys - 1 > last) {
                     // keys that are not there: whatever the stage holds (NaN
                     // codes too) must not meet their zero weights
-                    if (key < first || key > last) u[k] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int k = 0; k < PIECES; ++k) {
+                        const int piece = tid + 128 * k;
+                        const int key = tile * kProKeys + piece / (DIM / 2) * 8 + (piece & 7);
+                        if (key < first || key > last) u[k] = make_uint4(0u, 0u, 0u, 0u);
+                    }
                 }
                 mbar_arrive(vempty + 8 * vst);
                 if (++vst == Sm::kVStages) {
@@ -648,12 +603,11 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
                     uint32_t h[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t two = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu;
-                        asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-                            : "=r"(h[i])
-                            : "r"(two));
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                            : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
+                            : "r"(w[i]));
                     // [octet][D / 8][8 keys][8 dimensions]
                     uint8_t *at = dst + piece / (DIM / 2) * 16 * DIM + piece % (DIM / 2) / 8 * 256 + (piece & 7) * 16;
                     *reinterpret_cast<uint4 *>(at) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -878,61 +832,187 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             // ------------------------------------------------------ epilogue
             ok = ok && kv_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status, p.wait_cycles);
             tc_fence_after();
-            const bool whole = begin == s->begin && end == s->stop;
-            const bool valid = tid < rows;
-            const int row = s->row_first + 128 * half + tid;
-            const int out_token = s->row0 + row / group, head = s->g * group + row % group;
-            if (whole) {
-                if (warp_on) {
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll 1
-                    for (int x = 0; x < DIM / 32; ++x) {
-                        uint32_t v[32];
-                        tmem_ld32_nowait(o_tmem + 32 * x, v);
-                        tmem_wait_ld();
-                        float o[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = l > 0.0f ? __uint_as_float(v[i]) * inv : 0.0f;
-                        if (valid) attn_store<32>(p, out_token, head, DIM, 32 * x, o);
-                    }
-                    if (valid && p.lse != nullptr) attn_store_lse(p, out_token, head, m, l);
-                }
-                tc_fence_before();
-            } else {
-                const long long seg0 = w0 + s->done - (begin - s->begin), seg1 = seg0 + (s->stop - s->begin);
-                const long long c0 = ((seg0 + 1) * ctas - 1) / total, c1 = (seg1 * ctas - 1) / total;
-                constexpr long long kPart = kProRows * (DIM + 2);
-                float *part = p.partials + (cta * 2 + (begin != s->begin || seg0 == w0 ? 0 : 1)) * kPart;
-                if (warp_on) {
-#pragma unroll 1
-                    for (int x = 0; x < DIM / 32; ++x) {
-                        uint32_t v[32];
-                        tmem_ld32_nowait(o_tmem + 32 * x, v);
-                        tmem_wait_ld();
-                        float *at = part + (128 * half + tid) * DIM + 32 * x;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(at + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                    }
-                    *reinterpret_cast<float2 *>(part + kProRows * DIM + 2 * (128 * half + tid)) = make_float2(m, l);
-                }
-                tc_fence_before();
+            bool write = begin == s->begin && end == s->stop;
+            const bool from_tmem = write;
+            constexpr long long kPart = kProRows * (DIM + 2);
+            // float4 number c of a row in a partial: rows adjoin, so
+            // that a warp's rows are 512 contiguous bytes
+            auto quad = [&](float *part, int c) {
+                return reinterpret_cast<float4 *>(part) + c * kProRows + 128 * half + tid;
+            };
+            auto ml_of = [&](float *part) {
+                return reinterpret_cast<float2 *>(part + kProRows * DIM) + 128 * half + tid;
+            };
+            int members = 0, step = 1, node = 0, c0 = 0;
+            long long seg0 = 0;
+            auto slot_of = [&](int c) { return (c0 + c) * 2 + (c == 0 && seg0 != piece_begin(total, c0, ctas) ? 1 : 0); };
+            auto partial = [&](int c) { return p.partials + slot_of(c) * kPart; };
+            auto last_of = [&](unsigned *counter, int parts) {
                 __threadfence();
                 group_sync(1 + half);
                 if (tid == 0) {
-                    const unsigned parts = static_cast<unsigned>(c1 - c0 + 1);
-                    merge_now[half] = atomicInc(p.counters + 2 * c0 + half, parts - 1) == parts - 1;  // wraps to 0
+                    merge_now[half] = atomicInc(counter, static_cast<unsigned>(parts - 1)) ==
+                                      static_cast<unsigned>(parts - 1);  // wraps to 0
                     __threadfence();
                 }
                 group_sync(1 + half);
-                if (merge_now[half]) {
-                    pro_merge<DIM>(p, *s, half, rows, group, static_cast<int>(c1 - c0 + 1), [&](int c) {
-                        const int slot = c == 0 && seg0 != total * c0 / ctas ? 1 : 0;
-                        return p.partials + ((c0 + c) * 2 + slot) * kPart;
-                    });
+                const bool last = merge_now[half] != 0;
+                group_sync(1 + half);
+                return last;
+            };
+            float top = m, inv = 0.0f;
+            // values c .. c + 31 of this thread's columns, added over the
+            // members of a node
+            auto merge32 = [&](int c, float (&o)[32]) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+#pragma unroll 1
+                for (int k = 0; k < members; ++k) {
+                    float *part = partial((node + k) * step);
+                    const float mk = __ldcg(ml_of(part)).x;
+                    float4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = __ldcg(quad(part, c / 4 + i));
+                    const float e = mk == -INFINITY ? 0.0f : ex2(mk - top);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[4 * i] = fmaf(x[i].x, e, o[4 * i]);
+                        o[4 * i + 1] = fmaf(x[i].y, e, o[4 * i + 1]);
+                        o[4 * i + 2] = fmaf(x[i].z, e, o[4 * i + 2]);
+                        o[4 * i + 3] = fmaf(x[i].w, e, o[4 * i + 3]);
+                    }
                 }
-                group_sync(1 + half);  // merge_now has been read
+            };
+            auto put32 = [&](float *part, int c, const float (&o)[32]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *quad(part, c / 4 + i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            };
+            auto from_accumulator = [&](int c, float (&o)[32]) {
+                uint32_t v[32];
+                tmem_ld32_nowait(o_tmem + c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]);
+            };
+            if (!write) {
+                // the CTAs that share this row tile; a tree of fan-in kProFan
+                seg0 = w0 + s->done - (begin - s->begin);
+                c0 = piece_of(total, seg0, ctas);
+                const int c1 = piece_of(total, seg0 + (s->stop - s->begin) - 1, ctas);
+                int n = c1 - c0 + 1, index = static_cast<int>(cta) - c0;
+                unsigned *counters = p.counters;
+                if (warp_on) {
+                    float *part = partial(index);
+#pragma unroll 1
+                    for (int c = 0; c < DIM; c += 32) {
+                        float o[32];
+                        from_accumulator(c, o);
+                        put32(part, c, o);
+                    }
+                    *ml_of(part) = make_float2(m, l);
+                }
+                for (;;) {
+                    node = index / kProFan * kProFan;
+                    members = min(kProFan, n - node);
+                    write = last_of(counters + slot_of(node * step) * 2 + half, members);
+                    if (!write) break;
+                    top = -INFINITY;
+                    l = 0.0f;
+                    if (warp_on) {
+#pragma unroll 1
+                        for (int k = 0; k < members; ++k) top = fmaxf(top, __ldcg(ml_of(partial((node + k) * step))).x);
+#pragma unroll 1
+                        for (int k = 0; k < members; ++k) {
+                            const float2 ml = __ldcg(ml_of(partial((node + k) * step)));
+                            if (ml.x != -INFINITY) l = fmaf(ml.y, ex2(ml.x - top), l);
+                        }
+                    }
+                    m = top;
+                    if (n <= kProFan) break;
+                    if (warp_on) {
+                        float *to = partial(node * step);
+#pragma unroll 1
+                        for (int c = 0; c < DIM; c += 32) {
+                            float o[32];
+                            merge32(c, o);
+                            put32(to, c, o);
+                        }
+                    }
+                    group_sync(1 + half);  // the members' references have been read
+                    if (warp_on) *ml_of(partial(node * step)) = make_float2(m, l);
+                    index = node / kProFan;
+                    step *= kProFan;
+                    n = (n + kProFan - 1) / kProFan;
+                    counters += kProMaxCtas * 2 * 2;
+                }
             }
+            if (write && warp_on) {
+                // rows to the output's type in shared memory (the queries' are
+                // not needed any more), then out in whole rows: a store per
+                // row and thread would touch 32 lines
+                inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const bool codes = p.out_dtype == FP8L_E4M3;
+                const int pieces = codes ? DIM / 16 : DIM / 8;  // 16 bytes each, per row
+                uint8_t *stage = pro_smem + half * Sm::kParts * Sm::kQPart + (warp & 3) * 32 * 2 * DIM;
+                auto at = [&](int row, int piece) {
+                    return reinterpret_cast<uint4 *>(stage + (row * pieces + (piece ^ (row & (pieces - 1)))) * 16);
+                };
+#pragma unroll 1
+                for (int c = 0; c < DIM; c += 32) {
+                    float o[32];
+                    if (from_tmem)
+                        from_accumulator(c, o);
+                    else
+                        merge32(c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = l > 0.0f ? o[i] * inv : 0.0f;
+                    const int col = c;
+                    if (codes) {
+                        const Quot d = Quot::make<FP8L_F32>(p.out_scale[0]);
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            w[i] = codes_of_word<FP8L_F32, true>(
+                                       make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                                                  __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3])), d).x;
+                        *at(lane, col / 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *at(lane, col / 16 + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *at(lane, col / 8 + i) = make_uint4(pack_out16(o[8 * i], o[8 * i + 1], p.out_dtype),
+                                                                pack_out16(o[8 * i + 2], o[8 * i + 3], p.out_dtype),
+                                                                pack_out16(o[8 * i + 4], o[8 * i + 5], p.out_dtype),
+                                                                pack_out16(o[8 * i + 6], o[8 * i + 7], p.out_dtype));
+                    }
+                }
+                __syncwarp();
+                const int at_once = 32 / pieces;  // rows per step of the warp
+                const int piece = lane % pieces, row_of = lane / pieces, warp_row = 32 * (warp & 3);
+                const int first_row = s->row_first + 128 * half + warp_row + row_of;
+                int token = first_row / group, member = first_row % group;
+                const int token_step = at_once / group, member_step = at_once % group;
+                const int64_t row_bytes = codes ? DIM : 2 * DIM;
+                uint8_t *out = static_cast<uint8_t *>(p.out) + 16 * piece;
+#pragma unroll 1
+                for (int r = row_of; r < 32; r += at_once) {
+                    if (warp_row + r < rows)
+                        *reinterpret_cast<uint4 *>(out + (static_cast<int64_t>(s->row0 + token) * p.q_heads +
+                                                          s->g * group + member) * row_bytes) = *at(r, piece);
+                    token += token_step;
+                    member += member_step;
+                    if (member >= group) {
+                        member -= group;
+                        ++token;
+                    }
+                }
+                if (p.lse != nullptr && tid < rows) {
+                    const int row = s->row_first + 128 * half + tid;
+                    attn_store_lse(p, s->row0 + row / group, s->g * group + row % group, m, l);
+                }
+            }
+            tc_fence_before();
         }
     }
 
