@@ -628,16 +628,51 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
         const float4 *factors = reinterpret_cast<const float4 *>(pro_smem + Sm::kFactorOff);
         int count = 0, segment = 0, uses = 0;
         bool ok = true;
-        for (;;) {
-            const ProSegment *s = segment_at(segment);
-            // one answer for the half's threads, whose barriers below need all
-            // of them (a wait can give up in one thread and not in another)
-            if (group_any(1 + half, s == nullptr)) break;
+        // a piece, with one answer for the half's threads, whose barriers
+        // below need all of them (a wait can give up in one thread and not in
+        // another)
+        auto piece = [&](int n) -> const ProSegment * {
+            const ProSegment *s = segment_at(n);
+            return group_any(1 + half, s == nullptr) ? nullptr : s;
+        };
+        // A warp's 32 query rows of a piece, eight at a time: lane (r, c) =
+        // (lane % 8, lane / 8) holds the 16-dimension chunks c, c + 4 of row r,
+        // so that eight lanes store one 128-byte core matrix.  The loads start
+        // before the epilogue of the piece before.
+        constexpr int CHUNKS = DIM / 64;
+        const int qr = lane & 7, qc = lane >> 3;
+        uint4 raw[4][2 * CHUNKS];
+        auto load_queries = [&](const ProSegment &s) {
+            const int first = 128 * half + 32 * (warp & 3) + qr, row_first = s.row_first + first;
+            int token = row_first / group, member = row_first % group;
+            const int token_step = 8 / group, member_step = 8 % group;
+            const uint16_t *q0 = p.q + static_cast<int64_t>(s.row0) * p.q_stride + s.g * group * DIM + 16 * qc;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint16_t *at = q0 + static_cast<int64_t>(token) * p.q_stride + member * DIM;
+#pragma unroll
+                for (int x = 0; x < 2 * CHUNKS; ++x) {
+                    raw[k][x] = make_uint4(0u, 0u, 0u, 0u);
+                    if (first + 8 * k < s.rows)
+                        raw[k][x] = *reinterpret_cast<const uint4 *>(at + (x >> 1) * 64 + (x & 1) * 8);
+                }
+                token += token_step;
+                member += member_step;
+                if (member >= group) {
+                    member -= group;
+                    ++token;
+                }
+            }
+        };
+        const ProSegment *s = piece(0);
+        if (s != nullptr) load_queries(*s);
+        while (s != nullptr) {
             const int rows = s->rows - 128 * half;  // valid rows of this half
             const int end = s->end, begin = s->tile;
             if (rows <= 0) {
                 count += end - begin;
-                ++segment;
+                s = piece(++segment);
+                if (s != nullptr) load_queries(*s);
                 continue;
             }
             const bool warp_on = (tid & ~31) < rows;
@@ -645,75 +680,54 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             // positions of the warp's first and last valid row
             const int pos_lo = __shfl_sync(0xFFFFFFFFu, pos, 0);
             const int pos_hi = __shfl_sync(0xFFFFFFFFu, pos, min(31, max(rows - 1 - (tid & ~31), 0)));
-            // this half's queries as E4M3 parts, and each row's factor: LANES
-            // lanes hold a row, eight dimensions each, all loads in flight at
-            // once.  (The half's earlier score MMAs have retired: it has read
-            // their results.)
+            // the queries as E4M3 parts, and each row's factor.  (The half's
+            // earlier score MMAs have retired: it has read their results.)
             {
-                constexpr int LANES = DIM / 8, AT_ONCE = 128 / LANES, BATCH = 4;
-                const int l = tid % LANES;
-                const int row_first = s->row_first + 128 * half + tid / LANES;
-                int token = row_first / group, member = row_first % group;
-                const int token_step = AT_ONCE / group, member_step = AT_ONCE % group;
-                const uint16_t *q0 = p.q + static_cast<int64_t>(s->row0) * p.q_stride + s->g * group * DIM + 8 * l;
-                uint4 next[BATCH];
-                auto load = [&](int row0) {
-#pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        next[k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row0 + k * AT_ONCE + tid / LANES < rows)
-                            next[k] = *reinterpret_cast<const uint4 *>(q0 + static_cast<int64_t>(token) * p.q_stride +
-                                                                       member * DIM);
-                        token += token_step;
-                        member += member_step;
-                        if (member >= group) {
-                            member -= group;
-                            ++token;
-                        }
-                    }
-                };
-                load(0);
-                const int full = min((rows + AT_ONCE * BATCH - 1) / (AT_ONCE * BATCH), 128 / (AT_ONCE * BATCH));
+                uint8_t *dst = pro_smem + half * Sm::kParts * Sm::kQPart + (warp & 3) * 32 * DIM + qc * 128 + qr * 16;
 #pragma unroll 1
-                for (int b = 0; b < full; ++b) {
-                    uint4 u[BATCH];
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t mag = 0;
 #pragma unroll
-                    for (int k = 0; k < BATCH; ++k) u[k] = next[k];
-                    load((b + 1) * AT_ONCE * BATCH);  // (none past the last row)
+                    for (int x = 0; x < 2 * CHUNKS; ++x) mag = word_mag_max<QDT>(raw[0][x], mag);
+                    mag = fold_mag<QDT>(mag);
+                    mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 8));
+                    mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 16));
+                    const int e = part_exponent(mag_bits_to_float<QDT>(mag));
+                    const uint32_t up = static_cast<uint32_t>(127 + e) << 23;
+                    if (qc == 0)
+                        qf[32 * (warp & 3) + 8 * b + qr] =
+                            p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        const int row = (b * BATCH + k) * AT_ONCE + tid / LANES;
-                        uint32_t mag = fold_mag<QDT>(word_mag_max<QDT>(u[k], 0u));
+                    for (int x = 0; x < CHUNKS; ++x) {
+                        uint32_t h[8];  // the scaled row in fp16: exact from 2^-22 of its largest element on
 #pragma unroll
-                        for (int o = LANES / 2; o > 0; o >>= 1)
-                            mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o, LANES));
-                        const int e = part_exponent(mag_bits_to_float<QDT>(mag));
-                        const uint32_t up = static_cast<uint32_t>(127 + e) << 23;
-                        if (l == 0) qf[row] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                        uint32_t h[4];  // the scaled row in fp16: exact from 2^-22 of its largest element on
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint64_t x2 = f2_mul(widen16<QDT>(w[i]), f2_pack(up, up));
-                            const __half2 x = __floats2half2_rn(__uint_as_float(static_cast<uint32_t>(x2)),
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 &u = raw[0][2 * x + (i >> 2)];
+                            const uint32_t w = (i & 3) == 0 ? u.x : ((i & 3) == 1 ? u.y : ((i & 3) == 2 ? u.z : u.w));
+                            const uint64_t x2 = f2_mul(widen16<QDT>(w), f2_pack(up, up));
+                            const __half2 y = __floats2half2_rn(__uint_as_float(static_cast<uint32_t>(x2)),
                                                                 __uint_as_float(static_cast<uint32_t>(x2 >> 32)));
-                            h[i] = *reinterpret_cast<const uint32_t *>(&x);
+                            h[i] = *reinterpret_cast<const uint32_t *>(&y);
                         }
-                        uint8_t *dst = pro_smem + half * Sm::kParts * Sm::kQPart + (row >> 3) * 8 * DIM +
-                                       (l >> 1) * 128 + (row & 7) * 16 + 8 * (l & 1);
 #pragma unroll
                         for (int part = 0; part < Sm::kParts; ++part) {
-                            const uint32_t c0 = take_part_f16(h[0], h[1]), c1 = take_part_f16(h[2], h[3]);
-                            *reinterpret_cast<uint2 *>(dst + part * Sm::kQPart) = make_uint2(c0, c1);
+                            uint32_t c[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) c[i] = take_part_f16(h[2 * i], h[2 * i + 1]);
+                            *reinterpret_cast<uint4 *>(dst + part * Sm::kQPart + b * 8 * DIM + x * 512) =
+                                make_uint4(c[0], c[1], c[2], c[3]);
                         }
                     }
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+#pragma unroll
+                        for (int x = 0; x < 2 * CHUNKS; ++x) raw[k][x] = raw[k + 1][x];
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(qfull + 8 * half);
-                group_sync(1 + half);  // the row factors are written
+                __syncwarp();  // the row factors are written
             }
             const float f = qf[tid];
-            ++segment;
             float m = -INFINITY, l = 0.0f;
             for (int tile = begin; tile < end; ++tile, ++count, ++uses) {
                 // (a barrier per slot, not the key stage's, which may be
@@ -747,13 +761,15 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                             // others go back masked for the second reading
                             const int c0 = key0 + 64 * x;
                             const int lo = p.window > 0 ? pos - p.window + 1 - c0 : 0, hi = pos + 1 - c0;
+                            auto below = [](int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); };
                             const int lo_all = p.window > 0 ? pos_hi - p.window + 1 - c0 : 0, hi_all = pos_lo + 1 - c0;
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 if (32 * y >= lo_all && 32 * y + 32 <= hi_all) continue;
+                                const uint32_t seen = below(hi - 32 * y) & ~below(lo - 32 * y);
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    if (32 * y + i < lo || 32 * y + i >= hi) v[y][i] = 0xFF800000u;  // -inf
+                                    if (!(seen & (1u << i))) v[y][i] = 0xFF800000u;  // -inf
                                 tmem_st32_nowait(s_tmem + 64 * x + 32 * y, v[y]);
                             }
                             tmem_wait_st();
@@ -828,6 +844,8 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     mbar_arrive(wfull + 16 * half + 8);
                 }
             }
+
+            const ProSegment *next = piece(++segment);
 
             // ------------------------------------------------------ epilogue
             ok = ok && kv_wait(odone + 8 * half, (uses - 1) & 1u, abort_flag, p.status, p.wait_cycles);
@@ -1013,6 +1031,9 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 }
             }
             tc_fence_before();
+            group_sync(1 + half);  // the rows in shared memory have left
+            s = next;
+            if (s != nullptr) load_queries(*s);
         }
     }
 
