@@ -133,7 +133,7 @@ __device__ __forceinline__ ProRequest pro_request(const AttnParams &p, int r) {
     ProRequest d;
     const int a = min(max(p.q_offsets[r], 0), p.tokens), b = min(max(p.q_offsets[r + 1], 0), p.tokens);
     const int64_t cap = static_cast<int64_t>(p.table_width) << p.page_shift;
-    const int L = max(p.kv_lens[r], 0);
+    const int L = min(max(p.kv_lens[r], 0), INT32_MAX - 255);  // (a tile's last key fits an int)
     d.keys = static_cast<int64_t>(L) < cap ? L : static_cast<int>(cap);
     d.n = max(b - a, 0);
     d.row0 = a;

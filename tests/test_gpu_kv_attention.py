@@ -266,6 +266,24 @@ def test_offsets_past_32_bits(n):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("most", [1, 3, 24])
+def test_many_requests(most):
+    # more requests than a block has threads, empty ones among them
+    rng = np.random.default_rng(most)
+    q = rng.integers(0, most + 1, 700)
+    kv = q + rng.integers(0, 90, 700) * (rng.random(700) < 0.7)
+    q[::7], kv[::7] = 0, 0
+    q[3], kv[3] = most, 2000
+    check(make(torch.bfloat16, 16, 4, 2, 64, q, kv, seed=most))
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_a_larger_bound_of_new_tokens_gives_the_same_rows(n):
+    s = make(torch.bfloat16, 64, 8, 2, 128, [n, n], [700, 90], seed=2)
+    for bound in (n, n + 1, 5 * n + 40, 10 ** 6):
+        check(s, max_q_len=bound)
+
+
 def test_no_rows():
     s = make(torch.bfloat16, 64, 4, 2, 128, [1], [200], seed=2)
     out, lse = fl.fp8_kv_attention(s["q"][:0], s["cache"], s["table"], i32([0, 0]), i32([200]), 1,
