@@ -537,6 +537,30 @@ kv_attention_decode_kernel(const AttnParams p) {
             }
             group_sync(bar_id);  // the row factors of this piece are written
             const DecSegment *next = nullptr;
+            if (GROUPS > 1 && row_base >= s->n * group) {
+                // none of this group's rows exist: only its share of the
+                // barriers, and the next piece's queries
+                for (int tile = begin; tile < end; ++tile, ++i) {
+                    const int b = i & 1;
+                    ok = ok && kv_wait(sfull + 8 * b, (i >> 1) & 1u, abort_flag, p.status, p.wait_cycles);
+                    mbar_arrive(sempty + 8 * b);
+                    ok = ok && kv_wait(wfree + 8 * b, ((i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.wait_cycles);
+                    mbar_arrive(wfull + 8 * b);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (tile == begin) {
+                        next = segment_at(segment + 1);
+                        if (group_any(bar_id, next == nullptr)) next = nullptr;
+                        if (next != nullptr) load_queries(*next, qb ^ 1);
+                    }
+                }
+                ++segment;
+                s = next;
+                more = next != nullptr;
+                continue;
+            }
             for (int tile = begin; tile < end; ++tile, ++i) {
                 const int b = i & 1;
                 const int key = tile * kDecTile + tid;
