@@ -22,6 +22,15 @@
 // second time from L1.  Tokens that a page already holds are re-cast by the
 // whole block when the scale grew: a group alone would read up to 127 rows
 // one after the other.
+//
+// Measured (GB300, replayed from a graph; 8 kv heads of 128, bf16, norms and a
+// full rotation): 72 us for 13741 tokens with 32 query heads in pages of 128,
+// 4.3 TB/s of the 311 MB it has to move (a plain copy of qkv takes 51 us);
+// queries alone take 42 us, 5.4 TB/s, keys and values the rest, bound by
+// instructions (two readings, the exact quotient: 0.63 of the issue slots).
+// 7.2 us for one token each of 256 sequences with 64 query heads, 3.1 us for
+// one.  Holding the rows between the readings took 128 registers and 87 us;
+// alternating units and queries over the grid changed nothing.
 #include "kv_device.cuh"
 #include "quant_device.cuh"
 
@@ -446,7 +455,8 @@ __global__ void __launch_bounds__(kAppThreads, 4) qk_norm_rope_append_kernel(con
 template <int DT, int DIM>
 int launch_append(const AppendParams &p, dim3 grid, cudaStream_t stream) {
     // both dimensions of a rotation pair in one thread, where the halves of
-    // the whole head rotate against each other (the usual case)
+    // the whole head rotate against each other: 72 us against 104 for 13741
+    // tokens, 7.2 against 8.2 for 256 decoding
     if (p.rot == DIM && !p.interleaved)
         return launch_dependent(qk_norm_rope_append_kernel<DT, DIM, kSplit>, grid, kAppThreads, 0, stream, p);
     return launch_dependent(qk_norm_rope_append_kernel<DT, DIM, kContiguous>, grid, kAppThreads, 0, stream, p);
@@ -504,7 +514,9 @@ extern "C" int fp8_qk_norm_rope_append(const void *qkv, int dtype, int64_t token
     p.page_shift = __builtin_ctzll(static_cast<unsigned long long>(page_size));
     const int groups = kAppThreads / static_cast<int>(head_dim / 8);
     // few tokens: one run per group of a block; many: longer chunks, since in
-    // a prompt only every page_size-th token starts a run
+    // a prompt only every page_size-th token starts a run.  Measured (us, short
+    // chunks / long): 256 decoding 7.2 / 17.7, seven prompts of 250 tokens 16.9 /
+    // 19.0, of 400 tokens 20.9 / 18.9, of 900 42 / 35, 13741 tokens 87 / 72
     p.chunk = tokens <= 2048 ? groups : kAppMaxChunk;
     const int64_t kv_blocks = (tokens + p.chunk - 1) / p.chunk * 2 * kv_heads;
     p.head_groups = static_cast<int>((q_heads + kAppHeadsPerGroup - 1) / kAppHeadsPerGroup);

@@ -30,8 +30,9 @@
 // Work.  The tiles of all requests and kv heads are one line, cut into equal
 // pieces for the CTAs of one resident wave, whatever the lengths.  A request
 // and head inside one piece is written out directly; one that spans pieces
-// leaves its partial (m, l, O) in the workspace and the last CTA to arrive
-// adds the partials in CTA order, so the result does not depend on timing.
+// leaves its partial (m, l, O) in the workspace.  Of every kDecFan neighbours
+// the last to arrive adds the partials in CTA order and carries the sum to the
+// next level, so the result does not depend on timing.
 //
 // Roles: per eight rows a softmax group of four warps (warp w of a group owns
 // tensor-memory lanes 32 w ..: a thread is a key, and in the epilogue a
@@ -40,6 +41,15 @@
 // which also hands the pieces of the line to the others through shared memory;
 // one warp that issues the MMAs, the next tile's scores before this tile's
 // values.  Two CTAs per SM up to 16 rows, one with 32.
+//
+// What bounds it is HBM once a CTA has tens of tiles: 153 us for 5 sequences of
+// 60-131k keys (8 kv heads of 128, groups of 8: 989 MB, 6.5 TB/s, 0.95 of the
+// measured copy rate), 88 us for 64 of 0.1-8k (469 MB, 5.3 TB/s, 0.78: the
+// prologue, 3 us, and one boundary in every 28 tiles, where a CTA's softmax
+// waits for its epilogue while the SM's other CTA streams).  One tile's softmax
+// takes about 1200 cycles (2000 with four groups), which two CTAs hide and one
+// does not: 153 us with 20 rows, 104 us with 12.  6.7 us for one sequence of
+// 129 keys, of which the first bytes arrive after 3.
 #pragma once
 
 #include "kv_attention_params.cuh"
@@ -280,7 +290,10 @@ kv_attention_decode_kernel(const AttnParams p) {
         if (r0 == 0) before0 = before;
         total += sum;
     }
-    // fewer CTAs when each would get less than kDecMinTiles
+    // fewer CTAs when each would get less than kDecMinTiles: a merge costs about
+    // as much as two tiles.  Measured (us, 1 / 2 / 3 tiles): one sequence of 129
+    // keys 9.1 / 6.7 / 12.5, 1500 keys 13.2 / 11.6 / 11.6, 4000 keys 17.9 / 15.5 /
+    // 17.3, 30000 keys 23.3 / 23.4 / 23.3, eight of up to 1000 12.3 / 15.5 / 17.0
     const long long ctas = max(min(static_cast<long long>(gridDim.x), total / kDecMinTiles),
                                min(static_cast<long long>(gridDim.x), min(total, 1LL)));
     const long long cta = static_cast<long long>(blockIdx.x);

@@ -22,16 +22,31 @@
 // A row is one thread, a page's factors are uniform, so the maximum and the
 // sum cost one operation per score and page.  The reference m starts 7 below
 // the first tile's maximum and moves (rescaling l and the accumulator) only
-// when a score passes it by 15: weights stay below 2^15, fp16 keeps 11 bits
-// down to 2^-28 of the row's largest.
+// when a score passes it by 15: weights stay below 2^15 and the row's largest
+// is at least 2^7, so fp16 keeps 11 bits of a weight down to 2^-21 of the
+// largest and is within 2^-32 of the largest below that.
 //
 // Work: the tiles (request, kv head, row tile, key tile) form one line, cut
 // into equal pieces for one CTA per SM; row tiles that span pieces are merged
-// by the last CTA to arrive, in CTA order, as in the decode kernel.
+// as in the decode kernel, by a tree of kProFan.
 //
-// Roles (512 threads): warps 0-3 and 4-7 softmax of halves 0 and 1 (warp w
-// owns tensor-memory lanes 32 (w mod 4) ..), warps 8-11 queries to parts and V
-// to fp16, warp 12 copies, warp 13 issues the MMAs.
+// Roles (512 threads): warps 0-3 and 4-7 softmax, queries and epilogue of
+// halves 0 and 1 (warp w owns tensor-memory lanes 32 (w mod 4) ..), warps 8-11
+// V to fp16 and the scales' factors, warp 12 copies and hands the pieces of the
+// line to the others through shared memory, warp 13 issues the MMAs.
+//
+// Measured (GB300, 32 query and 8 kv heads of 128, bf16): 866 us for 4096
+// queries of a 20480-token context, 1428 TFLOP/s, 0.77 of the measured 16-bit
+// rate; 180 us for six ragged prompts of 6294 tokens (0.31: a row tile there
+// has about 8 key tiles, and its queries, masked tile and rows' way out weigh
+// as much).  A step of 256 rows and 128 keys needs 2048 tensor cycles and takes
+// about 3400: within a half scores, maximum, weights and the second product
+// follow each other, and the other half covers only part of that.  What moved
+// it: the register split, MMAs issued by an elected lane of a converged warp and
+// loops kept rolled for the instruction cache (1305 -> 942 us), waits that sleep
+// (942 -> 919; today 900 without the sleep), rows leaving through shared memory
+// and the cheaper conversion of V (919 -> 892).  What did not: two threads per
+// row (1006), weights against the old reference before any maximum (1007).
 #pragma once
 
 #include <type_traits>

@@ -15,6 +15,10 @@
 // instead of meeting the others at a grid barrier or in a second launch, and
 // takes its share of the rows and of the new table entries, each found in
 // the prefix sums by bisection in shared memory.
+//
+// Measured (GB300, replayed from a graph): 2.9 us for 64 requests of one new
+// token, 7.5 us for 1021 requests with 25085 (two rounds of scans, 13 blocks);
+// an empty launch takes 2 us.
 #include "kv_device.cuh"
 
 namespace fp8l {

@@ -492,7 +492,7 @@ FP8L_API int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_t 
  *          (a, b) <- (a cos_i - b sin_i, b cos_i + a sin_i), i < rot / 2, the
  *          pair being dimensions (i, i + rot/2), or (2i, 2i+1) when
  *          `interleaved`; cos_sin: float32 [max_positions, rot], cosines then
- *          sines; rot = 0 or a multiple of 16 up to head_dim; positions:
+ *          sines, 16-byte aligned; rot = 0 or a multiple of 16 up to head_dim; positions:
  *          int32 [tokens], clamped into the table
  *   q:     rounded to dtype into q_out [tokens, q_heads, head_dim]
  *   k, v:  quantized from float32 into the cache at slots[token] (int32, as
@@ -522,7 +522,8 @@ FP8L_API int fp8_qk_norm_rope_append(const void *qkv, int dtype, int64_t tokens,
  * start, the caller fills with zeros once (status word and merge counters;
  * every call leaves the counters at zero).  As with the other workspace,
  * calls that may overlap on the GPU need one each; fp8l_read_status reads
- * its status word. */
+ * its status word.  A call whose wait gave up may leave the counters mid-way:
+ * after FP8L_ETIMEOUT the caller fills the zero_bytes with zeros again. */
 FP8L_API size_t fp8_kv_attention_workspace_bytes(void);
 FP8L_API size_t fp8_kv_attention_workspace_zero_bytes(void);
 
@@ -543,8 +544,9 @@ FP8L_API size_t fp8_kv_attention_workspace_zero_bytes(void);
  * q: [tokens, q_heads, head_dim] of q_dtype (FP8L_F16 or FP8L_BF16), rows
  * `q_stride` elements apart (a multiple of 8); q_offsets: int32
  * [requests + 1]; kv_lens: int32 [requests], lengths after the step's
- * append; block_table as above, its entries for the tokens below kv_lens
- * valid pages (others are never read as data); max_q_len: an upper bound of
+ * append; block_table as above, its entries valid pages for every token
+ * below kv_lens that some row sees (a page out of range reads as page 0 or
+ * the last one; other entries are never read as data); max_q_len: an upper bound of
  * n known on the host (it selects the kernel; 0 means no rows).
  * out: [tokens, q_heads, head_dim] of out_dtype: q_dtype, or FP8L_E4M3 codes
  * of out / out_scale[0] (the static input scale of the o product); rows
