@@ -35,16 +35,16 @@
 // V to fp16 and the scales' factors, warp 12 copies and hands the pieces of the
 // line to the others through shared memory, warp 13 issues the MMAs.
 //
-// Measured (GB300, 32 query and 8 kv heads of 128, bf16): 866 us for 4096
-// queries of a 20480-token context, 1428 TFLOP/s, 0.77 of the measured 16-bit
+// Measured (GB300, 32 query and 8 kv heads of 128, bf16): 880 us for 4096
+// queries of a 20480-token context, 1406 TFLOP/s, 0.75 of the measured 16-bit
 // rate; 180 us for six ragged prompts of 6294 tokens (0.31: a row tile there
 // has about 8 key tiles, and its queries, masked tile and rows' way out weigh
 // as much).  A step of 256 rows and 128 keys needs 2048 tensor cycles and takes
-// about 3400: within a half scores, maximum, weights and the second product
+// about 3500: within a half scores, maximum, weights and the second product
 // follow each other, and the other half covers only part of that.  What moved
 // it: the register split, MMAs issued by an elected lane of a converged warp and
 // loops kept rolled for the instruction cache (1305 -> 942 us), waits that sleep
-// (942 -> 919; today 900 without the sleep), rows leaving through shared memory
+// (942 -> 919; later 900 against 867 without the sleep), rows leaving through shared memory
 // and the cheaper conversion of V (919 -> 892).  What did not: two threads per
 // row (1006), weights against the old reference before any maximum (1007).
 #pragma once
@@ -63,7 +63,7 @@ constexpr int kProWarps = kProThreads / 32;
 constexpr int kProMaxKStages = 4;
 constexpr int kProMaxVStages = 2;
 constexpr int kProScaleSlots = 8;  // tiles whose page scales are held
-constexpr int kProSegments = 8;    // pieces between the copy warp and the slowest role (stages + 2 at most)
+constexpr int kProSegments = 8;    // pieces between the copy warp and the softmax halves
 constexpr int kProMaxCtas = 160;
 // registers per thread of the softmax, converter and other warpgroups after
 // the split: 2 x 160 + 104 + 88 = 4 x 128, what the block starts with (184,
@@ -91,7 +91,8 @@ struct ProSmem {
     static constexpr int kQfOff = kFactorOff + kProScaleSlots * 8 * 16;     // [256] floats
     static constexpr int kSegOff = kQfOff + kProRows * 4;                   // [kProSegments] ProSegment
     static constexpr int kBarOff = kSegOff + kProSegments * 64;
-    static constexpr int kBars = 2 * kProMaxKStages + 2 * kProMaxVStages + 2 * kProScaleSlots + kProSegments + 4 + 8 + 3;
+    static constexpr int kBars =
+        2 * kProMaxKStages + 2 * kProMaxVStages + 2 * kProScaleSlots + 2 * kProSegments + 4 + 8 + 3;
     static constexpr int kMiscOff = kBarOff + kBars * 8;
     static constexpr int kBytes = kMiscOff + 16;
     static_assert(kBytes <= 227 * 1024 - 320, "one CTA's shared memory, beside the static variables");
@@ -259,7 +260,8 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
     const uint32_t kfull = take_bars(kProMaxKStages), kempty = take_bars(kProMaxKStages);
     const uint32_t vfull = take_bars(kProMaxVStages), vempty = take_bars(kProMaxVStages);
     const uint32_t scfull = take_bars(kProScaleSlots);
-    const uint32_t fcfull = take_bars(kProScaleSlots), segfull = take_bars(kProSegments);
+    const uint32_t fcfull = take_bars(kProScaleSlots);
+    const uint32_t segfull = take_bars(kProSegments), segfree = take_bars(kProSegments);
     const uint32_t v16full = take_bars(2), v16free = take_bars(2);
     const uint32_t sfull = take_bars(2), wfull = take_bars(4), odone = take_bars(2);
     const uint32_t qfull = take_bars(2), done_bar = take_bars(1);
@@ -272,7 +274,10 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             mbar_init(kfull + 8 * s, 1);
             mbar_init(kempty + 8 * s, 1);
         }
-        for (int s = 0; s < kProSegments; ++s) mbar_init(segfull + 8 * s, 1);
+        for (int s = 0; s < kProSegments; ++s) {
+            mbar_init(segfull + 8 * s, 1);
+            mbar_init(segfree + 8 * s, 256);
+        }
         for (int s = 0; s < kProScaleSlots; ++s) {
             mbar_init(scfull + 8 * s, 32);
             mbar_init(fcfull + 8 * s, 8);
@@ -384,6 +389,12 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
         while (ok) {
             const bool more = walk.next(p, s);
             if (!more) s.tile = s.end = 0;
+            // (half 1 can fall behind where pieces have no rows for it; the
+            // other roles cannot, the stages hold them together)
+            ok = __all_sync(0xFFFFFFFFu, kv_wait(segfree + 8 * (segment & (kProSegments - 1)),
+                                                  ((segment / kProSegments) & 1u) ^ 1u, abort_flag, p.status,
+                                                  p.wait_cycles));
+            if (!ok) break;
             if (lane == 0) {
                 segs[segment & (kProSegments - 1)] = s;
                 mbar_arrive(segfull + 8 * (segment & (kProSegments - 1)));
@@ -651,12 +662,15 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             const ProSegment *s = segment_at(n);
             return group_any(1 + half, s == nullptr) ? nullptr : s;
         };
+        // this thread is through with piece n
+        auto release = [&](int n) { mbar_arrive(segfree + 8 * (n & (kProSegments - 1))); };
         const ProSegment *s = piece(0);
         while (s != nullptr) {
             const int rows = s->rows - 128 * half;  // valid rows of this half
             const int end = s->end, begin = s->tile;
             if (rows <= 0) {
                 count += end - begin;
+                release(segment);
                 s = piece(++segment);
                 continue;
             }
@@ -1043,6 +1057,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
             }
             tc_fence_before();
             group_sync(1 + half);  // the rows in shared memory have left
+            release(segment - 1);
             s = next;
         }
     }

@@ -277,6 +277,14 @@ def test_many_requests(most):
     check(make(torch.bfloat16, 16, 4, 2, 64, q, kv, seed=most))
 
 
+def test_runs_of_small_prompts_after_full_row_tiles():
+    # a block then walks more pieces without rows for its second half (over
+    # 128) than the ring that hands out the pieces has slots
+    q = ([150] + [20] * 29) * 5
+    kv = [n + 40 * (i % 3) for i, n in enumerate(q)]
+    check(make(torch.bfloat16, 32, 32, 16, 64, q, kv, seed=4))
+
+
 @pytest.mark.parametrize("n", [1, 30])
 def test_a_larger_bound_of_new_tokens_gives_the_same_rows(n):
     s = make(torch.bfloat16, 64, 8, 2, 128, [n, n], [700, 90], seed=2)
