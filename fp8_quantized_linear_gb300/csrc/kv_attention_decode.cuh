@@ -90,7 +90,10 @@ struct DecShape {
     static constexpr int kScaleOff = kWOff + 2 * kWBytes + (GROUPS == 1 ? 0 : kRows * DIM * 4);  // [stage][2][8]
     static constexpr int kQfOff = kScaleOff + kDecMaxStages * 16 * 4;   // [2][kRows] floats
     static constexpr int kRedOff = kQfOff + 2 * kRows * 4;              // [4][kRows] floats
-    static constexpr int kRefOff = kRedOff + 4 * kRows * 4;             // [kRows] floats
+    // the epilogue's sums, apart from the maxima: a piece's last tile can move
+    // the reference, and no barrier lies between its reads and these writes
+    static constexpr int kSumOff = kRedOff + 4 * kRows * 4;             // [4][kRows] floats
+    static constexpr int kRefOff = kSumOff + 4 * kRows * 4;             // [kRows] floats
     static constexpr int kSegOff = (kRefOff + kRows * 4 + 15) / 16 * 16;  // [kDecSegments] DecSegment
     static constexpr int kBarOff = kSegOff + kDecSegments * 64;
     static constexpr int kBars = 2 * kDecMaxStages + 10 + kDecSegments + 1;
@@ -481,6 +484,7 @@ kv_attention_decode_kernel(const AttnParams p) {
         const uint32_t s_tmem = tmem + lane_addr + row_base, o_tmem = tmem + lane_addr + o_col + row_base;
         float *qf = reinterpret_cast<float *>(fixed_ptr + Sh::kQfOff) + row_base;
         float *red = reinterpret_cast<float *>(fixed_ptr + Sh::kRedOff) + row_base;
+        float *sums = reinterpret_cast<float *>(fixed_ptr + Sh::kSumOff) + row_base;
         float *ref = reinterpret_cast<float *>(fixed_ptr + Sh::kRefOff) + row_base;
         const float *scales = reinterpret_cast<const float *>(fixed_ptr + Sh::kScaleOff);
         bool ok = true;
@@ -704,7 +708,7 @@ kv_attention_decode_kernel(const AttnParams p) {
             // sums over the keys, and the accumulator turned from a dimension
             // per thread into rows of shared memory
             const float sum = reduce8<false>(l, lane);
-            if ((lane & 3) == 0) red[(warp & 3) * ROWS + (lane >> 2)] = sum;
+            if ((lane & 3) == 0) sums[(warp & 3) * ROWS + (lane >> 2)] = sum;
 #pragma unroll
             for (int r = 0; r < 8; ++r)
                 if (tid == r) ref[r] = m[r];
@@ -731,7 +735,7 @@ kv_attention_decode_kernel(const AttnParams p) {
             const int unit_row = row_base + row, token = unit_row / group, head = s->g * group + unit_row - token * group;
             const bool valid = token < s->n;
             float acc[V], mm = ref[row];
-            float ll = (red[row] + red[ROWS + row]) + (red[2 * ROWS + row] + red[3 * ROWS + row]);
+            float ll = (sums[row] + sums[ROWS + row]) + (sums[2 * ROWS + row] + sums[3 * ROWS + row]);
 #pragma unroll
             for (int v = 0; v < V; v += 4) {
                 const float4 x = *reinterpret_cast<const float4 *>(rows + row * DIM + at + v);

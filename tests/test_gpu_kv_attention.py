@@ -301,3 +301,27 @@ def test_no_rows():
     out, _ = fl.fp8_kv_attention(s["q"], s["cache"], s["table"], i32([0, 0]), i32([200]), 1,
                                  out=fresh)
     assert bool((out == 5.0).all())
+
+
+def rising(s, page):
+    """Every tile of 128 keys scores higher than the one before: the running
+    reference moves in each, a piece's last among them."""
+    for r, n in enumerate(s["kv"]):
+        for b in range(-(-int(n) // page)):
+            pg = int(s["table"][r, b])
+            old = s["cache"].k_scale[pg].clone()
+            s["cache"].k_scale[pg] *= 1 + b * page // 128
+            grown = (s["cache"].k_scale[pg].double() / old.double())[:, None, None]
+            s["k"][r][:, b * page:(b + 1) * page] *= grown
+    return s
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", [1, 3, 7, 100])
+def test_references_that_move_in_every_tile(n, dtype):
+    kv = [1500, 900, 129, 257, 640, 2000]
+    s = rising(make(dtype, 64, 8, 2, 128, [n] * len(kv), kv, seed=12 + n), 64)
+    first, lse = check(s)
+    for _ in range(100):
+        again, l2 = run(s, want_lse=True)
+        assert torch.equal(first, again) and torch.equal(lse, l2)
