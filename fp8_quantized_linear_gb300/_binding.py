@@ -102,6 +102,8 @@ def load():
         lib.fp8_qk_norm_rope_append.argtypes = [P, I, I64, I64, I64, I64, I64, P, P,
                                                 ctypes.c_float, P, I64, I64, I, P, P, P, P, P, P,
                                                 P, I64, I64, P]
+        lib.fp8l_capture_id.restype = I
+        lib.fp8l_capture_id.argtypes = [P, ctypes.POINTER(ctypes.c_ulonglong)]
         lib.fp8_kv_attention_workspace_bytes.restype = ctypes.c_size_t
         lib.fp8_kv_attention_workspace_bytes.argtypes = []
         lib.fp8_kv_attention_workspace_zero_bytes.restype = ctypes.c_size_t
@@ -685,27 +687,56 @@ def fp8_qk_norm_rope_append(qkv: torch.Tensor, cache: KvCache, positions: torch.
     return q
 
 
-_attention_workspaces = {}
+_attention_workspaces = {}  # (device, stream): workspace of its eager calls
+_capture_workspaces = {}  # (device, stream): (capture, workspace) of its last capture
+
+
+def _capture_id(index: int, stream: int) -> int:
+    """The stream's capture, 0 when it is not being captured."""
+    if not stream:
+        return 0  # the legacy default stream cannot be
+    got = ctypes.c_ulonglong()
+    f = (_lib or load()).fp8l_capture_id
+    if _current_device() == index:
+        st = f(stream, got)
+    else:
+        with torch.cuda.device(index):
+            st = f(stream, got)
+    _check(st, "fp8l_capture_id")
+    return got.value
 
 
 def fp8_kv_attention_workspace(device=None) -> torch.Tensor:
     """A workspace of fp8_kv_attention for the current stream of `device`:
     allocated once per stream and reused (its counters zeroed), so calls on
-    different streams do not share one.  During a graph capture without such
-    a workspace the graph gets its own, zeroed at every replay."""
+    different streams do not share one.  A graph capture never takes it: each
+    capture gets a workspace of its own for each of its streams, from the
+    graph's memory, whose counters every replay zeroes first, so a graph may
+    be replayed on any stream and beside eager calls."""
     if isinstance(device, int):
         index = device
     else:
         index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
     key = (index, _stream_handle(index))
-    ws = _attention_workspaces.get(key)
-    if ws is None:
-        lib = load()
-        ws = torch.empty(lib.fp8_kv_attention_workspace_bytes(), dtype=_U8,
-                         device=torch.device("cuda", index))
-        ws[: lib.fp8_kv_attention_workspace_zero_bytes()].zero_()
-        if not torch.cuda.is_current_stream_capturing():
-            _attention_workspaces[key] = ws
+    capture = _capture_id(*key)
+    if capture:
+        kept, ws = _capture_workspaces.get(key, (0, None))
+        if kept == capture:
+            return ws
+    else:
+        ws = _attention_workspaces.get(key)
+        if ws is not None:
+            return ws
+    lib = load()
+    ws = torch.empty(lib.fp8_kv_attention_workspace_bytes(), dtype=_U8,
+                     device=torch.device("cuda", index))
+    ws[: lib.fp8_kv_attention_workspace_zero_bytes()].zero_()
+    if capture:
+        # held until the stream's next capture: the later calls of this one
+        # need it, and the graph's memory outlives the tensor
+        _capture_workspaces[key] = (capture, ws)
+    else:
+        _attention_workspaces[key] = ws
     return ws
 
 

@@ -90,6 +90,17 @@ extern "C" {
 size_t fp8_kv_attention_workspace_bytes(void) { return fp8l::kAttnWorkspaceBytes; }
 size_t fp8_kv_attention_workspace_zero_bytes(void) { return fp8l::kAttnZeroBytes; }
 
+int fp8l_capture_id(void *stream, unsigned long long *id) {
+    if (id == nullptr) return FP8L_EINVAL;
+    *id = 0;
+    if (stream == nullptr) return FP8L_OK;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long capture = 0;
+    if (cudaStreamGetCaptureInfo(fp8l::as_stream(stream), &status, &capture) != cudaSuccess) return FP8L_ECUDA;
+    if (status == cudaStreamCaptureStatusActive) *id = capture;
+    return FP8L_OK;
+}
+
 int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_stride, int64_t q_heads,
                      int64_t kv_heads, int64_t head_dim, const uint8_t *k_cache, const uint8_t *v_cache,
                      const float *k_scale, const float *v_scale, int64_t num_pages, int64_t page_size,

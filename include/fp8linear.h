@@ -521,11 +521,19 @@ FP8L_API int fp8_qk_norm_rope_append(const void *qkv, int dtype, int64_t tokens,
 /* Bytes of fp8_kv_attention's workspace, and how many of them, from the
  * start, the caller fills with zeros once (status word and merge counters;
  * every call leaves the counters at zero).  As with the other workspace,
- * calls that may overlap on the GPU need one each; fp8l_read_status reads
+ * calls that may overlap on the GPU need one each, replays of a graph among
+ * them; fp8l_read_status reads
  * its status word.  A call whose wait gave up may leave the counters mid-way:
  * after FP8L_ETIMEOUT the caller fills the zero_bytes with zeros again. */
 FP8L_API size_t fp8_kv_attention_workspace_bytes(void);
 FP8L_API size_t fp8_kv_attention_workspace_zero_bytes(void);
+
+/* Identity of the stream capture that `stream` is part of, or 0 when it is not
+ * being captured (or is the legacy default stream, which cannot be), in *id.
+ * A caller that keeps a workspace per stream needs it: a captured call's
+ * workspace belongs to the graph, which may be replayed on any stream, beside
+ * later calls on the one it was captured on. */
+FP8L_API int fp8l_capture_id(void *stream, unsigned long long *id);
 
 /* Causal attention of a step's queries over the paged cache: decode (one
  * token per request), a few drafted tokens, and prompt chunks, ragged.

@@ -1,0 +1,92 @@
+"""Workspaces of fp8_kv_attention: one per stream for eager calls, one per
+capture for graphs, so that calls that may overlap share neither partials nor
+merge counters."""
+import pytest
+import torch
+
+import fp8_quantized_linear_gb300 as fl
+from gpu_util import DEV
+from test_gpu_kv_attention import i32, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+def test_a_capture_takes_a_workspace_of_its_own():
+    side = torch.cuda.Stream(DEV)
+    with torch.cuda.stream(side):
+        eager = fl.fp8_kv_attention_workspace(DEV)
+        assert fl.fp8_kv_attention_workspace(DEV) is eager
+    seen = [eager]
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            ws = fl.fp8_kv_attention_workspace(DEV)
+            assert fl.fp8_kv_attention_workspace(DEV) is ws
+        seen.append(ws)
+    assert len({ws.data_ptr() for ws in seen}) == 3
+    with torch.cuda.stream(side):
+        assert fl.fp8_kv_attention_workspace(DEV) is eager
+
+
+@pytest.mark.parametrize("n", [1, 4, 90])
+def test_graphs_of_one_stream_replay_beside_each_other_and_eager_calls(n):
+    # requests that span blocks, so that every call merges partials
+    cases = [make(torch.bfloat16, 64, 8, 2, 128, [n] * 3, [5000, 3000, 900 + i], seed=20 + i)
+             for i in range(3)]
+    lens = [(i32(s["off"]), i32(s["kv"])) for s in cases]
+
+    def call(i):
+        s, (off, kv) = cases[i], lens[i]
+        return fl.fp8_kv_attention(s["q"], s["cache"], s["table"], off, kv, s["n"])[0]
+
+    want = [call(i) for i in range(3)]
+    side = torch.cuda.Stream(DEV)
+    side.wait_stream(torch.cuda.current_stream(DEV))
+    with torch.cuda.stream(side):
+        call(0)  # the stream has a workspace before it is captured
+    side.synchronize()
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            out = torch.empty_like(want[i])
+            for _ in range(4):
+                out.copy_(call(i))
+        graphs.append(g)
+        outs.append(out)
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    for _ in range(20):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        with torch.cuda.stream(side):
+            eager = [call(2) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        assert all(torch.equal(e, want[2]) for e in eager)
+
+
+def test_one_capture_over_two_streams():
+    s = make(torch.bfloat16, 64, 8, 2, 128, [1] * 3, [5000, 3000, 900], seed=23)
+    off, kv = i32(s["off"]), i32(s["kv"])
+
+    def call():
+        return fl.fp8_kv_attention(s["q"], s["cache"], s["table"], off, kv, s["n"])[0]
+
+    want, _ = run(s)
+    main, side = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        first = call()
+        with torch.cuda.stream(side):
+            second = call()
+        main.wait_stream(side)
+    for _ in range(10):
+        first.zero_(), second.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, want) and torch.equal(second, want)
