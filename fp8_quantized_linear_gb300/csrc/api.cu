@@ -79,8 +79,9 @@ int make_kmajor_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t K, 
 
 namespace {
 // Status word of the calls that take no workspace (fp8_w8a16_mm's
-// tensor-core kernel): time-outs are recorded here and reported, then
-// cleared, by fp8l_read_status together with the workspace's word.
+// tensor-core kernel) or whose workspace may be out of the host's reach (the
+// attention kernels in a graph): time-outs are recorded here and reported,
+// then cleared, by fp8l_read_status together with the workspace's word.
 __device__ unsigned g_library_status;
 
 struct StatusSlot {

@@ -154,6 +154,7 @@ int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_strid
     p.lse = lse;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.status = status_word(workspace);
+    if (int st = library_status_word(&p.library_status); st != FP8L_OK) return st;
     p.counters = reinterpret_cast<unsigned *>(ws + kAttnCountersOffset);
     p.partials = reinterpret_cast<float *>(ws + kAttnZeroBytes);
     const WaitConfig waits = wait_config();

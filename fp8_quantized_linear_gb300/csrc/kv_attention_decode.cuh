@@ -839,6 +839,7 @@ kv_attention_decode_kernel(const AttnParams p) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    kv_report(abort_flag, p.library_status);
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kTmemCols));
 }

@@ -32,6 +32,7 @@ struct AttnParams {
     int stages;
     float *partials;
     unsigned *counters, *status;
+    unsigned *library_status;  // a call that gave up is recorded here too
     long long wait_cycles;
     unsigned stall;
 };
@@ -71,6 +72,13 @@ __device__ __forceinline__ void kv_drain(uint32_t bar, uint32_t parity, unsigned
             return;
         }
     }
+}
+
+// At the end of a block: a wait that gave up in it also goes to the library's
+// word.  The workspace of a captured call belongs to its graph, where no
+// status read looks and every replay clears it.
+__device__ __forceinline__ void kv_report(const volatile int *abort_flag, unsigned *library_status) {
+    if (threadIdx.x == 0 && *abort_flag) atomicOr(library_status, kStatusTimeout);
 }
 
 // One lane of the (converged) warp, always the same

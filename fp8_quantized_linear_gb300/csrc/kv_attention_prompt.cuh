@@ -1066,6 +1066,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    kv_report(abort_flag, p.library_status);
     if (warp == 13)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }

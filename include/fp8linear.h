@@ -32,9 +32,9 @@
  *  - Errors found on the host (FP8L_EINVAL, FP8L_ESHAPE, FP8L_EALIGN,
  *    FP8L_EUNSUPPORTED) are returned before anything is launched and leave
  *    every output untouched.  FP8L_ECUDA reports a failed CUDA call or
- *    launch.  Device-side wait time-outs are recorded in the workspace (or,
- *    for fp8_w8a16_mm, in a status word of the library) and reported by
- *    fp8l_read_status().
+ *    launch.  Device-side wait time-outs are recorded in the workspace (for
+ *    fp8_w8a16_mm in a status word of the library, for fp8_kv_attention in
+ *    both) and reported by fp8l_read_status().
  *  - Inputs must be finite.  NaN or Inf input is outside the contract.
  */
 #ifndef FP8LINEAR_H
@@ -523,7 +523,9 @@ FP8L_API int fp8_qk_norm_rope_append(const void *qkv, int dtype, int64_t tokens,
  * every call leaves the counters at zero).  As with the other workspace,
  * calls that may overlap on the GPU need one each, replays of a graph among
  * them; fp8l_read_status reads
- * its status word.  A call whose wait gave up may leave the counters mid-way:
+ * its status word.  A time-out is recorded in the library's own status word
+ * as well, so that one in a replayed graph is reported by the next
+ * fp8l_read_status of any workspace.  A call whose wait gave up may leave the counters mid-way:
  * after FP8L_ETIMEOUT the caller fills the zero_bytes with zeros again. */
 FP8L_API size_t fp8_kv_attention_workspace_bytes(void);
 FP8L_API size_t fp8_kv_attention_workspace_zero_bytes(void);
@@ -573,8 +575,8 @@ FP8L_API int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_
 
 /* Waits for `stream`, then reads and clears the workspace's status word and
  * the library's own status word on the current device (where
- * fp8_w8a16_mm, which takes no workspace, records its time-outs; looked up
- * per CUDA context like the no-alloc quantizer's scratch, so make a first
+ * fp8_w8a16_mm, which takes no workspace, and fp8_kv_attention, beside its
+ * workspace, record their time-outs; looked up per CUDA context like the no-alloc quantizer's scratch, so make a first
  * call before any stream capture).  Returns FP8L_OK, FP8L_ETIMEOUT if a
  * device-side wait of an earlier call gave up (that call's outputs are then
  * undefined; the workspace's barrier words are zeroed as well, so the next

@@ -5,8 +5,9 @@ import pytest
 import torch
 
 import fp8_quantized_linear_gb300 as fl
+from fp8_quantized_linear_gb300 import _binding as b
 from gpu_util import DEV
-from test_gpu_kv_attention import i32, make, run
+from test_gpu_kv_attention import check, i32, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,60 @@ def test_one_capture_over_two_streams():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(first, want) and torch.equal(second, want)
+
+
+@pytest.mark.parametrize("q_lens,kv", [([1, 1], [3000, 129]), ([200, 40], [1500, 40])])
+def test_a_time_out_in_a_replayed_graph_is_reported(q_lens, kv):
+    # the graph's workspace is its own: any status read reports it
+    s = make(torch.bfloat16, 64, 8, 2, 128, q_lens, kv, seed=1)
+    off, lens = i32(s["off"]), i32(s["kv"])
+    check(s)
+    ws = fl.workspace(s["q"].device)
+    assert fl.fp8l_read_status(ws) == b.OK
+    graphs = []
+    for stall in (b.STALL_MMA, 0):
+        g = torch.cuda.CUDAGraph()
+        fl.fp8l_debug_waits(wait_cycles=1 << 20 if stall else 0, stall_mask=stall)
+        try:
+            with torch.cuda.graph(g):
+                out, _ = fl.fp8_kv_attention(s["q"], s["cache"], s["table"], off, lens, s["n"])
+        finally:
+            fl.fp8l_debug_waits()
+        graphs.append((g, out))
+    for _ in range(2):
+        graphs[0][0].replay()
+        graphs[0][0].replay()
+        assert fl.fp8l_read_status(ws) == b.ETIMEOUT
+        assert fl.fp8l_read_status(ws) == b.OK
+    graphs[1][0].replay()
+    assert fl.fp8l_read_status(ws) == b.OK
+    assert torch.equal(graphs[1][1], run(s)[0])
+
+
+FIRST_CALL = """
+import torch
+import fp8_quantized_linear_gb300 as fl
+dev = torch.device("cuda:0")
+cache = fl.kv_cache(4, 16, 2, 64, dev)
+q = torch.ones(1, 4, 64, dtype=torch.half, device=dev)
+table = torch.zeros(1, 1, dtype=torch.int32, device=dev)
+off = torch.tensor([0, 1], dtype=torch.int32, device=dev)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out, lse = fl.fp8_kv_attention(q, cache, table, off, off[1:], 1, want_lse=True)
+g.replay()
+torch.cuda.synchronize()
+# lse = ln 1; the hardware logarithm of the smallest block scale is within 3
+# units of 2^-17, that is 2^-16 in lse
+assert bool((out == 0).all()) and bool((lse.abs() <= 2.0 ** -16 * 1.05).all()), (out, lse)
+assert fl.fp8l_read_status(fl.workspace(dev)) == 0
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import subprocess
+    import sys
+    root = b._PKG.rsplit("/", 1)[0]
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True,
+                          text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
