@@ -71,7 +71,8 @@ class PagedAttentionBlock:
 
     def forward(self, x: torch.Tensor, plan: b.KvPlan, max_q_len: int) -> torch.Tensor:
         """The layer's attention output for x [tokens, HIDDEN] (bf16), rows in
-        the plan's order; max_q_len: the most new tokens of a request."""
+        the plan's order; max_q_len: the most new tokens of a request.  The
+        plan has placed every token (its used[1] is 0)."""
         codes, scale, _ = b.fp8_rmsnorm_quant(x, self.gamma, self.eps, ws=self.ws)
         qkv = b.fp8_scaled_mm(codes, self.w["qkv"], scale, self.sw["qkv"], ws=self.ws,
                               stable_weights=True)
@@ -90,9 +91,15 @@ class PagedAttentionBlock:
         self.free = self.free[pages_taken:].contiguous()
 
     def step(self, x: torch.Tensor, q_lens: list[int]) -> torch.Tensor:
-        """plan, forward and commit of one step, with the lengths on the host."""
+        """plan, forward and commit of one step, with the lengths on the host.
+        Raises before anything is computed when a token finds no page (too few
+        free pages, or a request past its table's); the cache, the lengths and
+        the free pages are then as before, and a later step may be tried."""
         lens = torch.tensor(q_lens, dtype=torch.int32, device=self.device)
         plan = self.plan(lens, x.shape[0])
+        taken, lost = plan.used.tolist()
+        if lost:
+            raise RuntimeError(f"{lost} of the step's {x.shape[0]} tokens found no page")
         y = self.forward(x, plan, max(q_lens))
-        self.commit(plan, int(plan.used[0]))
+        self.commit(plan, taken)
         return y

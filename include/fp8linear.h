@@ -467,6 +467,9 @@ FP8L_API int fp8_quant_per_tensor_noalloc(const void *x, int x_dtype, int64_t ro
  *                            last request
  *   used[2]                  pages taken from the front of free_pages; new
  *                            tokens without a page (0: all were placed)
+ * A step whose used[1] is not 0 cannot go on to fp8_kv_attention, which takes
+ * a request's rows as the last of its kv_lens_out tokens: the rows of a
+ * request that lost tokens would see the wrong keys.
  * q_lens, kv_lens: int32 [requests]; block_table: int32 [requests,
  * table_width], in and out; free_pages: int32 [num_free].  No input other
  * than block_table is written, so a call may be repeated with the same
@@ -541,7 +544,8 @@ FP8L_API int fp8l_capture_id(void *stream, unsigned long long *id);
  * token per request), a few drafted tokens, and prompt chunks, ragged.
  *
  * Row i (0 <= i < n) of request r, n = q_offsets[r+1] - q_offsets[r], has
- * position p = kv_lens[r] - n + i (its own key is in the cache) and sees the
+ * position p = kv_lens[r] - n + i (its own key is in the cache: after
+ * fp8_kv_plan only when used[1] is 0) and sees the
  * keys j <= p, with window > 0 only those j > p - window.  Per query head h
  * (kv head h / (q_heads / kv_heads)):
  *   s_j = sm_scale * q . k_j,    out = sum_j exp(s_j) v_j / sum_j exp(s_j),

@@ -132,3 +132,26 @@ def test_captured_decode_step(weights):
         _, eager = decode()
         assert torch.equal(replayed, eager)
         blk.commit(plan, int(plan.used[0]))
+
+
+@pytest.mark.parametrize("why", ["pages", "width"])
+def test_a_step_whose_tokens_find_no_page_is_refused(weights, why):
+    blk, fresh = make(weights), make(weights)
+    x = synthetic.activation(23, 4096, torch.bfloat16, seed=1).to(DEV)
+    for one in (blk, fresh):
+        one.step(x, [20, 3, 0])
+    held = blk.free
+    if why == "pages":
+        blk.free, lens = held[:1].contiguous(), [100, 1, 1]
+    else:
+        lens = [1, 640, 1]  # 643 tokens, the table's 19 pages hold 608
+    before = [t.clone() for t in (*blk.cache, blk.kv_lens, blk.free)]
+    with pytest.raises(RuntimeError, match="page"):
+        blk.step(synthetic.activation(sum(lens), 4096, torch.bfloat16, seed=2).to(DEV), lens)
+    for a, t in zip(before, (*blk.cache, blk.kv_lens, blk.free)):
+        assert torch.equal(a, t)
+    # with pages again it goes on as if nothing had been tried
+    blk.free = held
+    x = synthetic.activation(42, 4096, torch.bfloat16, seed=3).to(DEV)
+    assert torch.equal(blk.step(x, [40, 1, 1]), fresh.step(x, [40, 1, 1]))
+    assert torch.equal(blk.kv_lens, fresh.kv_lens) and torch.equal(blk.free, fresh.free)
