@@ -60,7 +60,8 @@ class PagedAttentionBlock:
         self.table = torch.full((requests, self.width), -1, dtype=torch.int32, device=dev)
         self.free = torch.arange(num_pages, dtype=torch.int32, device=dev)
         self.kv_lens = torch.zeros(requests, dtype=torch.int32, device=dev)
-        self.cos_sin = rotation_table(max_tokens, device=dev)
+        # (a request's last page can hold tokens past max_tokens)
+        self.cos_sin = rotation_table(self.width * page_size, device=dev)
         self.out_scale = torch.full((1,), attention_scale, dtype=torch.float32, device=dev)
         self.ws = b.workspace(dev)
 

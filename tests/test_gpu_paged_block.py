@@ -155,3 +155,12 @@ def test_a_step_whose_tokens_find_no_page_is_refused(weights, why):
     x = synthetic.activation(42, 4096, torch.bfloat16, seed=3).to(DEV)
     assert torch.equal(blk.step(x, [40, 1, 1]), fresh.step(x, [40, 1, 1]))
     assert torch.equal(blk.kv_lens, fresh.kv_lens) and torch.equal(blk.free, fresh.free)
+
+
+def test_the_last_page_of_a_request_is_rotated_by_its_positions(weights):
+    # 600 tokens at most are 19 pages of 32: the table takes 608
+    blk, wide = make(weights), make(weights)
+    wide.cos_sin = rotation_table(608, device=DEV)
+    x = synthetic.activation(608, 4096, torch.bfloat16, seed=5).to(DEV)
+    assert torch.equal(blk.step(x, [0, 608, 0]), wide.step(x, [0, 608, 0]))
+    assert torch.equal(blk.cache.k, wide.cache.k)
