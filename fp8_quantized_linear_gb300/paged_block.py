@@ -91,6 +91,15 @@ class PagedAttentionBlock:
         self.kv_lens.copy_(plan.kv_lens)
         self.free = self.free[pages_taken:].contiguous()
 
+    def release(self, request: int) -> None:
+        """Ends a request: its pages return to the free list, and another
+        request can take its place.  (A page starts anew, codes and scales,
+        when a token is written at its offset 0.)"""
+        pages = -(-int(self.kv_lens[request]) // self.page_size)
+        self.free = torch.cat([self.free, self.table[request, :pages]])
+        self.table[request] = -1
+        self.kv_lens[request] = 0
+
     def step(self, x: torch.Tensor, q_lens: list[int]) -> torch.Tensor:
         """plan, forward and commit of one step, with the lengths on the host.
         Raises before anything is computed when a token finds no page (too few

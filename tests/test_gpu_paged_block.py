@@ -164,3 +164,22 @@ def test_the_last_page_of_a_request_is_rotated_by_its_positions(weights):
     x = synthetic.activation(608, 4096, torch.bfloat16, seed=5).to(DEV)
     assert torch.equal(blk.step(x, [0, 608, 0]), wide.step(x, [0, 608, 0]))
     assert torch.equal(blk.cache.k, wide.cache.k)
+
+
+def test_a_finished_request_gives_its_pages_back(weights):
+    blk, fresh = make(weights), make(weights)
+    first = synthetic.activation(230, 4096, torch.bfloat16, seed=1).to(DEV)
+    blk.step(first, [130, 0, 100])
+    fresh.step(first[130:].contiguous(), [0, 0, 100])
+    blk.free = blk.free[:0].contiguous()
+    blk.release(0)
+    assert blk.free.numel() == 5 and blk.kv_lens.tolist() == [0, 0, 100]
+    # another request in its place, on the same pages: five, and no more
+    for n, lens in enumerate(([157, 0, 1], [1, 0, 1], [2, 0, 0])):
+        x = synthetic.activation(sum(lens), 4096, torch.bfloat16, seed=2 + n).to(DEV)
+        assert torch.equal(blk.step(x, lens), fresh.step(x, lens))
+    assert blk.free.numel() == 0 and blk.kv_lens.tolist() == [160, 0, 102]
+    with pytest.raises(RuntimeError, match="page"):
+        blk.step(first[:1], [1, 0, 0])
+    blk.release(1)  # a request without tokens has nothing to give
+    assert blk.free.numel() == 0
