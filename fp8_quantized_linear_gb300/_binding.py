@@ -595,8 +595,9 @@ def fp8_kv_plan(q_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.
     front; tokens: rows of the step's token tensors.  Returns KvPlan
     (q_offsets [R + 1], kv_lens after the step [R], positions and slots
     [tokens], used [2]: pages taken, tokens without a page, which have to be 0
-    for the step to go on to fp8_kv_attention), in `plan`'s tensors when
-    given."""
+    for the step to go on to fp8_kv_attention), in `plan`'s tensors when given:
+    none may share memory with an input or another, but plan.kv_lens may be
+    the kv_lens given."""
     index = _kv_device(q_lens)
     given = (q_lens, kv_lens, block_table, free_pages)
     if not _kv_placed(index, given):

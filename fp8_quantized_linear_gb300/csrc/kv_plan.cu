@@ -152,6 +152,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
     }
 }
 
+// An int32 array of the call
+struct Span {
+    const int32_t *at;
+    int64_t n;
+    bool meets(const Span &o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+        return n > 0 && o.n > 0 && a < b + 4 * static_cast<uintptr_t>(o.n) && b < a + 4 * static_cast<uintptr_t>(n);
+    }
+};
+
 }  // namespace
 }  // namespace fp8l
 
@@ -174,6 +184,18 @@ extern "C" int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_
                             static_cast<const void *>(positions), static_cast<const void *>(slots),
                             static_cast<const void *>(used)})
         if (!aligned4(ptr)) return FP8L_EALIGN;
+    // Every block reads all inputs while others write outputs, so none may
+    // share memory; only the lengths may be updated in place (below).
+    const bool in_place = kv_lens_out == kv_lens;
+    const Span inputs[3] = {{q_lens, requests}, {free_pages, num_free}, {kv_lens, requests}};
+    const Span outputs[6] = {{block_table, requests * table_width}, {q_offsets, requests + 1}, {positions, tokens},
+                             {slots, tokens}, {used, 2}, {kv_lens_out, requests}};
+    for (int i = 0; i < 6; ++i) {
+        for (int j = 0; j < 3; ++j)
+            if (!(in_place && i == 5 && j == 2) && outputs[i].meets(inputs[j])) return FP8L_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (outputs[i].meets(outputs[j])) return FP8L_EINVAL;
+    }
     int sms = 0;
     if (int st = check_device(&sms); st != FP8L_OK) return st;
     PlanParams p;
@@ -197,7 +219,10 @@ extern "C" int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_
         cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
         return FP8L_ECUDA;
-    const int64_t want = (tokens + kPlanRowsPerBlock - 1) / kPlanRowsPerBlock;
+    // In place, one block: each thread reads a request's length before it writes
+    // it, and nobody else reads it.  Measured (us, apart / in place): 64 decoding
+    // 3.0 / 3.0, 12 requests with 19927 rows 4.2 / 16.9, 1021 with 24699 7.6 / 47
+    const int64_t want = in_place ? 1 : (tokens + kPlanRowsPerBlock - 1) / kPlanRowsPerBlock;
     const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : (want > sms ? sms : want));
     return launch_dependent(kv_plan_kernel, dim3(grid), kPlanThreads, smem, as_stream(stream), p);
 }

@@ -473,7 +473,9 @@ FP8L_API int fp8_quant_per_tensor_noalloc(const void *x, int x_dtype, int64_t ro
  * q_lens, kv_lens: int32 [requests]; block_table: int32 [requests,
  * table_width], in and out; free_pages: int32 [num_free].  No input other
  * than block_table is written, so a call may be repeated with the same
- * result.  1 <= requests <= 8192, 0 <= tokens < 2^31, table_width >= 1,
+ * result; except that kv_lens_out may be kv_lens itself, whose lengths the
+ * call then replaces.  Any other overlap of an output with an input or another
+ * output is FP8L_EINVAL.  1 <= requests <= 8192, 0 <= tokens < 2^31, table_width >= 1,
  * num_free * page_size < 2^31,
  * the sums of the lengths fit an int32. */
 FP8L_API int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_t requests,

@@ -77,3 +77,35 @@ def test_table_width_limits_a_request():
 def test_most_requests():
     rng = np.random.default_rng(5)
     check(rng.integers(0, 3, 8192), rng.integers(0, 50, 8192), 16, seed=2)
+
+
+@pytest.mark.parametrize("R,most", [(3, 9), (40, 300), (1500, 40)])
+def test_a_plan_reused_step_after_step(R, most):
+    # the lengths updated in place and all tensors reused; up to 30000 rows
+    # (several blocks, if the lengths were not shared)
+    rng = np.random.default_rng(R)
+    page, width = 16, 200
+    table, pages = np.full((R, width), -1), rng.permutation(R * width)
+    lens, tokens = np.zeros(R, int), R * most
+    dev_table, dev_lens = i32(table), i32(lens)
+    plan = None
+    for _ in range(4):
+        q = rng.integers(0, most + 1, R)
+        want = kv_ref.plan(q, lens, table, pages, tokens, page)
+        given = None if plan is None else plan._replace(kv_lens=dev_lens)
+        plan = fl.fp8_kv_plan(i32(q), dev_lens, dev_table, i32(pages), tokens, page, plan=given)
+        for name in ("q_offsets", "kv_lens", "positions", "slots", "used"):
+            assert np.array_equal(getattr(plan, name).cpu().numpy(), want[name]), name
+        assert np.array_equal(dev_table.cpu().numpy(), want["table"])
+        table, lens, pages = want["table"], want["kv_lens"], pages[want["used"][0]:]
+        dev_lens = plan.kv_lens
+
+
+def test_outputs_over_inputs_are_refused():
+    q, kv, table, free = i32([3, 2]), i32([4, 5]), i32(np.full((2, 4), -1)), i32(np.arange(9))
+    plan = fl.fp8_kv_plan(q, kv, table, free, 5, 16)
+    for given in (plan._replace(kv_lens=q), plan._replace(positions=free[:5]),
+                  plan._replace(slots=plan.positions), plan._replace(used=kv)):
+        with pytest.raises(fl.Fp8LinearError) as e:
+            fl.fp8_kv_plan(q, kv, table, free, 5, 16, plan=given)
+        assert e.value.status == 1
