@@ -6,8 +6,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <atomic>
-
 #include "kv_attention_decode.cuh"
 #include "kv_attention_params.cuh"
 #include "kv_attention_prompt.cuh"
@@ -29,19 +27,6 @@ static_assert(kAttnCountersOffset + 4 * kDecLevels * 2 * 2 * kDecMaxCtas <= kAtt
 
 constexpr int kSmemPerSm = 227 * 1024;  // what the CTAs of an SM can ask for, each with 1 KB of its own
 
-// Raises a kernel's shared-memory limit once per device.
-template <typename Kernel>
-int allow_smem(Kernel kernel, int smem, std::atomic<unsigned long long> &ready) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FP8L_ECUDA;
-    if (ready.load(std::memory_order_acquire) >> dev & 1u) return FP8L_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
-        return FP8L_ECUDA;
-    ready.fetch_or(1ull << dev, std::memory_order_release);
-    return FP8L_OK;
-}
-
 template <int QDT, int DIM, int GROUPS>
 int launch_decode(AttnParams p, int sms, cudaStream_t stream) {
     using Sh = DecShape<QDT, DIM, GROUPS>;
@@ -52,7 +37,7 @@ int launch_decode(AttnParams p, int sms, cudaStream_t stream) {
     const int smem = p.stages * Sh::kStageBytes + Sh::kFixedBytes;
     static std::atomic<unsigned long long> ready{0};
     auto kernel = kv_attention_decode_kernel<QDT, DIM, GROUPS>;
-    if (int st = allow_smem(kernel, smem, ready); st != FP8L_OK) return st;
+    if (int st = allow_smem(kernel, smem, ready, true); st != FP8L_OK) return st;
     const int most = kDecMaxCtas / 2 * Sh::kCtasPerSm, ctas = Sh::kCtasPerSm * sms;
     return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), Sh::kThreads, smem, stream,
                             p);
@@ -63,7 +48,7 @@ int launch_prompt(const AttnParams &p, int sms, cudaStream_t stream) {
     constexpr int smem = ProSmem<QDT, DIM>::kBytes;
     static std::atomic<unsigned long long> ready{0};
     auto kernel = kv_attention_prompt_kernel<QDT, DIM>;
-    if (int st = allow_smem(kernel, smem, ready); st != FP8L_OK) return st;
+    if (int st = allow_smem(kernel, smem, ready, true); st != FP8L_OK) return st;
     return launch_dependent(kernel, dim3(static_cast<unsigned>(sms < kProMaxCtas ? sms : kProMaxCtas)), kProThreads,
                             smem, stream, p);
 }

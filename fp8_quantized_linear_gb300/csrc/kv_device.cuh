@@ -2,6 +2,8 @@
 // arithmetic, the programmatic launch, the host checks of a cache.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace fp8l {
@@ -20,6 +22,23 @@ inline bool kv_page_size_ok(int64_t page_size) {
 }
 
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Raises a kernel's shared-memory limit to `smem`, the most that any of its
+// launches asks for, once per device (`ready` has a bit for each): a limit set
+// for every launch could be lowered by another thread before the launch.
+// `all_shared`: the SM's memory split in favour of shared memory.
+template <typename Kernel>
+inline int allow_smem(Kernel kernel, int smem, std::atomic<unsigned long long> &ready, bool all_shared) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FP8L_ECUDA;
+    if (ready.load(std::memory_order_acquire) >> dev & 1u) return FP8L_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        (all_shared &&
+         cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess))
+        return FP8L_ECUDA;
+    ready.fetch_or(1ull << dev, std::memory_order_release);
+    return FP8L_OK;
+}
 
 // Launches `kernel` as a programmatic dependent of the preceding kernel on
 // the stream: its blocks may become resident before that kernel ends, and

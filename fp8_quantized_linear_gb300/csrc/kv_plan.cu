@@ -215,10 +215,10 @@ extern "C" int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_
     p.used = used;
     // up to 96 KB of prefix sums (8192 requests)
     const size_t smem = 3 * sizeof(int) * static_cast<size_t>(requests);
-    if (smem > 47 * 1024 &&
-        cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-        return FP8L_ECUDA;
+    static std::atomic<unsigned long long> ready{0};
+    if (smem > 47 * 1024)
+        if (int st = allow_smem(kv_plan_kernel, 3 * sizeof(int) * kKvMaxRequests, ready, false); st != FP8L_OK)
+            return st;
     // In place, one block: each thread reads a request's length before it writes
     // it, and nobody else reads it.  Measured (us, apart / in place): 64 decoding
     // 3.0 / 3.0, 12 requests with 19927 rows 4.2 / 16.9, 1021 with 24699 7.6 / 47

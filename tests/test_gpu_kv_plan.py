@@ -109,3 +109,32 @@ def test_outputs_over_inputs_are_refused():
         with pytest.raises(fl.Fp8LinearError) as e:
             fl.fp8_kv_plan(q, kv, table, free, 5, 16, plan=given)
         assert e.value.status == 1
+
+
+def test_threads_that_plan_different_numbers_of_requests():
+    # both need more shared memory than a launch gets by default
+    import threading
+    errors = []
+
+    def work(R):
+        try:
+            rng = np.random.default_rng(R)
+            q, kv = rng.integers(0, 3, R), rng.integers(0, 50, R)
+            table, pages = np.full((R, 4), 7), np.arange(2 * R)
+            want = kv_ref.plan(q, kv, table, pages, 100, 16)
+            args = i32(q), i32(kv), i32(table), i32(pages), 100, 16
+            with torch.cuda.stream(torch.cuda.Stream(DEV)):
+                for _ in range(500):
+                    plan = fl.fp8_kv_plan(*args)
+                assert np.array_equal(plan.kv_lens.cpu().numpy(), want["kv_lens"])
+                assert np.array_equal(plan.slots.cpu().numpy(), want["slots"])
+        except Exception as e:  # noqa: BLE001 - reported by the main thread
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(R,)) for R in (8192, 4100, 6000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
