@@ -37,6 +37,11 @@ struct PlanParams {
     int32_t *q_offsets, *kv_lens_out, *positions, *slots, *used;
 };
 
+// Blocks of n tokens (n + P - 1 may not fit an int)
+__device__ __forceinline__ int blocks_of(int n, int page_shift) {
+    return (n >> page_shift) + ((n & ((1 << page_shift) - 1)) != 0 ? 1 : 0);
+}
+
 // Exclusive prefix sum over the block of one value per thread, plus `carry`;
 // carry grows by the block's total.
 __device__ __forceinline__ int block_scan(int v, int &carry, int *red) {
@@ -92,15 +97,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         const int q = mine ? max(p.q_lens[r], 0) : 0;
         const int at = min(block_scan(q, rows, red), T);
         const int total = kv + min(q, T - at);
-        const int old = (kv + P - 1) >> p.page_shift;
-        const int need = max(min((total + P - 1) >> p.page_shift, p.table_width) - old, 0);
+        const int old = blocks_of(kv, p.page_shift);
+        const int need = max(min(blocks_of(total, p.page_shift), p.table_width) - old, 0);
         const int b = block_scan(need, blocks, red);
         if (mine) {
             off[r] = at;
             base[r] = b;
             cached[r] = kv;
             const int got = min(max(p.num_free - b, 0), need);
-            const int after = min(total, (old + got) << p.page_shift);
+            const int after = static_cast<int>(
+                min(static_cast<int64_t>(total), static_cast<int64_t>(old + got) << p.page_shift));
             lost += total - after;
             if (blockIdx.x == 0) {
                 p.q_offsets[r] = at;
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
     const int first = static_cast<int>(blockIdx.x) * kPlanThreads + static_cast<int>(threadIdx.x);
     for (int k = first; k < blocks; k += stride) {
         const int r = last_not_above(base, R, k);
-        const int old = (cached[r] + P - 1) >> p.page_shift;
+        const int old = blocks_of(cached[r], p.page_shift);
         p.block_table[static_cast<int64_t>(r) * p.table_width + old + (k - base[r])] =
             k < p.num_free ? p.free_pages[k] : -1;
     }
@@ -135,7 +141,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
             const int r = last_not_above(off, R, t);
             const int kv = cached[r];
             pos = kv + t - off[r];
-            const int b = pos >> p.page_shift, old = (kv + P - 1) >> p.page_shift;
+            const int b = pos >> p.page_shift, old = blocks_of(kv, p.page_shift);
             int page = -1;
             if (b < p.table_width) {
                 if (b < old) {

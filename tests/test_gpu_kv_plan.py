@@ -138,3 +138,17 @@ def test_threads_that_plan_different_numbers_of_requests():
     for t in threads:
         t.join()
     assert not errors, errors
+
+
+@pytest.mark.parametrize("kv", [2 ** 31 - 1, 2 ** 31 - 60, 2 ** 31 - 200])
+@pytest.mark.parametrize("page", [16, 128])
+def test_lengths_up_to_32_bits(page, kv):
+    t = i32([[3, 3, 3], [7, 7, 7]])
+    plan = fl.fp8_kv_plan(i32([0, 5]), i32([kv, 3]), t, i32([4, 5]), 5, page)
+    assert plan.kv_lens.tolist() == [kv, 8] and plan.used.tolist() == [0, 0]
+    assert plan.slots.tolist() == [7 * page + 3 + i for i in range(5)]
+    # new tokens beyond the table have no page
+    plan = fl.fp8_kv_plan(i32([0, 5]), i32([3, kv - 200]), t, i32([4, 5]), 5, page)
+    full = -(-(kv - 200) // page) * page
+    assert plan.kv_lens.tolist() == [3, min(kv - 195, full)]
+    assert plan.used.tolist() == [0, max(kv - 195 - full, 0)] and plan.slots.tolist() == [-1] * 5
