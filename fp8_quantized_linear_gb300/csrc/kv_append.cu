@@ -476,7 +476,8 @@ extern "C" int fp8_qk_norm_rope_append(const void *qkv, int dtype, int64_t token
     if (dtype != FP8L_F16 && dtype != FP8L_BF16) return FP8L_EINVAL;
     if (!(eps >= 0.0f) || eps > 3.0e38f) return FP8L_EINVAL;
     if (tokens < 0 || tokens > INT32_MAX || (head_dim != 64 && head_dim != 128) || kv_heads < 1 ||
-        q_heads < kv_heads || q_heads % kv_heads != 0 || (q_heads + 2 * kv_heads) * head_dim > (1 << 20) ||
+        q_heads < kv_heads || q_heads > (1 << 20) || q_heads % kv_heads != 0 ||
+        (q_heads + 2 * kv_heads) * head_dim > (1 << 20) ||
         qkv_stride < (q_heads + 2 * kv_heads) * head_dim || qkv_stride % 8 != 0 || rot < 0 || rot > head_dim ||
         rot % 16 != 0 || (rot > 0 && (max_positions < 1 || max_positions > INT32_MAX)) ||
         !kv_page_size_ok(page_size) || num_pages < 1 || num_pages > INT32_MAX / page_size)

@@ -98,8 +98,8 @@ int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_strid
         !(sm_scale > 0.0f) || sm_scale > 3.0e38f)
         return FP8L_EINVAL;
     if (tokens < 0 || tokens > INT32_MAX || (head_dim != 64 && head_dim != 128) || kv_heads < 1 ||
-        q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads * head_dim > (1 << 20) ||
-        q_stride < q_heads * head_dim || q_stride % 8 != 0 || !kv_page_size_ok(page_size) || num_pages < 1 ||
+        q_heads < kv_heads || q_heads > (1 << 20) || q_heads % kv_heads != 0 || q_heads * head_dim > (1 << 20) ||
+        tokens * q_heads > INT32_MAX - kProRows || q_stride < q_heads * head_dim || q_stride % 8 != 0 || !kv_page_size_ok(page_size) || num_pages < 1 ||
         num_pages > INT32_MAX / page_size || table_width < 1 || table_width > INT32_MAX || requests < 1 ||
         requests > kKvMaxRequests || max_q_len < 0 || window < 0)
         return FP8L_ESHAPE;
@@ -113,7 +113,6 @@ int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_strid
     int sms = 0;
     if (int st = check_device(&sms); st != FP8L_OK) return st;
     if (tokens == 0 || max_q_len == 0) return FP8L_OK;
-    if (tokens * q_heads > INT32_MAX) return FP8L_ESHAPE;
     AttnParams p;
     p.q = static_cast<const uint16_t *>(q);
     p.tokens = static_cast<int>(tokens);

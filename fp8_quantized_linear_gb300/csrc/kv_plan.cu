@@ -179,7 +179,7 @@ extern "C" int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_
     using namespace fp8l;
     if (requests < 1 || requests > kKvMaxRequests || tokens < 0 || tokens > INT32_MAX ||
         !kv_page_size_ok(page_size) || table_width < 1 || table_width > INT32_MAX || num_free < 0 ||
-        num_free * page_size > INT32_MAX)
+        num_free > INT32_MAX / page_size)
         return FP8L_ESHAPE;
     if (!q_lens || !kv_lens || !block_table || (!free_pages && num_free > 0) || !q_offsets || !kv_lens_out ||
         ((!positions || !slots) && tokens > 0) || !used)

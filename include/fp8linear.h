@@ -567,7 +567,8 @@ FP8L_API int fp8l_capture_id(void *stream, unsigned long long *id);
  * out: [tokens, q_heads, head_dim] of out_dtype: q_dtype, or FP8L_E4M3 codes
  * of out / out_scale[0] (the static input scale of the o product); rows
  * outside the requests are not written.  lse: NULL or float [tokens,
- * q_heads].  0 <= window; 0 < sm_scale, finite.  1 <= requests <= 8192.
+ * q_heads].  0 <= window; 0 < sm_scale, finite.  1 <= requests <= 8192;
+ * q_heads * head_dim <= 2^20; tokens * q_heads < 2^31 - 256.
  * Deterministic: the same call gives the same bits. */
 FP8L_API int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_stride,
                               int64_t q_heads, int64_t kv_heads, int64_t head_dim,

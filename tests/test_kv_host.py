@@ -38,3 +38,30 @@ def test_plan_outputs_may_not_share_memory(lib):
                 if (o, other) == ("out", "kv") and at == ok["kv"]:
                     continue  # the lengths in place
                 assert call(**{o: at}) == b.EINVAL, (o, other, at)
+
+
+BIG = 2 ** 57  # times 128 wraps around to 0
+
+
+def test_sizes_whose_products_wrap_around(lib):
+    A = 0x10000
+    plan = dict(q=A, kv=A, R=4, T=9, page=64, table=A, W=3, free=A, F=5, off=A, out=A, pos=A, slots=A,
+                used=A, st=None)
+    append = dict(x=A, dt=b.BF16, T=9, ld=48 * 128, hq=32, hkv=8, dim=128, qg=A, kg=A, eps=1e-6,
+                  cs=A, mp=100, rot=128, il=0, pos=A, slots=A, q=A, k=A, v=A, ks=A, vs=A, pages=7,
+                  page=64, st=None)
+    attention = dict(q=A, dt=b.F16, T=9, ld=32 * 128, hq=32, hkv=8, dim=128, k=A, v=A, ks=A, vs=A,
+                     pages=7, page=64, table=A, W=3, off=A, kv=A, R=4, n=3, scale=0.1, window=0,
+                     os=A, out=A, od=b.F16, lse=None, ws=A, st=None)
+    for f, ok, bad in ((lib.fp8_kv_plan, plan, (dict(F=BIG, page=128), dict(F=2 ** 58 + 1),
+                                                dict(F=2 ** 62))),
+                       (lib.fp8_qk_norm_rope_append, append,
+                        (dict(hq=BIG), dict(hq=BIG, hkv=BIG), dict(hq=BIG, hkv=2 ** 56),
+                         dict(hq=2 ** 62, hkv=2 ** 61))),
+                       (lib.fp8_kv_attention, attention,
+                        (dict(hq=BIG), dict(hq=BIG, hkv=BIG), dict(hq=2 ** 62, hkv=2 ** 61),
+                         # rows of a tile past the last are numbered too
+                         dict(T=2 ** 31 - 1, hq=1, hkv=1, ld=128),
+                         dict(T=2 ** 24, hq=128, ld=128 * 128)))):
+        for kw in bad:
+            assert f(*dict(ok, **kw).values()) == b.ESHAPE, (f.__name__, kw)
