@@ -1,8 +1,10 @@
 """Host side of the paged FP8 cache entry points and their binding, without a
 GPU: no kernel is launched and no address dereferenced."""
+import contextlib
 import ctypes
 
 import pytest
+import torch
 
 import fp8_quantized_linear_gb300 as fl
 import fp8_quantized_linear_gb300._binding as b
@@ -65,3 +67,29 @@ def test_sizes_whose_products_wrap_around(lib):
                          dict(T=2 ** 24, hq=128, ld=128 * 128)))):
         for kw in bad:
             assert f(*dict(ok, **kw).values()) == b.ESHAPE, (f.__name__, kw)
+
+
+class FakeLibrary:
+    """The entry points that fp8l_read_status uses, after a time-out."""
+    asked = None
+
+    def fp8l_read_status(self, ws, stream):
+        return b.ETIMEOUT
+
+    def fp8_kv_attention_workspace_bytes(self):
+        return 4096
+
+    def fp8_kv_attention_workspace_zero_bytes(self):
+        return 1024
+
+
+@pytest.mark.parametrize("extra", [0, 16, 5000])
+def test_counters_are_zeroed_after_a_time_out_whatever_the_workspace_has_beyond(monkeypatch, extra):
+    monkeypatch.setattr(b, "load", lambda: FakeLibrary())
+    monkeypatch.setattr(b, "_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
+    ws = torch.ones(4096 + extra, dtype=torch.uint8)
+    assert fl.fp8l_read_status(ws) == b.ETIMEOUT
+    assert bool((ws[:1024] == 0).all()) and bool((ws[1024:] == 1).all())
+    small = torch.ones(512, dtype=torch.uint8)  # no attention workspace
+    assert fl.fp8l_read_status(small) == b.ETIMEOUT and bool((small == 1).all())
