@@ -145,10 +145,15 @@ def fp8l_workspace_bytes() -> int:
     return int(load().fp8l_workspace_bytes())
 
 
+def _device_index(device) -> int:
+    """Index of a CUDA device; the current one's when it names none."""
+    index = None if device is None else torch.device(device).index
+    return torch.cuda.current_device() if index is None else index
+
+
 def workspace(device=None) -> torch.Tensor:
     """A zero-filled workspace for `device`, allocated once and reused."""
-    device = torch.device("cuda", torch.cuda.current_device() if device is None
-                          else torch.device(device).index or 0)
+    device = torch.device("cuda", _device_index(device))
     ws = _workspaces.get(device)
     if ws is None:
         ws = torch.zeros(fp8l_workspace_bytes(), dtype=torch.uint8, device=device)
@@ -715,10 +720,7 @@ def fp8_kv_attention_workspace(device=None) -> torch.Tensor:
     capture gets a workspace of its own for each of its streams, from the
     graph's memory, whose counters every replay zeroes first, so a graph may
     be replayed on any stream and beside eager calls."""
-    if isinstance(device, int):
-        index = device
-    else:
-        index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    index = device if isinstance(device, int) else _device_index(device)
     key = (index, _stream_handle(index))
     capture = _capture_id(*key)
     if capture:

@@ -93,3 +93,19 @@ def test_counters_are_zeroed_after_a_time_out_whatever_the_workspace_has_beyond(
     assert bool((ws[:1024] == 0).all()) and bool((ws[1024:] == 1).all())
     small = torch.ones(512, dtype=torch.uint8)  # no attention workspace
     assert fl.fp8l_read_status(small) == b.ETIMEOUT and bool((small == 1).all())
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_a_device_without_an_index_is_the_current_one(monkeypatch, current):
+    def on(index):
+        return torch.device("cuda", index)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(b, "_stream_handle", lambda index: 0)
+    monkeypatch.setattr(b, "_workspaces", {on(i): ("workspace", i) for i in range(3)})
+    monkeypatch.setattr(b, "_attention_workspaces", {(i, 0): ("attention", i) for i in range(3)})
+    for get, name in ((fl.workspace, "workspace"), (fl.fp8_kv_attention_workspace, "attention")):
+        for device in (None, "cuda", torch.device("cuda")):
+            assert get(device) == (name, current)
+        for device in ("cuda:2", torch.device("cuda", 2)):
+            assert get(device) == (name, 2)
+        assert get("cuda:0") == (name, 0)
