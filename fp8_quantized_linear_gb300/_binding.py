@@ -62,6 +62,13 @@ def load():
             raise RuntimeError(
                 f"{LIB_PATH} has ABI version {version}, this binding needs {ABI_VERSION}: "
                 f"rebuild it with `python -c \"import __graft_entry__ as g; g.build()\"`")
+        # additions that kept the version: their symbols tell
+        missing = [name for name in ("fp8_kv_plan", "fp8_qk_norm_rope_append", "fp8_kv_attention",
+                                     "fp8l_capture_id") if not hasattr(lib, name)]
+        if missing:
+            raise RuntimeError(
+                f"{LIB_PATH} lacks {', '.join(missing)}: "
+                f"rebuild it with `python -c \"import __graft_entry__ as g; g.build()\"`")
         lib.fp8l_workspace_bytes.restype = ctypes.c_size_t
         lib.fp8l_workspace_bytes.argtypes = []
         lib.fp8l_strerror.restype = ctypes.c_char_p

@@ -2,6 +2,7 @@
 GPU: no kernel is launched and no address dereferenced."""
 import contextlib
 import ctypes
+import subprocess
 
 import pytest
 import torch
@@ -109,3 +110,15 @@ def test_a_device_without_an_index_is_the_current_one(monkeypatch, current):
         for device in ("cuda:2", torch.device("cuda", 2)):
             assert get(device) == (name, 2)
         assert get("cuda:0") == (name, 0)
+
+
+def test_a_stale_library_is_refused_by_name(monkeypatch, tmp_path):
+    # right version, but built before the paged cache's entry points
+    src, so = tmp_path / "old.c", tmp_path / "libold.so"
+    src.write_text("int fp8l_abi_version(void) { return %d; }\n" % b.ABI_VERSION)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    monkeypatch.setattr(b, "LIB_PATH", str(so))
+    monkeypatch.setattr(b, "_lib", None)
+    with pytest.raises(RuntimeError, match="rebuild"):
+        b.load()
+    assert b._lib is None
