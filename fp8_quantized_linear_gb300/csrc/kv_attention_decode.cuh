@@ -518,8 +518,7 @@ kv_attention_decode_kernel(const AttnParams p) {
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] *= up;
-                if (l == 0)
-                    qf[b * ROWS + row] = p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                if (l == 0) qf[b * ROWS + row] = part_factor(p.score_scale, m, e);
 #pragma unroll
                 for (int part = 0; part < Sh::kQParts; ++part) {
                     uint32_t c[4];
@@ -587,7 +586,8 @@ kv_attention_decode_kernel(const AttnParams p) {
                 const bool exists = key >= first && key < keys;
                 const float ks = exists ? scales[stage * 16 + pg] : 0.0f;
                 const float vs = exists ? scales[stage * 16 + 8 + pg] : 1.0f;
-                const float lv = __log2f(vs), rv = __frcp_rn(vs);
+                // (a NaN scale: in t, for the rows that see the key, alone)
+                const float lv = __log2f(vs), rv = __isnanf(vs) ? 0.0f : __frcp_rn(vs);
                 const float4 f0 = *reinterpret_cast<const float4 *>(qf + qb * ROWS);
                 const float4 f1 = *reinterpret_cast<const float4 *>(qf + qb * ROWS + 4);
                 const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
@@ -822,9 +822,9 @@ kv_attention_decode_kernel(const AttnParams p) {
                 }
             }
             if (write && valid) {
-                const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+                const float inv = 1.0f / ll;
 #pragma unroll
-                for (int v = 0; v < V; ++v) acc[v] = ll > 0.0f ? acc[v] * inv : 0.0f;
+                for (int v = 0; v < V; ++v) acc[v] = ll == 0.0f ? 0.0f : acc[v] * inv;
                 attn_store<V>(p, s->row0 + token, head, DIM, at, acc);
                 if ((tid & 15) == 0 && p.lse != nullptr) attn_store_lse(p, s->row0 + token, head, mm, ll);
             }

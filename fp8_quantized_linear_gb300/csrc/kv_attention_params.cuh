@@ -222,6 +222,12 @@ __device__ __forceinline__ int part_exponent(float m) {
     return min(134 - static_cast<int>(__float_as_uint(m) >> 23), 120);
 }
 
+// The factor of a row's scores, score_scale 2^-e; NaN when an element is not
+// finite (the parts of an infinity would be numbers)
+__device__ __forceinline__ float part_factor(float score_scale, float m, int e) {
+    return m < INFINITY ? score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
+}
+
 // ---------------------------------------------------------------- the line of tiles
 
 // A line of `total` tiles cut into `pieces` (below 2^15): piece c begins at
@@ -241,6 +247,22 @@ __device__ __forceinline__ int piece_of(long long total, long long at, long long
 
 constexpr float kLn2 = 0.693147180559945309f;
 
+// A row's sum l is 0 only when it sees no key (out 0, lse -inf); a NaN that it
+// met stays in l, and the row comes out as NaN, not as a row without keys.
+
+// E4M3 codes of four outputs; the code of a NaN is NaN (the saturating
+// quotient would clamp it to a number)
+__device__ __forceinline__ uint32_t attn_codes4(const float *o, const Quot &d) {
+    uint32_t c = codes_of_word<FP8L_F32, true>(make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]),
+                                                         __float_as_uint(o[2]), __float_as_uint(o[3])), d).x;
+    if (__isnanf(o[0]) || __isnanf(o[1]) || __isnanf(o[2]) || __isnanf(o[3])) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (__isnanf(o[i])) c |= 0x7Fu << (8 * i);
+    }
+    return c;
+}
+
 // VALS consecutive outputs of a row from dimension d on
 template <int VALS>
 __device__ __forceinline__ void attn_store(const AttnParams &p, int token, int head, int dim, int d,
@@ -256,10 +278,7 @@ __device__ __forceinline__ void attn_store(const AttnParams &p, int token, int h
             const Quot d = Quot::make<FP8L_F32>(s);
             uint32_t c[VALS / 4];
 #pragma unroll
-            for (int i = 0; i < VALS / 4; ++i)
-                c[i] = codes_of_word<FP8L_F32, true>(
-                           make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
-                                      __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3])), d).x;
+            for (int i = 0; i < VALS / 4; ++i) c[i] = attn_codes4(&o[4 * i], d);
             if constexpr (VALS % 16 == 0) {
 #pragma unroll
                 for (int i = 0; i < VALS / 4; i += 4)
@@ -292,7 +311,7 @@ __device__ __forceinline__ void attn_store(const AttnParams &p, int token, int h
 
 // lse from the reference m (base 2) and the sum l = sum 2^(s - m)
 __device__ __forceinline__ void attn_store_lse(const AttnParams &p, int token, int head, float m, float l) {
-    p.lse[static_cast<int64_t>(token) * p.q_heads + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    p.lse[static_cast<int64_t>(token) * p.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace

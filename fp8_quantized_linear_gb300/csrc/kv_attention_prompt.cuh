@@ -133,6 +133,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// The larger one, NaN when either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 __device__ __forceinline__ float max16(const uint32_t *v) {
     float m[5];
 #pragma unroll
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     const bool there = key <= last && key + 15 >= first;
                     const float ks = there ? sc[pg] : 0.0f, vs = there ? sc[8 + pg] : 1.0f;
                     reinterpret_cast<float4 *>(pro_smem + Sm::kFactorOff)[slot * 8 + tid] =
-                        make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.0f);
+                        make_float4(ks, __log2f(vs), __isnanf(vs) ? 0.0f : __frcp_rn(vs), 0.0f);
                     mbar_arrive(fcfull + 8 * slot);
                 }
                 constexpr int PIECES = kProKeys * DIM / 16 / 128;  // 16-byte pieces per thread
@@ -717,11 +724,10 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     mag = fold_mag<QDT>(mag);
                     mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 8));
                     mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 16));
-                    const int e = part_exponent(mag_bits_to_float<QDT>(mag));
+                    const float most = mag_bits_to_float<QDT>(mag);
+                    const int e = part_exponent(most);
                     const uint32_t up = static_cast<uint32_t>(127 + e) << 23;
-                    if (qc == 0)
-                        qf[32 * (warp & 3) + 8 * b + qr] =
-                            p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    if (qc == 0) qf[32 * (warp & 3) + 8 * b + qr] = part_factor(p.score_scale, most, e);
 #pragma unroll
                     for (int x = 0; x < CHUNKS; ++x) {
                         uint32_t h[8];  // the scaled row in fp16: exact from 2^-22 of its largest element on
@@ -753,7 +759,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 __syncwarp();  // the row factors are written
             }
             const float f = qf[tid];
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = __isnanf(f) ? f : 0.0f;
             for (int tile = begin; tile < end; ++tile, ++count, ++uses) {
                 // (a barrier per slot, not the key stage's, which may be
                 // filled again while this half is still in an epilogue)
@@ -838,7 +844,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                             const float4 k = fc[4 * x + y];
                             // (positive, so that -inf stays -inf where the
                             // factor is 0: a page that was not copied)
-                            const float a = fmaxf(f * k.x, 1e-37f), b = k.y - mu;
+                            const float a = max_nan(f * k.x, 1e-37f), b = k.y - mu;
                             const uint64_t a2 = f2_pack(__float_as_uint(a), __float_as_uint(a));
                             const uint64_t b2 = f2_pack(__float_as_uint(b), __float_as_uint(b));
                             uint64_t sum[2] = {0, 0};
@@ -968,7 +974,8 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
 #pragma unroll 1
                         for (int k = 0; k < members; ++k) {
                             const float2 ml = __ldcg(ml_of(partial((node + k) * step)));
-                            if (ml.x != -INFINITY) l = fmaf(ml.y, ex2(ml.x - top), l);
+                            // (a part without a reference: 0, or NaN)
+                            l = fmaf(ml.y, ml.x == -INFINITY ? 1.0f : ex2(ml.x - top), l);
                         }
                     }
                     m = top;
@@ -994,7 +1001,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                 // rows to the output's type in shared memory (the queries' are
                 // not needed any more), then out in whole rows: a store per
                 // row and thread would touch 32 lines
-                inv = l > 0.0f ? 1.0f / l : 0.0f;
+                inv = 1.0f / l;
                 const bool codes = p.out_dtype == FP8L_E4M3;
                 const int pieces = codes ? DIM / 16 : DIM / 8;  // 16 bytes each, per row
                 uint8_t *stage = pro_smem + half * Sm::kParts * Sm::kQPart + (warp & 3) * 32 * 2 * DIM;
@@ -1009,16 +1016,13 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     else
                         merge32(c, o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = l > 0.0f ? o[i] * inv : 0.0f;
+                    for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0.0f : o[i] * inv;
                     const int col = c;
                     if (codes) {
                         const Quot d = Quot::make<FP8L_F32>(p.out_scale[0]);
                         uint32_t w[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            w[i] = codes_of_word<FP8L_F32, true>(
-                                       make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
-                                                  __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3])), d).x;
+                        for (int i = 0; i < 8; ++i) w[i] = attn_codes4(&o[4 * i], d);
                         *at(lane, col / 16) = make_uint4(w[0], w[1], w[2], w[3]);
                         *at(lane, col / 16 + 1) = make_uint4(w[4], w[5], w[6], w[7]);
                     } else {

@@ -553,7 +553,8 @@ FP8L_API int fp8l_capture_id(void *stream, unsigned long long *id);
  *   s_j = sm_scale * q . k_j,    out = sum_j exp(s_j) v_j / sum_j exp(s_j),
  *   lse = ln sum_j exp(s_j)
  * with k_j, v_j the cache's values.  A row that sees no key gives out = 0
- * and lse = -inf.  Products and sums are float32 (the tensor core's
+ * and lse = -inf; one that meets a value that is not finite (outside the
+ * contract; also one hidden from it within the same 128 keys) gives NaN.  Products and sums are float32 (the tensor core's
  * accumulator); the softmax weights enter the second product rounded to at
  * least 11 bits, or 2^-25 of the row's largest weight.
  *
