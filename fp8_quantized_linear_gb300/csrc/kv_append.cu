@@ -60,9 +60,6 @@ struct AppendParams {
     int head_groups;  // ceil(q_heads / kAppHeadsPerGroup)
 };
 
-// The pages' blocks of a scale: values are never quantized with less
-constexpr float kKvMinScale = FP8L_KV_MIN_SCALE;
-
 // One row (a token's head) in a group of DIM / 8 lanes, eight dimensions each
 // as float pairs.  kSplit: a lane holds dimensions 4 l .. 4 l + 3 and
 // DIM / 2 + 4 l .. + 3, so that a rotation over the whole head in halves has

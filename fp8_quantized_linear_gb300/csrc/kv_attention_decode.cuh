@@ -585,7 +585,7 @@ kv_attention_decode_kernel(const AttnParams p) {
                 const int pg = tid >> p.page_shift;
                 const bool exists = key >= first && key < keys;
                 const float ks = exists ? scales[stage * 16 + pg] : 0.0f;
-                const float vs = exists ? scales[stage * 16 + 8 + pg] : 1.0f;
+                const float vs = exists ? value_scale(scales[stage * 16 + 8 + pg]) : 1.0f;
                 // (a NaN scale: in t, for the rows that see the key, alone)
                 const float lv = __log2f(vs), rv = __isnanf(vs) ? 0.0f : __frcp_rn(vs);
                 const float4 f0 = *reinterpret_cast<const float4 *>(qf + qb * ROWS);

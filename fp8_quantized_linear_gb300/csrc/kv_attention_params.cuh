@@ -216,6 +216,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A block's scale of values as the softmax takes it, by its logarithm and its
+// reciprocal: a smaller one (0 too, of a block of zeros not written here)
+// counts as the smallest
+__device__ __forceinline__ float value_scale(float s) { return s < kKvMinScale ? kKvMinScale : s; }
+
 // Exponent e with 2^7 <= m 2^e < 2^8, at most 120 (rows below 2^-113 lose
 // their last bits) so that 2^-e stays a normal float32; m >= 0
 __device__ __forceinline__ int part_exponent(float m) {

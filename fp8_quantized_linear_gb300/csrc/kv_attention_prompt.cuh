@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                                               p.wait_cycles);
                     const float *sc = reinterpret_cast<const float *>(pro_smem + Sm::kScaleOff) + slot * 16;
                     const bool there = key <= last && key + 15 >= first;
-                    const float ks = there ? sc[pg] : 0.0f, vs = there ? sc[8 + pg] : 1.0f;
+                    const float ks = there ? sc[pg] : 0.0f, vs = there ? value_scale(sc[8 + pg]) : 1.0f;
                     reinterpret_cast<float4 *>(pro_smem + Sm::kFactorOff)[slot * 8 + tid] =
                         make_float4(ks, __log2f(vs), __isnanf(vs) ? 0.0f : __frcp_rn(vs), 0.0f);
                     mbar_arrive(fcfull + 8 * slot);

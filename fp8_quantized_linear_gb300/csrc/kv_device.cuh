@@ -9,6 +9,7 @@
 namespace fp8l {
 
 constexpr int64_t kKvMaxRequests = 8192;
+constexpr float kKvMinScale = FP8L_KV_MIN_SCALE;  // of a page's block of keys or values
 
 // Byte offset of token `o` (in its page), dimension 16 c of page-and-head
 // `ph` = page * kv_heads + head: octets of tokens, then 16-byte chunks of

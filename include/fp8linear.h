@@ -433,7 +433,8 @@ FP8L_API int fp8_quant_per_tensor_noalloc(const void *x, int x_dtype, int64_t ro
  * d / 16, row o % 8, byte d % 16.  The 128-byte [8][16] blocks are the core
  * matrices the tensor core reads, and the tokens [8a, 8b) of a page and head
  * are one contiguous run of bytes.  k_scale and v_scale are
- * float32 [num_pages][kv_heads]: the value of a code c is dec(c) * scale.
+ * float32 [num_pages][kv_heads]: the value of a code c is dec(c) * scale.  A
+ * v_scale below FP8L_KV_MIN_SCALE (0 among them) is read as that.
  * num_pages * page_size < 2^31; head_dim is 64 or 128.  A block table is
  * int32 [requests][table_width]: entry [r][b] is the page of the tokens
  * [b * page_size, (b + 1) * page_size) of request r.

@@ -325,3 +325,15 @@ def test_references_that_move_in_every_tile(n, dtype):
     for _ in range(100):
         again, l2 = run(s, want_lse=True)
         assert torch.equal(first, again) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("n", [1, 3, 7, 60])
+def test_a_scale_of_zero_is_a_block_of_zeros(n):
+    s = make(torch.bfloat16, 64, 8, 2, 128, [n, n], [1000, 300], seed=33)
+    for r, L in enumerate(s["kv"]):
+        for b in range(0, -(-int(L) // 64), 2):
+            page = int(s["table"][r, b])
+            s["cache"].k_scale[page, 0] = s["cache"].v_scale[page] = 0.0
+            s["k"][r][0, b * 64:(b + 1) * 64] = 0
+            s["v"][r][:, b * 64:(b + 1) * 64] = 0
+    check(s)
