@@ -231,8 +231,11 @@ __device__ __forceinline__ uint2 row_codes(const Row &r, const Quot &d) {
     return make_uint2(codes_of_word<FP8L_F32, false>(a, d).x, codes_of_word<FP8L_F32, false>(b, d).x);
 }
 
+// The scale of a block of this largest magnitude.  A NaN among the values (the
+// largest of all bit patterns) stays in it: dropped, it would leave the
+// smallest scale, and the block's other values would be crushed by it.
 __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-    return fmaxf(__fdiv_rn(__uint_as_float(amax_bits), kE4M3Max), kKvMinScale);
+    return max_nan(__fdiv_rn(__uint_as_float(amax_bits), kE4M3Max), kKvMinScale);
 }
 
 // A page and head whose earlier tokens [0, offset) move to a larger scale
@@ -358,7 +361,7 @@ __device__ void append_unit(const AppendParams &p, int unit) {
         uint32_t m = max(row_mag(a), row_mag(b));
 #pragma unroll
         for (int x = LANES / 2; x > 0; x >>= 1) m = max(m, __shfl_xor_sync(mask, m, x, LANES));
-        const float s = fmaxf(block_scale(m), old);
+        const float s = max_nan(block_scale(m), old);
         const Quot d = Quot::make<FP8L_F32>(s);
         store(a, ph, o, d);
         if (n == 2) store(b, ph, o + 1, d);
@@ -396,7 +399,7 @@ __device__ void append_unit(const AppendParams &p, int unit) {
             uint32_t m = 0;
             each_row([&](const Row &r, int) { m = max(m, row_mag(r)); });
             m = block_max_u32(m, red);
-            const float s = fmaxf(block_scale(m), old);
+            const float s = max_nan(block_scale(m), old);
             const Quot d = Quot::make<FP8L_F32>(s);
             each_row([&](const Row &r, int i) { store(r, ph, o + i, d); });
             if (o > 0 && s > old) recast_block<DIM>(cache, Recast{ph, o, old, s}, P);

@@ -133,13 +133,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// The larger one, NaN when either is
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
 __device__ __forceinline__ float max16(const uint32_t *v) {
     float m[5];
 #pragma unroll

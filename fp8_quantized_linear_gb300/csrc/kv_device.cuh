@@ -60,6 +60,13 @@ inline int launch_dependent(void (*kernel)(Params), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FP8L_OK : FP8L_ECUDA;
 }
 
+// The larger one, NaN when either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 __device__ __forceinline__ void grid_dependency_sync() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -84,3 +84,26 @@ def test_codes_of_a_row_that_met_a_nan_are_nan(n):
         want = torch.zeros_like(nan)
         want[:n, :4, 65] = True
         assert torch.equal(nan, want)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("count", [1, 2, 40])  # runs of one or two tokens, and longer ones
+def test_a_page_that_is_given_a_value_that_is_not_finite_says_so(count, bad):
+    page, hkv, dim = 64, 2, 128
+    gen = torch.Generator().manual_seed(count)
+    x = torch.randn(count, 4 * dim + 2 * hkv * dim, generator=gen).bfloat16().to(DEV)
+    x[count - 1, 4 * dim + 3] = bad           # key head 0
+    x[0, 4 * dim + (hkv + 1) * dim + 9] = bad  # value head 1
+    cache = fl.kv_cache(3, page, hkv, dim, DEV)
+    pos = torch.arange(count, dtype=torch.int32, device=DEV)
+    slots = pos + 5 + page
+    cache.k_scale[1], cache.v_scale[1] = 0.01, 0.01
+    fl.fp8_qk_norm_rope_append(x, cache, pos, slots)
+    after = fl.fp8_qk_norm_rope_append(torch.ones_like(x[:1]), cache, pos[:1], slots[-1:] + 1)
+    assert bool(torch.isfinite(after).all())
+    for name, head in (("k_scale", 0), ("v_scale", 1)):
+        scale = getattr(cache, name)[1]
+        assert not math.isfinite(scale[head].item()) and math.isfinite(scale[1 - head].item())
+    # a request that takes the page over starts it anew
+    fl.fp8_qk_norm_rope_append(torch.ones_like(x[:1]), cache, pos[:1], pos[:1] + page)
+    assert bool(torch.isfinite(cache.k_scale[1]).all()) and bool(torch.isfinite(cache.v_scale[1]).all())
