@@ -13,10 +13,11 @@
 //
 // Precision.  The 16-bit query and the float32 weights enter as sums of E4M3
 // parts in columns of their own, each part the rounding of 16 times what the
-// parts before it left over: q, scaled by a power of two, is exact in two
-// parts for bf16 (an 8-bit significand is 4 + 4 bits with a sign) and in
-// three for fp16 (11 bits); a weight in three parts has 12 bits, or 2^-25 of
-// the running maximum.  The part columns are summed in float32.
+// parts before it left over.  A bf16 query (an 8-bit significand is 4 + 4 bits
+// with a sign), scaled so that its largest element is in [2^7, 2^8), is exact
+// in two parts from 2^-13 of that element on and within 2^-21 of it below; fp16
+// (11 bits) in three parts from 2^-14 on and within 2^-25.  A weight in three
+// parts has 12 bits, or 2^-25 of the running maximum.  The part columns are summed in float32.
 //
 // Softmax with block scales.  With k_j = sk c_j and v_j = sv d_j per page,
 //   t_j = log2(e) sm_scale q.k_j + log2 sv_j,   w_j = 2^(t_j - m),  m ~ max t

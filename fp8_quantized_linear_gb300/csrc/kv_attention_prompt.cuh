@@ -8,10 +8,13 @@
 // formed:
 //   S_X [128 rows x 128 keys] = Q_X K^T     (kind::f8f6f4, parts x D / 32 MMAs)
 //   O_X [128 rows x D]       += W_X V       (kind::f16, 8 MMAs, W in tensor memory)
-// K is multiplied as stored: a 16-bit query row, scaled by a power of two, is
-// the sum of two (bf16, exactly: 8 significand bits) or three (fp16) E4M3
-// parts, which share the accumulator; two fp8 MMAs take the time of one
-// 16-bit one and K is never widened.  The weights need a 16-bit format's
+// K is multiplied as stored: a 16-bit query row, scaled so that its largest
+// element is in [2^7, 2^8), is a sum of two (bf16, 8 significand bits) or three
+// (fp16, 11 bits) E4M3 parts.  They share the accumulator, so no part can be
+// scaled up and all stop at E4M3's step of 2^-9: elements from 2^-9 (bf16) or
+// 2^-6 (fp16) of the row's largest on are exact, smaller ones within 2^-17 of the
+// largest.  Two fp8 MMAs take the time of one 16-bit one and K is never
+// widened.  The weights need a 16-bit format's
 // range (a first token often draws most of a row's weight, leaving the others
 // below 2^-16 of it), so V is widened to fp16, exactly, once per key tile for
 // all 256 rows, by four warps of their own.
@@ -723,7 +726,9 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
                     if (qc == 0) qf[32 * (warp & 3) + 8 * b + qr] = part_factor(p.score_scale, most, e);
 #pragma unroll
                     for (int x = 0; x < CHUNKS; ++x) {
-                        uint32_t h[8];  // the scaled row in fp16: exact from 2^-22 of its largest element on
+                        // the scaled row in fp16: exact from 2^-22 of its
+                        // largest element on, further than the parts reach
+                        uint32_t h[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint4 &u = raw[0][2 * x + (i >> 2)];

@@ -558,7 +558,9 @@ FP8L_API int fp8l_capture_id(void *stream, unsigned long long *id);
  * with k_j, v_j the cache's values.  A row that sees no key gives out = 0
  * and lse = -inf; one that meets a value that is not finite (outside the
  * contract; also one hidden from it within the same 128 keys) gives NaN.  Products and sums are float32 (the tensor core's
- * accumulator); the softmax weights enter the second product rounded to at
+ * accumulator).  What enters them: a query element exactly or, far below its
+ * row's largest, within 2^-21 (bf16) or 2^-25 (fp16) of that one, with more than
+ * 32 rows per request and kv head within 2^-17; the softmax weights rounded to at
  * least 11 bits, or 2^-25 of the row's largest weight.
  *
  * q: [tokens, q_heads, head_dim] of q_dtype (FP8L_F16 or FP8L_BF16), rows

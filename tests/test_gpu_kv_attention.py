@@ -337,3 +337,47 @@ def test_a_scale_of_zero_is_a_block_of_zeros(n):
             s["k"][r][0, b * 64:(b + 1) * 64] = 0
             s["v"][r][:, b * 64:(b + 1) * 64] = 0
     check(s)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", [1, 3, 7, 60])
+def test_one_query_channel_a_thousand_times_the_others(n, dtype):
+    # The parts of a query stop at E4M3's step of 2^-9 under a row's largest
+    # element of 2^7 at least: up to 32 rows per kv head the last part is
+    # scaled by 16 (bf16) or 256 (fp16), so an element is within 2^-10 / 2^7 /
+    # 16 or / 256 of the largest, above within 2^-17.  Keys are 0 in the strong
+    # channel, so that the scores are those of the weak ones.
+    s = make(dtype, 64, 8, 2, 128, [n, n], [900, 300], seed=40)
+    s["q"][:, :, 3] = 1000.0
+    s["cache"].k[:, :, :, 0, :, 3] = 0
+    for k in s["k"]:
+        k[:, :, 3] = 0
+    got, lse = run(s, want_lse=True)
+    q = s["q"].double()
+    want, want_lse, spread, reach = kv_ref.attention(q, s["k"], s["v"], s["off"], s["kv"],
+                                                     128 ** -0.5, 0)
+    bits = 17 if 4 * n > 32 else (21 if dtype == torch.bfloat16 else 25)
+    keys = max(k.abs().sum(2).max().item() for k in s["k"])
+    score = (2.0 ** -bits * 1000 * keys * 128 ** -0.5 + 128 * 2.0 ** -24 * reach)[:, :, None]
+    top = np.nanmax(np.where(np.isnan(s["v_scale"]), 0, s["v_scale"]))
+    slack = spread * (2.0 ** -11 + 2.0 ** -17 + torch.expm1(2 * score)) + 900 * 448 * top * 2.0 ** -25
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11
+    err = (got.double() - want).abs()
+    assert bool((err <= slack + half * (want.abs() + slack) + 2.0 ** -25).all())
+    assert bool(((lse.double() - want_lse).abs() <=
+                 2.0 ** -18 * (1 + want_lse.abs()) + score[:, :, 0]).all())
+
+
+@pytest.mark.parametrize("n", [1, 90])
+def test_given_outputs(n):
+    s = make(torch.bfloat16, 64, 8, 2, 128, [n, n], [700, 90], seed=41)
+    want, want_lse = run(s, want_lse=True)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    got, got_lse = run(s, out=out, lse=lse)
+    assert got is out and got_lse is lse
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    scale = torch.full((1,), 0.02, device=DEV)
+    codes, _ = run(s, out_dtype=torch.uint8, out_scale=scale)
+    given = torch.empty(codes.shape, dtype=torch.float8_e4m3fn, device=DEV)
+    got, none = run(s, out=given, out_dtype=torch.float8_e4m3fn, out_scale=scale)
+    assert none is None and got is given and torch.equal(given.view(torch.uint8), codes)
