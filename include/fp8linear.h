@@ -510,7 +510,10 @@ FP8L_API int fp8_kv_plan(const int32_t *q_lens, const int32_t *kv_lens, int64_t 
  *            code  = E4M3(x / s)   (IEEE quotient, saturating, as
  *                    fp8_quant_per_tensor)
  *          and when s > s_old the codes of the page's earlier tokens become
- *          E4M3((dec(c) * s_old) / s).  Values that are not finite (outside
+ *          E4M3((dec(c) * s_old) / s): each growth re-rounds them, so a page
+ *          filled token by token holds its early tokens less exactly than
+ *          one written at once, and a token that is rejected later leaves
+ *          its scale behind.  Values that are not finite (outside
  *          the contract) give the page and head a scale that is not finite,
  *          until a token is written at its offset 0 again.
  * The slots of a page's tokens are ascending and consecutive in token order,

@@ -168,3 +168,52 @@ def test_appending_twice_is_the_same():
     first = [fl.fp8_qk_norm_rope_append(x, cache, pos, slot)] + [t.clone() for t in cache]
     again = [fl.fp8_qk_norm_rope_append(x, cache, pos, slot)] + list(cache)
     assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_a_given_q():
+    x = torch.randn(33, 12 * 128, device=DEV).bfloat16()
+    pos = torch.arange(33, dtype=torch.int32, device=DEV)
+    caches = [fl.kv_cache(4, 16, 2, 128, DEV) for _ in range(2)]
+    want = fl.fp8_qk_norm_rope_append(x, caches[0], pos, pos)
+    given = torch.empty_like(want)
+    assert fl.fp8_qk_norm_rope_append(x, caches[1], pos, pos, q=given) is given
+    assert torch.equal(given, want)
+    assert all(torch.equal(a, b) for a, b in zip(*caches))
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_a_page_filled_token_by_token_against_its_values(page):
+    """A scale that grows re-rounds the page's earlier codes.  A token written
+    when the block's maxima were a_1 <= .. <= a_i is rounded once, and again
+    at every later growth, each time by at most 2^-4 of the value at hand and
+    half a subnormal step, 2^-10 of the scale then; a page written at once is
+    rounded once."""
+    dim = 128
+    gen = torch.Generator().manual_seed(page)
+    x = torch.randn(page, 4 * dim, generator=gen)
+    x[:, 2 * dim:3 * dim] *= torch.linspace(0.5, 2, page)[:, None]  # keys grow in size
+    x = x.bfloat16().to(DEV)
+    pos = torch.arange(page, dtype=torch.int32, device=DEV)
+    slow, once = fl.kv_cache(2, page, 1, dim, DEV), fl.kv_cache(2, page, 1, dim, DEV)
+    for t in range(page):
+        fl.fp8_qk_norm_rope_append(x[t:t + 1], slow, pos[t:t + 1], pos[t:t + 1] + page)
+    fl.fp8_qk_norm_rope_append(x, once, pos, pos + page)
+    values = {"k": x[:, 2 * dim:3 * dim], "v": x[:, 3 * dim:]}
+    for name in ("k", "v"):
+        v = values[name].double().cpu().numpy()
+        top = np.maximum.accumulate(np.abs(v).max(1))  # the block's maximum after each token
+        decoded = []
+        for cache, by_token in ((slow, True), (once, False)):
+            s = getattr(cache, name + "_scale")[1, 0].double().item()
+            assert abs(s - top[-1] / 448) <= 2.0 ** -22 * s
+            got = kv_ref.TABLE[kv_ref.pages_view(getattr(cache, name))[1, 0]] * s
+            decoded.append(got)
+            for t in range(page):
+                scales = np.unique(top[t:]) / 448 if by_token else top[-1:] / 448
+                bound, size = 0.0, np.abs(v[t])
+                for s_i in scales * 1.0001:
+                    step = 2.0 ** -4 * (size + bound) * 1.0001 + 2.0 ** -10 * s_i
+                    bound = bound + step
+                assert np.all(np.abs(got[t] - v[t]) <= bound), (name, t)
+        slow_rms, once_rms = (np.sqrt(((d - v) ** 2).mean()) for d in decoded)
+        assert slow_rms >= once_rms * 0.99
