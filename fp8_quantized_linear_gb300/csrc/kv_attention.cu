@@ -81,7 +81,8 @@ int fp8l_capture_id(void *stream, unsigned long long *id) {
     if (stream == nullptr) return FP8L_OK;
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
     unsigned long long capture = 0;
-    if (cudaStreamGetCaptureInfo(fp8l::as_stream(stream), &status, &capture) != cudaSuccess) return FP8L_ECUDA;
+    if (cudaStreamGetCaptureInfo(fp8l::as_stream(stream), &status, &capture) != cudaSuccess)
+        return fp8l::cuda_failed();
     if (status == cudaStreamCaptureStatusActive) *id = capture;
     return FP8L_OK;
 }
@@ -138,7 +139,7 @@ int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_strid
     p.lse = lse;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.status = status_word(workspace);
-    if (int st = library_status_word(&p.library_status); st != FP8L_OK) return st;
+    if (library_status_word(&p.library_status) != FP8L_OK) return cuda_failed();
     p.counters = reinterpret_cast<unsigned *>(ws + kAttnCountersOffset);
     p.partials = reinterpret_cast<float *>(ws + kAttnZeroBytes);
     const WaitConfig waits = wait_config();

@@ -24,6 +24,14 @@ inline bool kv_page_size_ok(int64_t page_size) {
 
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Status of a CUDA call that failed.  The runtime keeps its error for the next
+// look, which another entry point may take after a launch of its own: it is
+// cleared here.
+inline int cuda_failed() {
+    (void)cudaGetLastError();
+    return FP8L_ECUDA;
+}
+
 // Raises a kernel's shared-memory limit to `smem`, the most that any of its
 // launches asks for, once per device (`ready` has a bit for each): a limit set
 // for every launch could be lowered by another thread before the launch.
@@ -31,12 +39,12 @@ inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3
 template <typename Kernel>
 inline int allow_smem(Kernel kernel, int smem, std::atomic<unsigned long long> &ready, bool all_shared) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FP8L_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
     if (ready.load(std::memory_order_acquire) >> dev & 1u) return FP8L_OK;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         (all_shared &&
          cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess))
-        return FP8L_ECUDA;
+        return cuda_failed();
     ready.fetch_or(1ull << dev, std::memory_order_release);
     return FP8L_OK;
 }
@@ -57,7 +65,7 @@ inline int launch_dependent(void (*kernel)(Params), dim3 grid, int threads, size
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FP8L_OK : FP8L_ECUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FP8L_OK : cuda_failed();
 }
 
 // The larger one, NaN when either is

@@ -148,3 +148,49 @@ def test_the_first_call_of_a_process_may_be_captured():
     done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True,
                           text=True, timeout=300)
     assert done.returncode == 0, done.stderr
+
+
+FAILED_LAUNCH = """
+import torch
+import fp8_quantized_linear_gb300 as fl
+dev = torch.device("cuda:0")
+cache = fl.kv_cache(4, 16, 2, 64, dev)
+q = torch.ones(1, 4, 64, dtype=torch.half, device=dev)
+x = torch.ones(1, 8 * 64, dtype=torch.half, device=dev)
+i = torch.zeros(1, dtype=torch.int32, device=dev)
+off = torch.tensor([0, 1], dtype=torch.int32, device=dev)
+table, ws = torch.zeros_like(i).view(1, 1), fl.fp8_kv_attention_workspace(dev)
+calls = (lambda: fl.fp8_kv_attention(q, cache, i.view(1, 1), off, off[1:], 1, ws=ws),
+         lambda: fl.fp8_qk_norm_rope_append(x, cache, i, i, q=q),
+         lambda: fl.fp8_kv_plan(i, i, table, off, 0, 16))
+for call in calls:
+    call()
+    fl.fp8_quant_per_tensor(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    try:
+        with torch.cuda.graph(g):
+            try:
+                torch.cuda.synchronize()  # not allowed here: the capture is lost
+            except RuntimeError:
+                pass
+            try:
+                call()
+            except fl.Fp8LinearError as e:
+                assert e.status == 4, e
+            else:
+                raise AssertionError("launched into a lost capture")
+    except RuntimeError:
+        pass
+    fl.fp8_quant_per_tensor(x)  # raises if it finds the other call's error
+"""
+
+
+def test_a_launch_that_failed_is_not_reported_by_the_next_call():
+    # a lost graph capture refuses launches on its stream, on the host
+    import subprocess
+    import sys
+    root = b._PKG.rsplit("/", 1)[0]
+    done = subprocess.run([sys.executable, "-c", FAILED_LAUNCH], cwd=root, capture_output=True,
+                          text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
