@@ -268,49 +268,26 @@ __device__ __forceinline__ uint32_t attn_codes4(const float *o, const Quot &d) {
     return c;
 }
 
-// VALS consecutive outputs of a row from dimension d on
+// VALS (4 or 8) consecutive outputs of a row from dimension d on
 template <int VALS>
 __device__ __forceinline__ void attn_store(const AttnParams &p, int token, int head, int dim, int d,
                                            const float (&o)[VALS]) {
+    static_assert(VALS == 4 || VALS == 8, "whole words of codes, at most one 16-byte store");
     const int64_t at = (static_cast<int64_t>(token) * p.q_heads + head) * dim + d;
     if (p.out_dtype == FP8L_E4M3) {
-        const float s = p.out_scale[0];
+        const Quot s = Quot::make<FP8L_F32>(p.out_scale[0]);
         uint8_t *y = static_cast<uint8_t *>(p.out) + at;
-        if constexpr (VALS < 4) {
 #pragma unroll
-            for (int i = 0; i < VALS; ++i) y[i] = code_of(o[i], s);
-        } else {
-            const Quot d = Quot::make<FP8L_F32>(s);
-            uint32_t c[VALS / 4];
-#pragma unroll
-            for (int i = 0; i < VALS / 4; ++i) c[i] = attn_codes4(&o[4 * i], d);
-            if constexpr (VALS % 16 == 0) {
-#pragma unroll
-                for (int i = 0; i < VALS / 4; i += 4)
-                    *reinterpret_cast<uint4 *>(y + 4 * i) = make_uint4(c[i], c[i + 1], c[i + 2], c[i + 3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VALS / 4; ++i) *reinterpret_cast<uint32_t *>(y + 4 * i) = c[i];
-            }
-        }
+        for (int i = 0; i < VALS; i += 4) *reinterpret_cast<uint32_t *>(y + i) = attn_codes4(&o[i], s);
     } else {
         uint16_t *y = static_cast<uint16_t *>(p.out) + at;
-        if constexpr (VALS == 1) {
-            *y = static_cast<uint16_t>(pack_out16(o[0], o[0], p.out_dtype) & 0xFFFFu);
-        } else {
-            uint32_t w[VALS / 2];
+        uint32_t w[VALS / 2];
 #pragma unroll
-            for (int i = 0; i < VALS / 2; ++i) w[i] = pack_out16(o[2 * i], o[2 * i + 1], p.out_dtype);
-            if constexpr (VALS == 2) {
-                *reinterpret_cast<uint32_t *>(y) = w[0];
-            } else if constexpr (VALS == 4) {
-                *reinterpret_cast<uint2 *>(y) = make_uint2(w[0], w[1]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VALS / 2; i += 4)
-                    *reinterpret_cast<uint4 *>(y + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-            }
-        }
+        for (int i = 0; i < VALS / 2; ++i) w[i] = pack_out16(o[2 * i], o[2 * i + 1], p.out_dtype);
+        if constexpr (VALS == 4)
+            *reinterpret_cast<uint2 *>(y) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint4 *>(y) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
