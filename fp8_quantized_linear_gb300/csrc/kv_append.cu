@@ -28,9 +28,18 @@
 // 4.3 TB/s of the 311 MB it has to move (a plain copy of qkv takes 51 us);
 // queries alone take 42 us, 5.4 TB/s, keys and values the rest, bound by
 // instructions (two readings, the exact quotient: 0.63 of the issue slots).
-// 7.2 us for one token each of 256 sequences with 64 query heads, 3.1 us for
-// one.  Holding the rows between the readings took 128 registers and 87 us;
+// 7.3 us for one token each of 256 sequences with 64 query heads, 3.3 us for
+// one: the same append replayed, so that no scale grows.  With the cache put
+// back before each call the 256 take 9.1 us when no scale grows, 12.8 when those
+// of a random cache do, 23 when every page and head re-casts its earlier tokens
+// (a block's pages one after the other).  Holding the rows between the readings took 128 registers and 87 us;
 // alternating units and queries over the grid changed nothing.
+//
+// Codes against a 64-bit computation: of 17.2 M each for 13741 tokens, 16-28 of
+// the keys differ (float32 norm and rotation; as many as with separate products
+// and an exact root) and about 10^4 of the values.  Those are ties: a 16-bit
+// value over its block's amax / 448 is halfway between two codes in 1 of 190
+// cases, and the last bit of either quotient, here or in 64 bits, decides.
 #include "kv_device.cuh"
 #include "quant_device.cuh"
 

@@ -49,7 +49,8 @@
 // prologue, 3 us, and one boundary in every 28 tiles, where a CTA's softmax
 // waits for its epilogue while the SM's other CTA streams).  One tile's softmax
 // takes about 1200 cycles (2000 with four groups), which two CTAs hide and one
-// does not: 153 us with 20 rows, 104 us with 12.  6.7 us for one sequence of
+// does not: 159 us with 20 rows, 105 us with 12.  D = 64 takes 77 us for half the
+// bytes, fp16 96: the softmax of a tile costs the same.  7.0 us for one sequence of
 // 129 keys, of which the first bytes arrive after 3.
 #pragma once
 

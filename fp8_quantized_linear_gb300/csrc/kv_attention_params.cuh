@@ -218,7 +218,9 @@ __device__ __forceinline__ float ex2(float x) {
 
 // A block's scale of values as the softmax takes it, by its logarithm and its
 // reciprocal: a smaller one (0 too, of a block of zeros not written here)
-// counts as the smallest
+// counts as the smallest.  (__log2f is within 3 units in the last place, 2^-20
+// for scales around 0.01 and 2^-16 for the smallest: so much do a page's weights
+// and the log-sum-exp stray.)
 __device__ __forceinline__ float value_scale(float s) { return s < kKvMinScale ? kKvMinScale : s; }
 
 // Exponent e with 2^7 <= m 2^e < 2^8, at most 120 (rows below 2^-113 lose

@@ -38,9 +38,9 @@
 // V to fp16 and the scales' factors, warp 12 copies and hands the pieces of the
 // line to the others through shared memory, warp 13 issues the MMAs.
 //
-// Measured (GB300, 32 query and 8 kv heads of 128, bf16): 880 us for 4096
-// queries of a 20480-token context, 1406 TFLOP/s, 0.75 of the measured 16-bit
-// rate; 180 us for six ragged prompts of 6294 tokens (0.31: a row tile there
+// Measured (GB300, 32 query and 8 kv heads of 128, bf16): 865-905 us from one
+// GPU to another for 4096 queries of a 20480-token context, 1370-1430 TFLOP/s,
+// 0.73-0.77 of the measured 16-bit rate (fp16 944, D = 64 877); 180 us for six ragged prompts of 6294 tokens (0.31: a row tile there
 // has about 8 key tiles, and its queries, masked tile and rows' way out weigh
 // as much).  A step of 256 rows and 128 keys needs 2048 tensor cycles and takes
 // about 3500: within a half scores, maximum, weights and the second product

@@ -16,8 +16,8 @@
 // takes its share of the rows and of the new table entries, each found in
 // the prefix sums by bisection in shared memory.
 //
-// Measured (GB300, replayed from a graph): 2.9 us for 64 requests of one new
-// token, 7.5 us for 1021 requests with 25085 (two rounds of scans, 13 blocks);
+// Measured (GB300, replayed from a graph): 3.0-3.3 us for 64 requests of one new
+// token, 7.7 us for 1021 requests with 25085 (two rounds of scans, 13 blocks);
 // an empty launch takes 2 us.
 #include "kv_device.cuh"
 

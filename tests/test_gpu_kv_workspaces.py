@@ -194,3 +194,27 @@ def test_a_launch_that_failed_is_not_reported_by_the_next_call():
     done = subprocess.run([sys.executable, "-c", FAILED_LAUNCH], cwd=root, capture_output=True,
                           text=True, timeout=300)
     assert done.returncode == 0, done.stderr
+
+
+def test_two_host_threads_on_streams_of_their_own():
+    import threading
+    cases = [make(torch.bfloat16, 64, 8, 2, 128, [n] * 3, [5000, 3000, 900], seed=50 + n)
+             for n in (1, 4, 90)]
+    want = [run(s)[0] for s in cases]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(s, w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream(DEV)):
+                for _ in range(50):
+                    assert torch.equal(run(s)[0], w)
+        except Exception as e:  # noqa: BLE001 - reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
