@@ -35,9 +35,9 @@
 // (a block's pages one after the other).  Holding the rows between the readings took 128 registers and 87 us;
 // alternating units and queries over the grid changed nothing.
 //
-// Codes against a 64-bit computation: of 17.2 M each for 13741 tokens, 16-28 of
-// the keys differ (float32 norm and rotation; as many as with separate products
-// and an exact root) and about 10^4 of the values.  Those are ties: a 16-bit
+// Codes against a 64-bit computation: of 17.2 M each for 13741 tokens, 17 of
+// the keys differ (float32 norm and rotation; 24 with a rounding after every
+// operation) and about 10^4 of the values.  Those are ties: a 16-bit
 // value over its block's amax / 448 is halfway between two codes in 1 of 190
 // cases, and the last bit of either quotient, here or in 64 bits, decides.
 #include "kv_device.cuh"
@@ -187,10 +187,11 @@ __device__ __forceinline__ float row_rms(const Row &r, float eps, uint32_t mask)
     return rsqrtf(ss * (1.0f / (8 * LANES)) + eps);
 }
 
+// x r gamma, gamma first: the product of two 16-bit numbers is exact in float32
 __device__ __forceinline__ void scale_row(Row &r, float inv, const Row &gamma) {
     const uint64_t i2 = pair_of(inv, inv);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.p[i] = f2_mul(f2_mul(r.p[i], i2), gamma.p[i]);
+    for (int i = 0; i < 4; ++i) r.p[i] = f2_mul(f2_mul(r.p[i], gamma.p[i]), i2);
 }
 
 // (a, b) <- (a cos - b sin, b cos + a sin)
