@@ -27,16 +27,16 @@ static_assert(kAttnCountersOffset + 4 * kDecLevels * 2 * 2 * kDecMaxCtas <= kAtt
 
 constexpr int kSmemPerSm = 227 * 1024;  // what the CTAs of an SM can ask for, each with 1 KB of its own
 
-template <int QDT, int DIM, int GROUPS>
+template <int QDT, int DIM, int GROUPS, int WPARTS>
 int launch_decode(AttnParams p, int sms, cudaStream_t stream) {
-    using Sh = DecShape<QDT, DIM, GROUPS>;
+    using Sh = DecShape<QDT, DIM, GROUPS, WPARTS>;
     constexpr int kBudget = kSmemPerSm / Sh::kCtasPerSm - 1024;
     constexpr int kFit = (kBudget - Sh::kFixedBytes) / Sh::kStageBytes;
     static_assert(kFit >= 2, "two stages at least");
     p.stages = kFit < kDecMaxStages ? kFit : kDecMaxStages;
     const int smem = p.stages * Sh::kStageBytes + Sh::kFixedBytes;
     static std::atomic<unsigned long long> ready{0};
-    auto kernel = kv_attention_decode_kernel<QDT, DIM, GROUPS>;
+    auto kernel = kv_attention_decode_kernel<QDT, DIM, GROUPS, WPARTS>;
     if (int st = allow_smem(kernel, smem, ready, true); st != FP8L_OK) return st;
     const int most = kDecMaxCtas / 2 * Sh::kCtasPerSm, ctas = Sh::kCtasPerSm * sms;
     return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), Sh::kThreads, smem, stream,
@@ -61,11 +61,20 @@ int launch_prompt(const AttnParams &p, int sms, cudaStream_t stream) {
 // Measured over 64 sequences of 0.1-8k keys, 8 kv heads of 128:
 //   8 rows: 88 us with one group, 99 with two;   16: 106 with two, 145 with four;
 //   20 rows: 153 us, 244 with the prompt kernel;  32: 160 against 238.
+//
+// Outputs in codes: a value near a code's border shows the weights' rounding,
+// which a 16-bit output's own covers.  Of 262144 codes over the same sequences 96
+// differ from the 64-bit value's with 12-bit weights, 4 with 16 bits (13 with
+// 32-bit weights and no other rounding).  Up to eight rows the fourth part's columns
+// are there anyway and cost 1 % (88.3 -> 89.2 us; 2.5 % at D = 64); with 16 rows 2.5 %,
+// with 32 4.5 %, and there the three parts stay.
 template <int QDT, int DIM>
 int launch_attention(const AttnParams &p, int64_t rows, int sms, cudaStream_t stream) {
-    if (rows <= 8) return launch_decode<QDT, DIM, 1>(p, sms, stream);
-    if (rows <= 16) return launch_decode<QDT, DIM, 2>(p, sms, stream);
-    if (rows <= 32) return launch_decode<QDT, DIM, 4>(p, sms, stream);
+    if (rows <= 8)
+        return p.out_dtype == FP8L_E4M3 ? launch_decode<QDT, DIM, 1, 4>(p, sms, stream)
+                                        : launch_decode<QDT, DIM, 1, 3>(p, sms, stream);
+    if (rows <= 16) return launch_decode<QDT, DIM, 2, 3>(p, sms, stream);
+    if (rows <= 32) return launch_decode<QDT, DIM, 4, 3>(p, sms, stream);
     return launch_prompt<QDT, DIM>(p, sms, stream);
 }
 

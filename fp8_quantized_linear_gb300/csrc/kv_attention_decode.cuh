@@ -17,7 +17,8 @@
 // with a sign), scaled so that its largest element is in [2^7, 2^8), is exact
 // in two parts from 2^-13 of that element on and within 2^-21 of it below; fp16
 // (11 bits) in three parts from 2^-14 on and within 2^-25.  A weight in three
-// parts has 12 bits, or 2^-25 of the running maximum.  The part columns are summed in float32.
+// parts has 12 bits, or 2^-25 of the running maximum; in four, 16 bits or 2^-29.
+// The part columns are summed in float32.
 //
 // Softmax with block scales.  With k_j = sk c_j and v_j = sv d_j per page,
 //   t_j = log2(e) sm_scale q.k_j + log2 sv_j,   w_j = 2^(t_j - m),  m ~ max t
@@ -67,15 +68,15 @@ constexpr int kDecFan = 16;        // partials added by one CTA
 constexpr int kDecLevels = 3;      // 16^3 CTAs and more
 constexpr int kDecSegments = 16;   // pieces between the copy warp and the slowest role (stages + 3 at most)
 
-// GROUPS softmax groups of eight rows
-template <int QDT, int DIM, int GROUPS>
+// GROUPS softmax groups of eight rows; the weights in WPARTS E4M3 parts
+template <int QDT, int DIM, int GROUPS, int WPARTS>
 struct DecShape {
     static constexpr int kRows = 8 * GROUPS;
     static constexpr int kCtasPerSm = GROUPS <= 2 ? 2 : 1;
     static constexpr int kThreads = 128 * GROUPS + 64;
     static constexpr int kQParts = QDT == FP8L_BF16 ? 2 : 3;
     static constexpr int kSCols = (kRows * kQParts + 15) / 16 * 16;
-    static constexpr int kOCols = (kRows * 3 + 15) / 16 * 16;
+    static constexpr int kOCols = (kRows * WPARTS + 15) / 16 * 16;
     static constexpr int kUsedCols = 2 * kSCols + kOCols;
     static constexpr int kTmemCols = kUsedCols <= 64 ? 64 : (kUsedCols <= 128 ? 128 : (kUsedCols <= 256 ? 256 : 512));
     static_assert(kUsedCols <= 512 / kCtasPerSm, "the SM's CTAs share its tensor memory");
@@ -236,10 +237,11 @@ __device__ __forceinline__ long long dec_scan(long long v, long long *red, long 
     return before + inc - v;
 }
 
-template <int QDT, int DIM, int GROUPS>
-__global__ void __launch_bounds__(DecShape<QDT, DIM, GROUPS>::kThreads, DecShape<QDT, DIM, GROUPS>::kCtasPerSm)
+template <int QDT, int DIM, int GROUPS, int WPARTS>
+__global__ void __launch_bounds__(DecShape<QDT, DIM, GROUPS, WPARTS>::kThreads,
+                                  DecShape<QDT, DIM, GROUPS, WPARTS>::kCtasPerSm)
 kv_attention_decode_kernel(const AttnParams p) {
-    using Sh = DecShape<QDT, DIM, GROUPS>;
+    using Sh = DecShape<QDT, DIM, GROUPS, WPARTS>;
     constexpr int ROWS = Sh::kRows;
     extern __shared__ __align__(128) uint8_t dec_smem[];
     __shared__ long long scan_red[Sh::kThreads / 32];
@@ -650,7 +652,7 @@ kv_attention_decode_kernel(const AttnParams p) {
                                            p.wait_cycles);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int part = 0; part < 3; ++part) {
+                        for (int part = 0; part < WPARTS; ++part) {
                             uint32_t o[8];
                             tmem_ld8(o_tmem + static_cast<uint32_t>(part * ROWS), o);
                             tmem_wait_ld();
@@ -673,7 +675,7 @@ kv_attention_decode_kernel(const AttnParams p) {
                 ok = ok && kv_wait(wfree + 8 * b, ((i >> 1) & 1u) ^ 1u, abort_flag, p.status, p.wait_cycles);
                 uint8_t *wrow = fixed_ptr + Sh::kWOff + b * Sh::kWBytes + (tid >> 3) * 8 * Sh::kOCols + (tid & 7) * 16;
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {
+                for (int part = 0; part < WPARTS; ++part) {
                     uint32_t c[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) c[r] = take_part(w[2 * r], w[2 * r + 1]);
@@ -718,16 +720,20 @@ kv_attention_decode_kernel(const AttnParams p) {
             tc_fence_after();
             float *rows = reinterpret_cast<float *>(fixed_ptr + Sh::kRowsOff) + row_base * DIM;
             {
-                uint32_t o[3][8];
+                uint32_t o[WPARTS][8];
 #pragma unroll
-                for (int part = 0; part < 3; ++part) tmem_ld8(o_tmem + static_cast<uint32_t>(part * ROWS), o[part]);
+                for (int part = 0; part < WPARTS; ++part) tmem_ld8(o_tmem + static_cast<uint32_t>(part * ROWS), o[part]);
                 tmem_wait_ld();
                 tc_fence_before();
                 if (tid < DIM) {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        rows[r * DIM + tid] = fmaf(fmaf(__uint_as_float(o[2][r]), 0.0625f, __uint_as_float(o[1][r])),
-                                                   0.0625f, __uint_as_float(o[0][r])) * (1.0f / 128.0f);
+                    for (int r = 0; r < 8; ++r) {
+                        float x = __uint_as_float(o[WPARTS - 1][r]);
+#pragma unroll
+                        for (int part = WPARTS - 2; part >= 0; --part)
+                            x = fmaf(x, 0.0625f, __uint_as_float(o[part][r]));
+                        rows[r * DIM + tid] = x * (1.0f / 128.0f);
+                    }
                 }
             }
             group_sync(bar_id);

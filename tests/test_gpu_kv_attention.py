@@ -381,3 +381,27 @@ def test_given_outputs(n):
     given = torch.empty(codes.shape, dtype=torch.float8_e4m3fn, device=DEV)
     got, none = run(s, out=given, out_dtype=torch.float8_e4m3fn, out_scale=scale)
     assert none is None and got is given and torch.equal(given.view(torch.uint8), codes)
+
+
+def test_codes_of_few_rows_take_weights_of_16_bits():
+    # Two keys of like weight, so that a weight's rounding shows in the output
+    # (2^-16 of it, or 2^-29 of the row's largest), and small scores, whose own
+    # float32 error is less.  16.8 million codes: few are near enough a border.
+    dim, hq, hkv, n = 64, 32, 8, 512
+    scale = torch.full((1,), 0.02, device=DEV)
+    for seed in range(16):
+        s = make(torch.bfloat16, 16, hq, hkv, dim, [1] * n, [2] * n, seed=seed, magnitude=0.05)
+        got, _ = run(s, out_dtype=torch.uint8, out_scale=scale)
+        k, v = (torch.stack(s[x]).repeat_interleave(hq // hkv, 1) for x in ("k", "v"))
+        q = s["q"].double()
+        p = torch.softmax(torch.einsum("rhd,rhjd->rhj", q, k) * dim ** -0.5, 2)
+        want, spread = (torch.einsum("rhj,rhjd->rhd", p, x) for x in (v, v.abs()))
+        reach = torch.einsum("rhd,rhjd->rhj", q.abs(), k.abs()).amax(2) * dim ** -0.5
+        score = (dim * 2.0 ** -24 * reach)[:, :, None]
+        assert score.max().item() < 2.0 ** -17
+        top = np.nanmax(np.where(np.isnan(s["v_scale"]), 0, s["v_scale"]))
+        slack = spread * (2.0 ** -16 + 2.0 ** -17 + 2 * score) + 2 * 448 * top * 2.0 ** -29
+        unit = scale.double()
+        ok = kv_ref.nearest_code_ok((want / unit).cpu().numpy(), kv_ref.TABLE[got.cpu().numpy()],
+                                    (slack / unit).cpu().numpy())
+        assert ok.all(), (seed, (~ok).sum())
