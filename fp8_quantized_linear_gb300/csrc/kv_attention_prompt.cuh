@@ -1064,7 +1064,9 @@ __global__ void __launch_bounds__(kProThreads, 1) kv_attention_prompt_kernel(con
         }
     }
 
-    kv_drain(done_bar, 0, p.status);
+    // MMAs retired.  The two warps without a role wait at the barrier below: here
+    // they would wait all the call, and a long one is no time-out.
+    if (warp < 14) kv_drain(done_bar, 0, p.status);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
