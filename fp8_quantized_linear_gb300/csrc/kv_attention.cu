@@ -143,7 +143,9 @@ int fp8_kv_attention(const void *q, int q_dtype, int64_t tokens, int64_t q_strid
     p.kv_lens = kv_lens;
     p.requests = static_cast<int>(requests);
     p.score_scale = sm_scale * 1.44269504088896341f;
-    p.window = static_cast<int>(window < INT32_MAX ? window : 0);
+    // a window that holds every key the table can is none (and negative positions
+    // less a window stay in 32 bits)
+    p.window = static_cast<int>(window <= INT32_MAX - tokens && window < table_width * page_size ? window : 0);
     p.out_scale = out_scale;
     p.out = out;
     p.out_dtype = out_dtype;

@@ -405,3 +405,13 @@ def test_codes_of_few_rows_take_weights_of_16_bits():
         ok = kv_ref.nearest_code_ok((want / unit).cpu().numpy(), kv_ref.TABLE[got.cpu().numpy()],
                                     (slack / unit).cpu().numpy())
         assert ok.all(), (seed, (~ok).sum())
+
+
+@pytest.mark.parametrize("n", [10, 100])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 6, 2 ** 40, 64 * 4])
+def test_a_window_wider_than_every_context(n, window):
+    # more rows than keys, so that the first positions are negative
+    s = make(torch.bfloat16, 64, 8, 2, 128, [n, n], [3, 190], seed=60 + n)
+    want, want_lse = run(s, want_lse=True)
+    got, lse = run(s, want_lse=True, window=window)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
