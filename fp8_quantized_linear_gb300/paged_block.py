@@ -105,6 +105,8 @@ class PagedAttentionBlock:
         Raises before anything is computed when a token finds no page (too few
         free pages, or a request past its table's); the cache, the lengths and
         the free pages are then as before, and a later step may be tried."""
+        if sum(q_lens) > x.shape[0]:
+            raise ValueError(f"{sum(q_lens)} new tokens, but x has {x.shape[0]} rows")
         lens = torch.tensor(q_lens, dtype=torch.int32, device=self.device)
         plan = self.plan(lens, x.shape[0])
         taken, lost = plan.used.tolist()

@@ -183,3 +183,12 @@ def test_a_finished_request_gives_its_pages_back(weights):
         blk.step(first[:1], [1, 0, 0])
     blk.release(1)  # a request without tokens has nothing to give
     assert blk.free.numel() == 0
+
+
+def test_a_step_with_more_tokens_than_rows_is_refused(weights):
+    blk = make(weights)
+    x = synthetic.activation(12, 4096, torch.bfloat16, seed=1).to(DEV)
+    with pytest.raises(ValueError, match="rows"):
+        blk.step(x, [10, 3, 0])
+    assert blk.kv_lens.tolist() == [0, 0, 0] and blk.free.numel() == 40
+    assert blk.step(x, [9, 3, 0]).shape == (12, 4096)
