@@ -1,0 +1,95 @@
+// Epilogue of the linear products (fp8_linear, fp8_w8a16_linear): bias,
+// activation (plain or gated), residual addition and the output cast, on
+// float32 sums in registers.
+//
+//   z = acc * scale + bias(n)
+//   plain   t[n] = act(z[n])
+//   gated   t[n] = act(z[n]) * z[N/2 + n]      (gate rows first, then up rows)
+//   y = cast(t + residual)
+//
+// Everything is float32 and rounded once, by the output cast.  The logistic
+// forms are written as z / (1 + e^-u): no cancellation for negative z, and an
+// overflowing exponential gives the right limit 0.  GELU's normal
+// distribution is erfc(-z / sqrt 2) / 2, which keeps its relative accuracy
+// where 1 + erf would cancel.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace fp8l {
+
+// What a product's epilogue does (kernel argument).
+struct Epilogue {
+    const void *bias;      // [N] of bias_dtype, or null
+    int bias_dtype;        // FP8L_F16, FP8L_BF16 or FP8L_F32
+    int act;               // FP8L_ACT_* without the gate bit
+    const void *residual;  // [M, width] of the output's 16-bit type, or null
+    const float *out_scale;
+    void *y;  // [M, width]
+    int out_dtype;
+    int width;  // columns of y: N, or N / 2 when gated
+};
+
+namespace {
+
+__device__ __forceinline__ float silu_of(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+__device__ __forceinline__ float gelu_of(float z) {
+    return 0.5f * z * erfcf(z * -0.70710678118654752f);
+}
+
+// z (1 + tanh u) / 2 with u = sqrt(2 / pi) (z + 0.044715 z^3) is z times the
+// logistic function of 2 u
+__device__ __forceinline__ float gelu_tanh_of(float z) {
+    const float u2 = z * fmaf(z * z, 0.07135481282970f, 1.59576912160573f);
+    return __fdividef(z, 1.0f + __expf(-u2));
+}
+
+// COUNT values through the activation; one branch for all of them
+template <int COUNT>
+__device__ __forceinline__ void activate(float (&v)[COUNT], int act) {
+    if (act == FP8L_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) v[i] = silu_of(v[i]);
+    } else if (act == FP8L_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) v[i] = gelu_tanh_of(v[i]);
+    } else if (act == FP8L_ACT_GELU) {
+        // (rolled: erfcf is long)
+#pragma unroll 4
+        for (int i = 0; i < COUNT; ++i) v[i] = gelu_of(v[i]);
+    } else if (act == FP8L_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+    }
+}
+
+// Loads of what the preceding kernel on the stream may have written:
+// coherent, and kept after griddepcontrol.wait.
+__device__ __forceinline__ float epi_ld_f32(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float epi_ld_16(const void *p, int64_t i, int dtype) {
+    unsigned short u;
+    asm volatile("ld.global.u16 %0, [%1];"
+                 : "=h"(u)
+                 : "l"(static_cast<const unsigned short *>(p) + i)
+                 : "memory");
+    return dtype == FP8L_BF16 ? __uint_as_float(static_cast<uint32_t>(u) << 16)
+                              : __half2float(__ushort_as_half(u));
+}
+
+__device__ __forceinline__ float epi_bias(const Epilogue &e, int64_t n) {
+    if (e.bias == nullptr) return 0.0f;
+    return e.bias_dtype == FP8L_F32 ? epi_ld_f32(static_cast<const float *>(e.bias) + n)
+                                    : epi_ld_16(e.bias, n, e.bias_dtype);
+}
+
+}  // namespace
+}  // namespace fp8l

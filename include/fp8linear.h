@@ -296,6 +296,65 @@ FP8L_API int fp8_w8a16_mm(const void *x, int x_dtype, const uint8_t *w,
  * they make one).  A pure function of its arguments; needs no GPU. */
 FP8L_API unsigned fp8_w8a16_mm_kernel(int64_t M, int64_t N, int64_t K, unsigned flags);
 
+/* Activations of fp8_linear and fp8_w8a16_linear, z in float32:
+ *   NONE       z
+ *   RELU       max(z, 0)
+ *   SILU       z / (1 + e^-z)
+ *   GELU       z (1 + erf(z / sqrt 2)) / 2
+ *   GELU_TANH  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ * FP8L_ACT_GATED, added to one of them, makes the product a gated one (the
+ * fused gate/up product of a feed-forward layer). */
+enum fp8l_activation {
+    FP8L_ACT_NONE = 0,
+    FP8L_ACT_RELU = 1,
+    FP8L_ACT_SILU = 2,
+    FP8L_ACT_GELU = 3,
+    FP8L_ACT_GELU_TANH = 4,
+    FP8L_ACT_GATED = 16
+};
+
+/* The W8A8 linear layer: fp8_scaled_mm with bias, activation and the residual
+ * stream's addition in its epilogue ("[Kernel][FP8] Initial support ...": the
+ * product replaces nn.Linear, bias and all; "RFC: FP8 Quantization Schema in
+ * vLLM": an E4M3 result through output_scale).
+ *
+ *   z[m,n] = sum_k dec(a[m,k]) dec(w[n,k]) * as(m) ws(n) + bias[n]
+ *   plain:  t[m,n] = act(z[m,n]),                          width = N
+ *   gated:  t[m,n] = act(z[m,n]) * z[m, N/2 + n], n < N/2, width = N/2
+ *   out_dtype FP8L_BF16 / FP8L_F16: y[m,n] = RN(t[m,n] + residual[m,n])
+ *   out_dtype FP8L_E4M3:            y[m,n] = E4M3(t[m,n] / out_scale[0])
+ *
+ * in float32 throughout, rounded once.  a, w, a_scale, w_scale,
+ * w_per_channel, out_scale and workspace as for fp8_scaled_mm; w (and bias,
+ * and a per-channel w_scale) hold the N/2 gate rows first, then the N/2 up
+ * rows, when gated.  bias: N values of bias_dtype (FP8L_F16, FP8L_BF16 or
+ * FP8L_F32, aligned to their size), or NULL.  activation: an
+ * fp8l_activation, with FP8L_ACT_GATED or not.  residual: [M, width] of
+ * out_dtype, or NULL; NULL for an E4M3 output (FP8L_EINVAL otherwise).  y:
+ * [M, width]; it may be the residual itself, which is then updated in place,
+ * and shares memory with nothing else that is read (FP8L_EINVAL).  N is a
+ * multiple of 16 (32 when gated), K of 16, both positive and at most 2^20;
+ * 0 <= M <= 2^31 - 1 (M == 0 launches nothing).  flags: any of
+ * FP8L_WEIGHTS_STABLE and FP8L_A_PER_TOKEN. */
+FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N, int64_t K,
+                        const float *a_scale, const float *w_scale, int w_per_channel,
+                        const void *bias, int bias_dtype, int activation, const void *residual,
+                        const float *out_scale, void *y, int out_dtype, void *workspace,
+                        unsigned flags, void *stream);
+
+/* The W8A16 linear layer: fp8_w8a16_mm with the same epilogue ("Marlin
+ * fp8").  z[m,n] = w_scale[n] sum_k x[m,k] dec(w[n,k]) + bias[n]; then as
+ * fp8_linear, with y and residual of x_dtype.  x, w (row-major, or packed
+ * with FP8L_WEIGHTS_PACKED: the packed layout of the whole [N, K], gate and
+ * up rows alike) and w_scale as for fp8_w8a16_mm; the other arguments and
+ * the rules on y as for fp8_linear.  flags: any of FP8L_WEIGHTS_STABLE and
+ * FP8L_WEIGHTS_PACKED.  A time-out of a device-side wait is recorded as for
+ * fp8_w8a16_mm. */
+FP8L_API int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, const float *w_scale,
+                              int64_t M, int64_t N, int64_t K, const void *bias, int bias_dtype,
+                              int activation, const void *residual, void *y, unsigned flags,
+                              void *stream);
+
 /* Grouped W8A8 product for mixture-of-experts layers ("RFC: FP8
  * Quantization Schema in vLLM", the gate_proj question: FP8 products need
  * shapes divisible by 16; the experts' products are FP8, and a gate whose
@@ -382,6 +441,27 @@ FP8L_API int fp8_pack_w8a16_weights(const uint8_t *w, int64_t N, int64_t K,
 FP8L_API int fp8_rmsnorm_quant(const void *x, int x_dtype, const void *gamma, float eps,
                                int64_t M, int64_t K, uint8_t *q, float *scale, int mode,
                                void *h, void *workspace, void *stream);
+
+/* fp8_rmsnorm_quant with the residual stream's addition before it: the
+ * element-wise part between two of a decoder layer's blocks in one pass
+ * ("Condition to achieve linear speedup?": the quantization is fused into the
+ * element-wise kernel before the product).  Per row m:
+ *
+ *   total[m,k] = RN16(x[m,k] + residual[m,k])       (x's 16-bit format)
+ *   r, h and the codes from total as fp8_rmsnorm_quant takes them from x
+ *
+ * (the float32 sum of squares adds in an order of its own, so h agrees with
+ * the two calls up to one rounding where h is next to a border).  x,
+ * residual: [M, K] of x_dtype; total: [M, K], the new residual stream; it may
+ * be x or residual itself (updated in place).  gamma, eps, q, scale, mode, h,
+ * workspace, M and K as for fp8_rmsnorm_quant.  Apart from that, no output
+ * shares memory with an input or another output (FP8L_EINVAL).  workspace is
+ * used in FP8L_NQ_DYNAMIC only; a time-out of its grid barrier is recorded in
+ * it and in the library's status word.  Deterministic. */
+FP8L_API int fp8_add_rmsnorm_quant(const void *x, const void *residual, int x_dtype,
+                                   const void *gamma, float eps, int64_t M, int64_t K, void *total,
+                                   uint8_t *q, float *scale, int mode, void *h, void *workspace,
+                                   void *stream);
 
 /* Dynamic per-tensor quantization that allocates nothing and takes no
  * workspace.  The pages have no counterpart to this entry point.
