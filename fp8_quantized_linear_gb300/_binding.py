@@ -9,6 +9,7 @@ kernels; there is no CPU or PyTorch fallback, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -111,7 +112,9 @@ def load():
         lib.fp8_linear.restype = I
         lib.fp8_linear.argtypes = [P, P, I64, I64, I64, P, P, I, P, I, I, P, P, P, I, P, U, P]
         lib.fp8_w8a16_linear.restype = I
-        lib.fp8_w8a16_linear.argtypes = [P, I, P, P, I64, I64, I64, P, I, I, P, P, U, P]
+        lib.fp8_w8a16_linear.argtypes = [P, I, P, P, I64, I64, I64, P, I, I, P, P, P, U, P]
+        lib.fp8_w8a16_linear_workspace_bytes.restype = ctypes.c_size_t
+        lib.fp8_w8a16_linear_workspace_bytes.argtypes = [I, I64, I64]
         lib.fp8_kv_plan.restype = I
         lib.fp8_kv_plan.argtypes = [P, P, I64, I64, I64, P, I64, P, I64, P, P, P, P, P, P]
         lib.fp8_qk_norm_rope_append.restype = I
@@ -937,6 +940,11 @@ def fp8_linear(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale:
     return y
 
 
+@functools.lru_cache(maxsize=4096)
+def _w8a16_linear_bytes(dtype_code: int, M: int, K: int) -> int:
+    return int((_lib or load()).fp8_w8a16_linear_workspace_bytes(dtype_code, M, K))
+
+
 def fp8_w8a16_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                      bias: torch.Tensor | None = None, activation: str | None = None,
                      gated: bool = False, residual: torch.Tensor | None = None,
@@ -968,8 +976,11 @@ def fp8_w8a16_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
         y = torch.empty((M, width), dtype=x.dtype, device=x.device)
     elif y.shape != (M, width) or y.dtype is not x.dtype:
         raise ValueError("y is [M, N] ([M, N / 2] when gated) of x's dtype")
-    args = (x.data_ptr(), _DTYPE_CODE[x.dtype], w.data_ptr(), w_scale.data_ptr(), M, N, K,
-            bias_ptr, bias_code, act, res_ptr, y.data_ptr(),
+    dtype_code = _DTYPE_CODE[x.dtype]
+    # scratch of this call, from the stream's memory
+    scratch = torch.empty(_w8a16_linear_bytes(dtype_code, M, K), dtype=_U8, device=x.device)
+    args = (x.data_ptr(), dtype_code, w.data_ptr(), w_scale.data_ptr(), M, N, K,
+            bias_ptr, bias_code, act, res_ptr, y.data_ptr(), scratch.data_ptr(),
             (WEIGHTS_STABLE if stable_weights else 0) | (WEIGHTS_PACKED if packed else 0))
     f = (_lib or load()).fp8_w8a16_linear
     st = (f(*args, _stream_handle(index)) if _current_device() == index

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "linear_launch.cuh"
 
 namespace fp8l {
 
@@ -114,6 +115,25 @@ int library_status_word(unsigned **out) {
     }
     *out = slot.ptr;
     return FP8L_OK;
+}
+
+int make_swizzle64_map(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims,
+                       const uint64_t *strides, const uint32_t *box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (enc == nullptr || rank < 2 || rank > 5) return FP8L_ECUDA;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = static_cast<cuuint32_t>(box[i]);
+        estr[i] = 1;
+        if (i + 1 < rank) st[i] = static_cast<cuuint64_t>(strides[i]);
+    }
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
+                           const_cast<void *>(ptr), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FP8L_OK : FP8L_ECUDA;
 }
 
 int make_tile_map(CUtensorMap *map, const void *ptr, int elem_bytes, int rank, const uint64_t *dims,

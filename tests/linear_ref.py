@@ -47,12 +47,22 @@ def act(name, z):
     return z
 
 
-def linear(x, w, scale, bias=None, activation=None, gated=False, residual=None):
+def parts_error(x):
+    """What a 16-bit token may differ by when it is held in E4M3 parts: the
+    row's largest magnitude is brought to [2^7, 2^8); a value below E4M3's
+    normal range is off by at most half its smallest step, 2^-10, in the first
+    part, 2^-14 after the second (bf16), 2^-18 after the third (fp16)."""
+    return x.double().abs().amax(1, keepdim=True) * (2.0 ** -21 if x.dtype == torch.bfloat16
+                                                     else 2.0 ** -25)
+
+
+def linear(x, w, scale, bias=None, activation=None, gated=False, residual=None, x_error=0.0):
     """(t, d): the layer in doubles and the error bound.  x [M, K], w [N, K]
-    doubles; scale broadcasts to [M, N]."""
+    doubles; scale broadcasts to [M, N]; x_error: of every x, by row."""
     K = x.shape[1]
     z = (x @ w.T) * scale
-    d = (x.abs() @ w.abs().T) * scale.abs() * (K * 2.0 ** -23) + z.abs() * 2.0 ** -22
+    d = x_error * w.abs().sum(1) * scale.abs() + z.abs() * 2.0 ** -22
+    d = d + (x.abs() @ w.abs().T) * scale.abs() * (K * 2.0 ** -23)
     if bias is not None:
         z = z + bias.double()
         d = d + (z.abs() + bias.double().abs()) * 2.0 ** -23

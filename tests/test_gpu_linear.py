@@ -195,7 +195,7 @@ def check_w8a16(seed, M, N, K, dtype=BF, bias=None, activation=None, gated=False
     b = None if bias is None else torch.randn(N, generator=gen, device=DEV).to(bias)
     r = torch.randn(M, width, generator=gen, device=DEV).to(dtype) if residual else None
     t, d = ref.linear(x.double(), ref.e4m3_values(w), sw.double().view(1, -1), b, activation, gated,
-                      r)
+                      r, x_error=ref.parts_error(x))
     y = fl.fp8_w8a16_linear(x, fl.fp8_pack_w8a16_weights(w) if packed else w, sw, bias=b,
                             activation=activation, gated=gated, residual=r, y=r if inplace else None,
                             packed=packed, **kw)

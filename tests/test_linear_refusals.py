@@ -68,17 +68,18 @@ def test_linear_output_over_inputs(lib):
 
 def test_w8a16_argument_errors(lib):
     ok = dict(x=at(0), dt=b.F16, w=at(1), sw=at(2), M=9, N=256, K=64, bias=at(3), bdt=b.F16, act=1,
-              res=at(4), y=at(5), flags=0, st=None)
+              res=at(4), y=at(5), ws=at(6), flags=0, st=None)
 
     def call(**kw):
         return lib.fp8_w8a16_linear(*dict(ok, **kw).values())
     for kw in (dict(dt=b.E4M3), dict(dt=b.F32), dict(act=7), dict(bdt=b.E4M3), dict(flags=4),
-               dict(flags=8), dict(x=None), dict(w=None), dict(sw=None), dict(y=None)):
+               dict(flags=8), dict(x=None), dict(w=None), dict(sw=None), dict(y=None),
+               dict(ws=None)):
         assert call(**kw) == b.EINVAL, kw
     for kw in (dict(M=-1), dict(M=1 << 31), dict(N=24), dict(K=24), dict(N=0), dict(K=-16),
                dict(N=272, act=16 + 1)):
         assert call(**kw) == b.ESHAPE, kw
-    for name in ("x", "w", "y", "res"):
+    for name in ("x", "w", "y", "res", "ws"):
         assert call(**{name: at(0) + 4}) == b.EALIGN, name
     assert call(sw=at(2) + 2) == b.EALIGN and call(bias=at(3) + 1) == b.EALIGN
     y = at(5)
