@@ -881,7 +881,7 @@ def fp8_linear(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale:
                gated: bool = False, residual: torch.Tensor | None = None, out_dtype=None,
                out_scale: torch.Tensor | None = None, y: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, stable_weights: bool = False,
-               per_token: bool | None = None) -> torch.Tensor:
+               per_token: bool | None = None, kernel: str = "auto") -> torch.Tensor:
     """The W8A8 linear layer (fp8_linear): fp8_scaled_mm of E4M3 a [M, K] and
     w [N, K] with bias [N] (fp16, bf16 or float32), activation (None, "relu",
     "silu", "gelu", "gelu_tanh") and residual in the epilogue.  gated: w holds
@@ -889,7 +889,8 @@ def fp8_linear(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale:
     N / 2].  residual: [M, N] ([M, N / 2]) of the output's 16-bit type, added
     last; y may be the residual itself.  out_dtype: y's, else the residual's,
     else bf16; uint8 for E4M3 codes of the result / out_scale (no residual
-    then).  Scales, ws, stable_weights and per_token as for fp8_scaled_mm."""
+    then).  Scales, ws, stable_weights, per_token and kernel as for
+    fp8_scaled_mm."""
     index = _kv_device(a)
     given = (w, a_scale, w_scale, bias, residual, out_scale, y, ws, a)
     if not _kv_placed(index, given):
@@ -903,7 +904,9 @@ def fp8_linear(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale:
     scales = w_scale.numel()
     if scales != N and scales != 1:
         raise ValueError("w_scale must have 1 or N entries")
-    flags = WEIGHTS_STABLE if stable_weights else 0
+    flags = KERNELS[kernel]
+    if stable_weights:
+        flags |= WEIGHTS_STABLE
     if per_token is None:
         per_token = a_scale.numel() == M and M > 1
     if a_scale.numel() != (M if per_token else 1) or a_scale.dtype is not _F32:

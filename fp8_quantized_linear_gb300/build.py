@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8linear.so")
 
 SOURCES = ["api.cu", "quant.cu", "norm_quant.cu", "skinny.cu", "skinny_quant.cu", "gemm_tcgen05.cu",
-           "gemm_swapab.cu", "add_norm.cu", "linear.cu", "linear_swapped.cu",
+           "gemm_swapab.cu", "add_norm.cu", "linear.cu", "linear_swapped.cu", "linear_pair.cu",
            "kv_plan.cu", "kv_append.cu", "kv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-Xcompiler", "-fvisibility=hidden",

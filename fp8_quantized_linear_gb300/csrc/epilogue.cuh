@@ -58,8 +58,7 @@ __device__ __forceinline__ void activate(float (&v)[COUNT], int act) {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) v[i] = gelu_tanh_of(v[i]);
     } else if (act == FP8L_ACT_GELU) {
-        // (rolled: erfcf is long)
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < COUNT; ++i) v[i] = gelu_of(v[i]);
     } else if (act == FP8L_ACT_RELU) {
 #pragma unroll
@@ -83,6 +82,13 @@ __device__ __forceinline__ float epi_ld_16(const void *p, int64_t i, int dtype) 
                  : "memory");
     return dtype == FP8L_BF16 ? __uint_as_float(static_cast<uint32_t>(u) << 16)
                               : __half2float(__ushort_as_half(u));
+}
+
+// a pair of 16-bit values (the first in the low half)
+__device__ __forceinline__ float2 widen_pair(uint32_t w, int dtype) {
+    if (dtype == FP8L_BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
 __device__ __forceinline__ float epi_bias(const Epilogue &e, int64_t n) {

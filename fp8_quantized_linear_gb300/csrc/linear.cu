@@ -65,6 +65,14 @@ int check_output(const Epilogue &e, int64_t M, int64_t N, const void *x, size_t 
     return FP8L_OK;
 }
 
+// The kernel of fp8_linear: tiles over SM pairs when there are enough tokens
+// for them, else the swapped-operand kernel.
+unsigned choose_linear(int64_t M, int64_t N, int64_t K) {
+    (void)N;
+    (void)K;
+    return M > 256 ? FP8L_KERNEL_TILED : FP8L_KERNEL_SWAPPED;
+}
+
 }  // namespace
 }  // namespace fp8l
 
@@ -75,7 +83,7 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
                           unsigned flags, void *stream) {
     using namespace fp8l;
     if (out_dtype != FP8L_F16 && out_dtype != FP8L_BF16 && out_dtype != FP8L_E4M3) return FP8L_EINVAL;
-    if ((flags & ~(FP8L_WEIGHTS_STABLE | FP8L_A_PER_TOKEN)) != 0u) return FP8L_EINVAL;
+    if ((flags & ~(FP8L_WEIGHTS_STABLE | FP8L_A_PER_TOKEN | FP8L_KERNEL_MASK)) != 0u) return FP8L_EINVAL;
     if (a_scale == nullptr || w_scale == nullptr || workspace == nullptr || w == nullptr)
         return FP8L_EINVAL;
     if (out_dtype == FP8L_E4M3 && out_scale == nullptr) return FP8L_EINVAL;
@@ -110,6 +118,9 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     c.status = status_word(workspace);
     c.stable = (flags & FP8L_WEIGHTS_STABLE) != 0u;
     c.stream = as_stream(stream);
+    unsigned kernel = flags & FP8L_KERNEL_MASK;
+    if (kernel == FP8L_KERNEL_AUTO) kernel = choose_linear(M, N, K);
+    if (kernel == FP8L_KERNEL_TILED) return launch_linear_pair(c);
     return launch_linear_swapped(c, 1, a_scale);
 }
 

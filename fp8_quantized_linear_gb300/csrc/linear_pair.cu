@@ -1,0 +1,572 @@
+// Linear layer on the tcgen05 tensor cores for many tokens: 256 x 256 tiles
+// over pairs of SMs (sm_103a).
+//
+// ("[Kernel][FP8] Initial support with dynamic per-tensor scaling": the W8A8
+// product of a prefill batch; "RFC: FP8 Quantization Schema in vLLM": an E4M3
+// result through output_scale.)
+//
+//   z[m, n] = sum_k dec(a[m,k]) dec(w[n,k]) * a_scale(m) w_scale(n) + bias(n)
+//   y = the epilogue of epilogue.cuh
+//
+// A cluster of two CTAs computes a tile of 256 tokens by 256 weight rows with
+// tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 32): each CTA stages 128
+// rows of a and half of the tile's weight rows per 128-deep k-block (32 KB a
+// stage, six stages), the MMA reads the peer's halves from its shared memory,
+// and each CTA's TMEM receives its 128 tokens of the accumulator (512
+// columns: two accumulators, so the epilogue of one tile runs under the MMAs
+// of the next).  With a gate the even CTA stages 128 gate rows and the odd
+// one the up rows of the same outputs: the accumulator's left half is the
+// gate, its right half the up product, and both sit in the same lane, so the
+// epilogue needs no exchange and writes half the columns.
+//   warp 0     TMA producer in each CTA; both CTAs' copies complete on the
+//              even CTA's full barrier.  With stable weights the first
+//              stages' weights are loaded before the wait for the preceding
+//              kernel.
+//   warp 1     TMEM; in the even CTA one lane issues the MMAs, whose commits
+//              arrive on the barriers of both CTAs.
+//   warps 2-9  epilogue in each CTA, two warps a TMEM lane quarter (each half
+//              of the tile's 32-column chunks).  A tile's scales and biases
+//              are spread over the 256 threads once and read back from shared
+//              memory (any type, any alignment, one load a column); the
+//              residual of a row's next chunk is loaded while the present
+//              one is computed.
+// Tail tiles: 256-wide tiles fill whole rounds of the SM pairs; the columns
+// left over become narrower tiles when that ends the last round sooner.
+// Waits are bounded; a time-out raises both CTAs' abort flags, and both meet
+// at a cluster barrier before TMEM is released.
+#include <atomic>
+
+#include "linear_launch.cuh"
+#include "skinny_device.cuh"
+#include "tc_device.cuh"
+
+namespace fp8l {
+namespace {
+
+constexpr int LP_BM = 128;  // tokens a CTA; a pair covers 256
+constexpr int LP_BN = 256;  // weight rows a tile; each CTA stages half
+constexpr int LP_BK = 128;
+constexpr int LP_STAGES = 6;
+constexpr int kLpABytes = LP_BM * LP_BK;
+constexpr int kLpBBytes = (LP_BN / 2) * LP_BK;
+constexpr int kLpStageBytes = kLpABytes + kLpBBytes;
+constexpr int kLpEpiWarps = 8;
+constexpr int kLpEpiThreads = 32 * kLpEpiWarps;
+constexpr int kLpThreads = 64 + kLpEpiThreads;
+constexpr int kLpBarriers = 2 * LP_STAGES + 2 + 2 + 1;
+constexpr int kLpColBytes = 2 * 2 * LP_BN * 4;  // two tiles' scales and biases
+constexpr size_t kLpSmemBytes =
+    1024 + size_t(LP_STAGES) * kLpStageBytes + kLpColBytes + kLpBarriers * 8 + 16;
+constexpr uint32_t kLpTmemCols = 2 * LP_BN;
+
+struct PairArgs {
+    int M, num_k_blocks;
+    int tiles_m, main_tiles, n_main, tail_w, tail_n;  // n_main: output columns of the main tiles
+    int prefetch;
+    const float *a_scale;
+    int a_per_token;
+    const float *w_scale;
+    int w_per_channel;
+    Epilogue e;
+    unsigned *status;
+    long long wait_cycles;
+    unsigned stall;
+};
+
+// kind::f8f6f4, D f32, A and B E4M3 K-major, N = w, M = 256 (pair)
+__host__ __device__ constexpr uint32_t lp_idesc(int w) {
+    return (1u << 4) | (static_cast<uint32_t>(w >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
+}
+
+// TMA load into this CTA's shared memory, completing on an mbarrier of
+// either CTA of the pair
+__device__ __forceinline__ void lp_tma(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void lp_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// arrive on the barrier at this offset in both CTAs once the MMAs issued so
+// far have retired
+__device__ __forceinline__ void lp_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+struct LpTile {
+    int mt, n0, w;  // 256-token block, first output column, accumulator columns
+};
+
+template <bool GATED>
+__device__ __forceinline__ LpTile lp_tile(const PairArgs &p, int tile) {
+    LpTile t;
+    if (tile < p.main_tiles) {
+        t.mt = tile % p.tiles_m;
+        t.n0 = (tile / p.tiles_m) * (GATED ? LP_BN / 2 : LP_BN);
+        t.w = LP_BN;
+    } else {
+        const int u = tile - p.main_tiles;
+        t.mt = u % p.tiles_m;
+        t.w = p.tail_w;
+        t.n0 = p.n_main + (u / p.tiles_m) * (GATED ? t.w / 2 : t.w);
+    }
+    return t;
+}
+
+__device__ __forceinline__ uint4 lp_ld_res(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// z = acc * (sa * scale) + bias of 32 columns; cols: the tile's scales, then
+// its biases LP_BN floats on, in shared memory (all lanes read one address)
+__device__ __forceinline__ void lp_scaled(const uint32_t (&r)[32], const float *cols, float sa, bool bias,
+                                          float (&v)[32]) {
+    const float4 *s4 = reinterpret_cast<const float4 *>(cols);
+    const float4 *b4 = reinterpret_cast<const float4 *>(cols + LP_BN);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float4 s = s4[q];
+        const float4 b = bias ? b4[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[4 * q] = fmaf(__uint_as_float(r[4 * q]), sa * s.x, b.x);
+        v[4 * q + 1] = fmaf(__uint_as_float(r[4 * q + 1]), sa * s.y, b.y);
+        v[4 * q + 2] = fmaf(__uint_as_float(r[4 * q + 2]), sa * s.z, b.z);
+        v[4 * q + 3] = fmaf(__uint_as_float(r[4 * q + 3]), sa * s.w, b.w);
+    }
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kLpThreads, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                   const __grid_constant__ CUtensorMap tmap_b,
+                   const __grid_constant__ CUtensorMap tmap_bt, const PairArgs p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (sbase - raw);
+    float *cols_sh = reinterpret_cast<float *>(gbase + LP_STAGES * kLpStageBytes);
+    const uint32_t bar0 = sbase + LP_STAGES * kLpStageBytes + kLpColBytes;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (LP_STAGES + s); };
+    auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * LP_STAGES + b); };
+    auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * LP_STAGES + 2 + b); };
+    const uint32_t done_bar = bar0 + 8u * (2 * LP_STAGES + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + LP_STAGES * kLpStageBytes + kLpColBytes +
+                                                       kLpBarriers * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < LP_STAGES; ++s) {
+            mbar_init(full_bar(s), 1);   // the even CTA's arming arrival (+ both CTAs' bytes)
+            mbar_init(empty_bar(s), 1);  // the MMA commit, multicast to both CTAs
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), 2 * kLpEpiWarps);  // the pair's epilogue warps
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)),
+                     "r"(kLpTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before either touches the other's
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1u);
+
+    const int pair = static_cast<int>(blockIdx.x) >> 1;
+    const int num_pairs = static_cast<int>(gridDim.x) >> 1;
+    const int num_tiles = p.main_tiles + p.tiles_m * p.tail_n;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
+            if (p.tail_n > 0)
+                asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_bt)) : "memory");
+            uint32_t armed = 0, armed_parity = 0;  // even CTA: stages armed, their parity
+            auto arm = [&](int stage, uint32_t phase, int w) {
+                if (!leader) return;
+                // both CTAs' bytes: a rows and half of the tile's weight rows
+                mbar_expect_tx(full_bar(stage), 2 * (kLpABytes + static_cast<uint32_t>(w / 2) * LP_BK));
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            };
+            auto load_a = [&](int stage, int kb, const LpTile &t) {
+                lp_tma(sbase + stage * kLpStageBytes, &tmap_a, kb * LP_BK,
+                       t.mt * 2 * LP_BM + static_cast<int>(rank) * LP_BM, map_to_rank(full_bar(stage), 0));
+            };
+            auto load_w = [&](int stage, int kb, const LpTile &t) {
+                const int row = GATED ? static_cast<int>(rank) * p.e.width + t.n0
+                                      : t.n0 + static_cast<int>(rank) * (t.w / 2);
+                lp_tma(sbase + stage * kLpStageBytes + kLpABytes, t.w != LP_BN ? &tmap_bt : &tmap_b,
+                       kb * LP_BK, row, map_to_rank(full_bar(stage), 0));
+            };
+            // stable weights: the first tile's first stages before the wait
+            int pre = 0;
+            if (p.prefetch && pair < num_tiles) {
+                const LpTile t = lp_tile<GATED>(p, pair);
+                pre = p.num_k_blocks < LP_STAGES ? p.num_k_blocks : LP_STAGES;
+                for (int s = 0; s < pre; ++s) {
+                    arm(s, 0, t.w);
+                    load_w(s, s, t);
+                }
+            }
+            pdl_wait();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+                const LpTile t = lp_tile<GATED>(p, tile);
+                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+                    if (pre > 0) {  // armed, its weights on their way
+                        --pre;
+                        load_a(stage, kb, t);
+                    } else {
+                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.wait_cycles,
+                                       peer_abort)) {
+                            ok = false;
+                            break;
+                        }
+                        arm(stage, phase, t.w);
+                        load_a(stage, kb, t);
+                        load_w(stage, kb, t);
+                    }
+                    if (++stage == LP_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // every armed stage lands before either CTA passes the final
+            // cluster barrier
+            for (int s = 0; s < LP_STAGES; ++s)
+                if (armed & (1u << s)) mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.status);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            if (p.stall & kStallMma)
+                ok = mbar_wait(done_bar, 0, abort_flag, p.status, p.wait_cycles, peer_abort);
+            for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+                if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status, p.wait_cycles,
+                               peer_abort))
+                    break;
+                tc_fence_after();
+                const uint32_t idesc = lp_idesc(tile < p.main_tiles ? LP_BN : p.tail_w);
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * LP_BN);
+                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+                    if (!mbar_wait_fast(full_bar(stage), phase, abort_flag, p.status, p.wait_cycles,
+                                        peer_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = sbase + stage * kLpStageBytes;
+                    const uint64_t da = sw128_desc(sa), db = sw128_desc(sa + kLpABytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        lp_mma(d_tmem, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
+                    lp_commit(empty_bar(stage));
+                    if (++stage == LP_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                lp_commit(tfull_bar(acc));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            // every MMA issued has retired
+            lp_commit(done_bar);
+            mbar_wait_drain(done_bar, 0, p.status);
+        }
+        __syncwarp();
+    } else {
+        pdl_wait();
+        const int quarter = warp & 3;     // the TMEM lanes this warp may read
+        const int grp = (warp - 2) >> 2;  // its half of each tile's chunks
+        const int et = static_cast<int>(threadIdx.x) - 64;
+        const int row = static_cast<int>(rank) * LP_BM + quarter * 32 + lane;
+        const float sa0 = epi_ld_f32(p.a_scale);
+        const OutDiv od = OutDiv::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
+        const bool bias = p.e.bias != nullptr;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int tile = pair; tile < num_tiles; tile += num_pairs) {
+            const LpTile t = lp_tile<GATED>(p, tile);
+            const int half = t.w / 2;
+            const int m = t.mt * 2 * LP_BM + row;
+            const bool row_ok = m < p.M;
+            // column et's scale and bias (accumulator order) for every thread;
+            // the buffer was last read two tiles ago, before the barrier of
+            // the tile in between
+            float *cols = cols_sh + acc * 2 * LP_BN;
+            {
+                int n = t.n0 + et;  // weight row of accumulator column et
+                bool in = et < t.w && n < p.e.width;
+                if constexpr (GATED) {
+                    if (et >= half) n = p.e.width + t.n0 + et - half;
+                    in = et < t.w && t.n0 + (et >= half ? et - half : et) < p.e.width;
+                }
+                cols[et] = in ? epi_ld_f32(p.w_scale + (p.w_per_channel ? n : 0)) : 0.0f;
+                if (bias) cols[LP_BN + et] = in ? epi_bias(p.e, n) : 0.0f;
+            }
+            const float sa = p.a_per_token ? (row_ok ? epi_ld_f32(p.a_scale + m) : 0.0f) : sa0;
+            const int chunks = GATED ? half / 32 : t.w / 32;
+            const int c_begin = grp * chunks / 2, c_end = (grp + 1) * chunks / 2;
+            // residual of a chunk: 32 16-bit values of this row
+            uint4 res[4];
+            auto load_res = [&](int c) {
+                const int n0 = t.n0 + c * 32;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) res[q] = make_uint4(0, 0, 0, 0);
+                if (p.e.residual == nullptr || !row_ok || n0 >= p.e.width) return;
+                const uint16_t *src = static_cast<const uint16_t *>(p.e.residual) +
+                                      static_cast<size_t>(m) * p.e.width + n0;
+                res[0] = lp_ld_res(src);
+                res[1] = lp_ld_res(src + 8);
+                if (n0 + 32 <= p.e.width) {  // width % 16 == 0: else 16 columns remain
+                    res[2] = lp_ld_res(src + 16);
+                    res[3] = lp_ld_res(src + 24);
+                }
+            };
+            if (c_begin < c_end) load_res(c_begin);
+            asm volatile("bar.sync 1, %0;" ::"n"(kLpEpiThreads) : "memory");
+            if (ok) ok = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status, p.wait_cycles, peer_abort);
+            if (!ok) continue;  // the others still meet at the barrier above
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                   static_cast<uint32_t>(acc * LP_BN);
+#pragma unroll 1
+            for (int c = c_begin; c < c_end; ++c) {
+                const int n0 = t.n0 + c * 32;
+                float v[32];
+                {
+                    uint32_t r[32];
+                    tmem_ld32(taddr + static_cast<uint32_t>(c * 32), r);
+                    lp_scaled(r, cols + c * 32, sa, bias, v);
+                }
+                activate(v, p.e.act);
+                if constexpr (GATED) {
+                    uint32_t r[32];
+                    float u[32];
+                    tmem_ld32(taddr + static_cast<uint32_t>(half + c * 32), r);
+                    lp_scaled(r, cols + half + c * 32, sa, bias, u);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= u[j];
+                }
+                if (p.e.residual != nullptr) {
+                    const uint32_t rw[16] = {res[0].x, res[0].y, res[0].z, res[0].w, res[1].x, res[1].y,
+                                             res[1].z, res[1].w, res[2].x, res[2].y, res[2].z, res[2].w,
+                                             res[3].x, res[3].y, res[3].z, res[3].w};
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 f = widen_pair(rw[j], p.e.out_dtype);
+                        v[2 * j] += f.x;
+                        v[2 * j + 1] += f.y;
+                    }
+                    if (c + 1 < c_end) load_res(c + 1);
+                }
+                if (!row_ok || n0 >= p.e.width) continue;
+                const bool full32 = n0 + 32 <= p.e.width;
+                if (p.e.out_dtype == FP8L_E4M3) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = out_e4m3x2(od.quot(v[4 * i]), od.quot(v[4 * i + 1])) |
+                               (out_e4m3x2(od.quot(v[4 * i + 2]), od.quot(v[4 * i + 3])) << 16);
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.e.y) +
+                                                           static_cast<size_t>(m) * p.e.width + n0);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (full32) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack_out16(v[2 * i], v[2 * i + 1], p.e.out_dtype);
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.e.y) +
+                                                           static_cast<size_t>(m) * p.e.width + n0);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    if (full32) {
+                        dst[2] = make_uint4(w[8], w[9], w[10], w[11]);
+                        dst[3] = make_uint4(w[12], w[13], w[14], w[15]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    mbar_arrive(tempty_bar(acc));
+                else
+                    mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+
+    // every copy, MMA and TMEM read of the pair is finished before TMEM is
+    // released and before either CTA's shared memory goes away
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(kLpTmemCols)
+                     : "memory");
+    }
+}
+
+// Tile plan: 256-wide tiles, then the columns left over in tiles `tail_w`
+// wide (accumulator columns, a multiple of `step`) when the most loaded pair
+// then has less to do.  A tile w wide costs max(w, 96) / 256 of a full one
+// (its tokens are loaded whatever its width).
+struct LpPlan {
+    int main_tiles, n_main, tail_w, tail_n;  // n_main in accumulator columns
+};
+
+LpPlan lp_plan(int tiles_m, int cols, int pairs, int step) {
+    const int nb = (cols + LP_BN - 1) / LP_BN;
+    const int64_t total = int64_t(tiles_m) * nb;
+    LpPlan best{static_cast<int>(total), nb * LP_BN, 0, 0};
+    auto cost = [&](int64_t main_tiles, int64_t tail_tiles, int w) {
+        // main tiles go round the pairs, the tail tiles start after the last
+        const int64_t mr = main_tiles % pairs, tr = tail_tiles % pairs;
+        const int64_t wc = w > 96 ? w : 96;
+        int64_t worst = 0;
+        for (int q = 0; q < pairs; ++q) {
+            const int64_t mc = main_tiles / pairs + (q < mr ? 1 : 0);
+            const int64_t d = (q - mr + pairs) % pairs;
+            const int64_t c = mc * LP_BN + (tail_tiles / pairs + (d < tr ? 1 : 0)) * wc;
+            worst = c > worst ? c : worst;
+        }
+        return worst;
+    };
+    if (total % pairs == 0) return best;
+    int64_t best_cost = cost(total, 0, LP_BN);
+    int64_t c = total / pairs * pairs / tiles_m;  // whole blocks before the tail
+    if (c > nb) c = nb;
+    const int rem = cols - static_cast<int>(c) * LP_BN;
+    if (rem <= 0) return best;
+    for (int w = LP_BN - step; w >= step; w -= step) {
+        const int tail_n = (rem + w - 1) / w;
+        const int64_t cst = cost(c * tiles_m, int64_t(tail_n) * tiles_m, w);
+        if (cst < best_cost) {
+            best_cost = cst;
+            best = LpPlan{static_cast<int>(c) * tiles_m, static_cast<int>(c) * LP_BN, w, tail_n};
+        }
+    }
+    return best;
+}
+
+constexpr int kLpMaxDevices = 64;
+std::atomic<int> g_lp_ready[kLpMaxDevices];
+
+}  // namespace
+
+int launch_linear_pair(const LinearCall &c) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kLpMaxDevices || c.sms < 2) return FP8L_ECUDA;
+    if (!g_lp_ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(linear_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kLpSmemBytes)) != cudaSuccess ||
+            cudaFuncSetAttribute(linear_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kLpSmemBytes)) != cudaSuccess)
+            return FP8L_ECUDA;
+        g_lp_ready[dev].store(1, std::memory_order_release);
+    }
+    PairArgs p{};
+    p.M = c.M;
+    p.num_k_blocks = (c.K + LP_BK - 1) / LP_BK;
+    p.tiles_m = static_cast<int>((int64_t(c.M) + 2 * LP_BM - 1) / (2 * LP_BM));
+    const int pairs = c.sms / 2;
+    const LpPlan plan = lp_plan(p.tiles_m, c.gated ? 2 * c.e.width : c.e.width, pairs, c.gated ? 64 : 32);
+    p.main_tiles = plan.main_tiles;
+    p.n_main = c.gated ? plan.n_main / 2 : plan.n_main;
+    p.tail_w = plan.tail_w;
+    p.tail_n = plan.tail_n;
+    p.prefetch = c.stable ? 1 : 0;
+    p.a_scale = c.a_scale;
+    p.a_per_token = c.a_per_token;
+    p.w_scale = c.w_scale;
+    p.w_per_channel = c.w_per_channel;
+    p.e = c.e;
+    p.status = c.status;
+    const WaitConfig wc = wait_config();
+    p.wait_cycles = wc.cycles;
+    p.stall = wc.stall;
+
+    CUtensorMap ma, mb, mbt;
+    if (make_kmajor_map(&ma, c.x, c.M, c.K, LP_BK, LP_BM) != FP8L_OK ||
+        make_kmajor_map(&mb, c.w, c.N, c.K, LP_BK, LP_BN / 2) != FP8L_OK)
+        return FP8L_ECUDA;
+    mbt = mb;
+    if (plan.tail_n > 0 && make_kmajor_map(&mbt, c.w, c.N, c.K, LP_BK, plan.tail_w / 2) != FP8L_OK)
+        return FP8L_ECUDA;
+
+    const int64_t tiles = int64_t(plan.main_tiles) + int64_t(p.tiles_m) * plan.tail_n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
+    cfg.blockDim = dim3(kLpThreads, 1, 1);
+    cfg.dynamicSmemBytes = kLpSmemBytes;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.stable ? 2 : 1;
+    const cudaError_t e = c.gated ? cudaLaunchKernelEx(&cfg, linear_pair_kernel<true>, ma, mb, mbt, p)
+                                  : cudaLaunchKernelEx(&cfg, linear_pair_kernel<false>, ma, mb, mbt, p);
+    if (e != cudaSuccess) return FP8L_ECUDA;
+    return launch_status();
+}
+
+}  // namespace fp8l

@@ -143,12 +143,6 @@ __device__ __forceinline__ uint2 ld_global_uint2(const void *p) {
     return v;
 }
 
-__device__ __forceinline__ float2 widen_pair(uint32_t w, int dtype) {
-    if (dtype == FP8L_BF16)
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-
 // Four columns of the float tile, the cluster's partials added in rank order.
 __device__ __forceinline__ float4 ls_sum(uint32_t off, int split) {
     if (split == 1) return ld_shared_float4(off);
