@@ -9,9 +9,7 @@
 //
 // Everything is float32 and rounded once, by the output cast.  The logistic
 // forms are written as z / (1 + e^-u): no cancellation for negative z, and an
-// overflowing exponential gives the right limit 0.  GELU's normal
-// distribution is erfc(-z / sqrt 2) / 2, which keeps its relative accuracy
-// where 1 + erf would cancel.
+// overflowing exponential gives the right limit 0.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,8 +35,25 @@ namespace {
 
 __device__ __forceinline__ float silu_of(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 
+// z Phi(z) = max(z, 0) - |z| h(|z|), h(a) = erfc(a / sqrt 2) / 2: no
+// cancellation for negative z.  h(a) = e^(-a^2 / 2) t R(t), t = 1 / (1 + 0.36
+// a), which maps a >= 0 to (0, 1] and gives the right decay 1 / a; R is the
+// polynomial of degree 6 with the least largest relative error over 0 <= a <=
+// 14, fitted by reweighted least squares: 9e-7, below the exponential's own
+// error.  (erfcf in its place cost 20 to 30 % of a product with K = 4096: 1024
+// x 28672 112 us against 80 without an activation.)
 __device__ __forceinline__ float gelu_of(float z) {
-    return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    const float a = fabsf(z);
+    const float t = __fdividef(1.0f, fmaf(0.36f, a, 1.0f));
+    float r = 0.047059460972601275f;
+    r = fmaf(r, t, -0.1797755885232244f);
+    r = fmaf(r, t, 0.18096890501073565f);
+    r = fmaf(r, t, 0.02653901863037719f);
+    r = fmaf(r, t, 0.13972304963865187f);
+    r = fmaf(r, t, 0.14177175868564995f);
+    r = fmaf(r, t, 0.14371309497733017f);
+    const float e = __expf(-0.5f * a * a);
+    return fmaf(-a * e, t * r, fmaxf(z, 0.0f));
 }
 
 // z (1 + tanh u) / 2 with u = sqrt(2 / pi) (z + 0.044715 z^3) is z times the

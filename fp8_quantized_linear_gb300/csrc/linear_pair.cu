@@ -11,7 +11,7 @@
 // A cluster of two CTAs computes a tile of 256 tokens by 256 weight rows with
 // tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 32): each CTA stages 128
 // rows of a and half of the tile's weight rows per 128-deep k-block (32 KB a
-// stage, six stages), the MMA reads the peer's halves from its shared memory,
+// stage, five stages), the MMA reads the peer's halves from its shared memory,
 // and each CTA's TMEM receives its 128 tokens of the accumulator (512
 // columns: two accumulators, so the epilogue of one tile runs under the MMAs
 // of the next).  With a gate the even CTA stages 128 gate rows and the odd
@@ -27,9 +27,12 @@
 //   warps 2-9  epilogue in each CTA, two warps a TMEM lane quarter (each half
 //              of the tile's 32-column chunks).  A tile's scales and biases
 //              are spread over the 256 threads once and read back from shared
-//              memory (any type, any alignment, one load a column); the
-//              residual of a row's next chunk is loaded while the present
-//              one is computed.
+//              memory (any type, any alignment, one load a column).  16-bit
+//              results and residuals cross global memory as TMA boxes of 32
+//              rows by 32 columns through a warp's own two buffers (a lane
+//              has a row: plain 16-byte accesses of 32 different lines each
+//              took the load/store unit from the MMA's operand reads; 1024 x
+//              28672 x 4096 with a residual 88.9 us, with boxes 84.6).
 // Tail tiles: 256-wide tiles fill whole rounds of the SM pairs; the columns
 // left over become narrower tiles when that ends the last round sooner.
 // Waits are bounded; a time-out raises both CTAs' abort flags, and both meet
@@ -46,7 +49,7 @@ namespace {
 constexpr int LP_BM = 128;  // tokens a CTA; a pair covers 256
 constexpr int LP_BN = 256;  // weight rows a tile; each CTA stages half
 constexpr int LP_BK = 128;
-constexpr int LP_STAGES = 6;
+constexpr int LP_STAGES = 5;  // (six: the same, and no room for the boxes)
 constexpr int kLpABytes = LP_BM * LP_BK;
 constexpr int kLpBBytes = (LP_BN / 2) * LP_BK;
 constexpr int kLpStageBytes = kLpABytes + kLpBBytes;
@@ -54,9 +57,13 @@ constexpr int kLpEpiWarps = 8;
 constexpr int kLpEpiThreads = 32 * kLpEpiWarps;
 constexpr int kLpThreads = 64 + kLpEpiThreads;
 constexpr int kLpBarriers = 2 * LP_STAGES + 2 + 2 + 1;
+constexpr int kLpBoxBytes = 32 * 64;             // 32 rows of 32 16-bit values
+constexpr int kLpBoxes = 2 * kLpEpiWarps;
 constexpr int kLpColBytes = 2 * 2 * LP_BN * 4;  // two tiles' scales and biases
-constexpr size_t kLpSmemBytes =
-    1024 + size_t(LP_STAGES) * kLpStageBytes + kLpColBytes + kLpBarriers * 8 + 16;
+constexpr int kLpBoxOffset = LP_STAGES * kLpStageBytes;  // from the 1024-aligned base
+constexpr int kLpColOffset = kLpBoxOffset + kLpBoxes * kLpBoxBytes;
+constexpr int kLpBarOffset = kLpColOffset + kLpColBytes;
+constexpr size_t kLpSmemBytes = 1024 + kLpBarOffset + (kLpBarriers + kLpBoxes) * 8 + 16;
 constexpr uint32_t kLpTmemCols = 2 * LP_BN;
 
 struct PairArgs {
@@ -128,11 +135,37 @@ __device__ __forceinline__ LpTile lp_tile(const PairArgs &p, int tile) {
     return t;
 }
 
-__device__ __forceinline__ uint4 lp_ld_res(const void *p) {
+// a box between shared memory and a [rows, bytes] matrix (x in bytes)
+__device__ __forceinline__ void lp_load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    mbar_expect_tx(bar, kLpBoxBytes);
+    tma_load_2d(dst, map, x, y, bar);
+}
+
+__device__ __forceinline__ void lp_store_box(const CUtensorMap *map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// until at most N of this thread's stores have still to read shared memory
+template <int N>
+__device__ __forceinline__ void lp_stores_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// address of 16-byte piece j of lane `row`'s 64 bytes in a box (64-byte
+// swizzle: eight rows of a wavefront hit different banks)
+__device__ __forceinline__ uint32_t lp_box_piece(uint32_t box, int row, int j) {
+    return box + static_cast<uint32_t>(row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint4 lp_ld_shared(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
+                 : "r"(addr)
                  : "memory");
     return v;
 }
@@ -158,21 +191,23 @@ template <bool GATED>
 __global__ void __launch_bounds__(kLpThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_b,
-                   const __grid_constant__ CUtensorMap tmap_bt, const PairArgs p) {
+                   const __grid_constant__ CUtensorMap tmap_bt,
+                   const __grid_constant__ CUtensorMap tmap_y,
+                   const __grid_constant__ CUtensorMap tmap_r, const PairArgs p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (sbase - raw);
-    float *cols_sh = reinterpret_cast<float *>(gbase + LP_STAGES * kLpStageBytes);
-    const uint32_t bar0 = sbase + LP_STAGES * kLpStageBytes + kLpColBytes;
+    float *cols_sh = reinterpret_cast<float *>(gbase + kLpColOffset);
+    const uint32_t bar0 = sbase + kLpBarOffset;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (LP_STAGES + s); };
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * LP_STAGES + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * LP_STAGES + 2 + b); };
     const uint32_t done_bar = bar0 + 8u * (2 * LP_STAGES + 4);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + LP_STAGES * kLpStageBytes + kLpColBytes +
-                                                       kLpBarriers * 8);
+    const uint32_t box_bar0 = done_bar + 8u;  // residual boxes: two an epilogue warp
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kLpBarOffset + (kLpBarriers + kLpBoxes) * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -190,6 +225,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             mbar_init(tempty_bar(b), 2 * kLpEpiWarps);  // the pair's epilogue warps
         }
         mbar_init(done_bar, 1);
+        for (int b = 0; b < kLpBoxes; ++b) mbar_init(box_bar0 + 8u * b, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -219,31 +255,21 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if (p.tail_n > 0)
                 asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_bt)) : "memory");
             uint32_t armed = 0, armed_parity = 0;  // even CTA: stages armed, their parity
-            auto arm = [&](int stage, uint32_t phase, int w) {
-                if (!leader) return;
-                // both CTAs' bytes: a rows and half of the tile's weight rows
-                mbar_expect_tx(full_bar(stage), 2 * (kLpABytes + static_cast<uint32_t>(w / 2) * LP_BK));
-                armed |= 1u << stage;
-                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-            };
-            auto load_a = [&](int stage, int kb, const LpTile &t) {
-                lp_tma(sbase + stage * kLpStageBytes, &tmap_a, kb * LP_BK,
-                       t.mt * 2 * LP_BM + static_cast<int>(rank) * LP_BM, map_to_rank(full_bar(stage), 0));
-            };
-            auto load_w = [&](int stage, int kb, const LpTile &t) {
-                const int row = GATED ? static_cast<int>(rank) * p.e.width + t.n0
-                                      : t.n0 + static_cast<int>(rank) * (t.w / 2);
-                lp_tma(sbase + stage * kLpStageBytes + kLpABytes, t.w != LP_BN ? &tmap_bt : &tmap_b,
-                       kb * LP_BK, row, map_to_rank(full_bar(stage), 0));
-            };
+            const uint32_t full0 = map_to_rank(full_bar(0), 0);  // the even CTA's full barriers
+            const int a_row = static_cast<int>(rank) * LP_BM;
             // stable weights: the first tile's first stages before the wait
             int pre = 0;
             if (p.prefetch && pair < num_tiles) {
                 const LpTile t = lp_tile<GATED>(p, pair);
+                const CUtensorMap *map = t.w != LP_BN ? &tmap_bt : &tmap_b;
+                const int w_row = t.n0 + static_cast<int>(rank) * (GATED ? p.e.width : t.w / 2);
                 pre = p.num_k_blocks < LP_STAGES ? p.num_k_blocks : LP_STAGES;
                 for (int s = 0; s < pre; ++s) {
-                    arm(s, 0, t.w);
-                    load_w(s, s, t);
+                    if (leader) {
+                        mbar_expect_tx(full_bar(s), 2 * (kLpABytes + static_cast<uint32_t>(t.w / 2) * LP_BK));
+                        armed |= 1u << s;
+                    }
+                    lp_tma(sbase + s * kLpStageBytes + kLpABytes, map, s * LP_BK, w_row, full0 + 8u * s);
                 }
             }
             pdl_wait();
@@ -252,20 +278,34 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             bool ok = true;
             for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
                 const LpTile t = lp_tile<GATED>(p, tile);
-                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
-                    if (pre > 0) {  // armed, its weights on their way
-                        --pre;
-                        load_a(stage, kb, t);
-                    } else {
-                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.wait_cycles,
-                                       peer_abort)) {
-                            ok = false;
-                            break;
-                        }
-                        arm(stage, phase, t.w);
-                        load_a(stage, kb, t);
-                        load_w(stage, kb, t);
+                // bytes of a stage in both CTAs: a rows and half of the tile's weight rows
+                const uint32_t bytes = 2 * (kLpABytes + static_cast<uint32_t>(t.w / 2) * LP_BK);
+                const CUtensorMap *map = t.w != LP_BN ? &tmap_bt : &tmap_b;
+                const int x_row = t.mt * 2 * LP_BM + a_row;
+                const int w_row = t.n0 + static_cast<int>(rank) * (GATED ? p.e.width : t.w / 2);
+                int kb = 0;
+                for (; kb < pre; ++kb)  // armed, the weights on their way
+                    lp_tma(sbase + kb * kLpStageBytes, &tmap_a, kb * LP_BK, x_row, full0 + 8u * kb);
+                if (kb > 0) {
+                    stage = kb == LP_STAGES ? 0 : kb;
+                    phase = kb == LP_STAGES ? 1u : 0u;
+                    pre = 0;
+                }
+                for (; kb < p.num_k_blocks; ++kb) {
+                    if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.wait_cycles,
+                                   peer_abort)) {
+                        ok = false;
+                        break;
                     }
+                    const uint32_t sa = sbase + stage * kLpStageBytes;
+                    const uint32_t fb = full0 + 8u * stage;
+                    if (leader) {
+                        mbar_expect_tx(full_bar(stage), bytes);
+                        armed |= 1u << stage;
+                        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    }
+                    lp_tma(sa, &tmap_a, kb * LP_BK, x_row, fb);
+                    lp_tma(sa + kLpABytes, map, kb * LP_BK, w_row, fb);
                     if (++stage == LP_STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -331,6 +371,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         const float sa0 = epi_ld_f32(p.a_scale);
         const OutDiv od = OutDiv::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
         const bool bias = p.e.bias != nullptr;
+        const uint32_t box0 = sbase + kLpBoxOffset + static_cast<uint32_t>((warp - 2) * 2 * kLpBoxBytes);
+        const uint32_t box_bar = box_bar0 + 16u * (warp - 2);
+        int buf = 0;             // the box of the next chunk
+        uint32_t box_phase = 0;  // parities of the two boxes' barriers
+        bool loading = false;    // a residual box on its way into `buf`
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -356,25 +401,23 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const float sa = p.a_per_token ? (row_ok ? epi_ld_f32(p.a_scale + m) : 0.0f) : sa0;
             const int chunks = GATED ? half / 32 : t.w / 32;
             const int c_begin = grp * chunks / 2, c_end = (grp + 1) * chunks / 2;
-            // residual of a chunk: 32 16-bit values of this row
-            uint4 res[4];
+            // (a box partly outside the matrix is cut by TMA; one wholly outside is left out)
+            const int box_row = t.mt * 2 * LP_BM + static_cast<int>(rank) * LP_BM + quarter * 32;
+            auto box_in = [&](int c) { return box_row < p.M && t.n0 + c * 32 < p.e.width; };
             auto load_res = [&](int c) {
-                const int n0 = t.n0 + c * 32;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) res[q] = make_uint4(0, 0, 0, 0);
-                if (p.e.residual == nullptr || !row_ok || n0 >= p.e.width) return;
-                const uint16_t *src = static_cast<const uint16_t *>(p.e.residual) +
-                                      static_cast<size_t>(m) * p.e.width + n0;
-                res[0] = lp_ld_res(src);
-                res[1] = lp_ld_res(src + 8);
-                if (n0 + 32 <= p.e.width) {  // width % 16 == 0: else 16 columns remain
-                    res[2] = lp_ld_res(src + 16);
-                    res[3] = lp_ld_res(src + 24);
+                if (p.e.residual == nullptr || !box_in(c)) return;
+                if (lane == 0) {
+                    lp_stores_read<0>();  // the buffer's last store is through with it
+                    lp_load_box(box0 + buf * kLpBoxBytes, &tmap_r, 2 * (t.n0 + c * 32), box_row,
+                                box_bar + 8u * buf);
                 }
+                loading = true;
             };
-            if (c_begin < c_end) load_res(c_begin);
+            if (ok && c_begin < c_end) load_res(c_begin);
             asm volatile("bar.sync 1, %0;" ::"n"(kLpEpiThreads) : "memory");
-            if (ok) ok = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status, p.wait_cycles, peer_abort);
+            if (ok)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status,
+                                                       p.wait_cycles, peer_abort));
             if (!ok) continue;  // the others still meet at the barrier above
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -397,44 +440,59 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] *= u[j];
                 }
-                if (p.e.residual != nullptr) {
-                    const uint32_t rw[16] = {res[0].x, res[0].y, res[0].z, res[0].w, res[1].x, res[1].y,
-                                             res[1].z, res[1].w, res[2].x, res[2].y, res[2].z, res[2].w,
-                                             res[3].x, res[3].y, res[3].z, res[3].w};
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 f = widen_pair(rw[j], p.e.out_dtype);
-                        v[2 * j] += f.x;
-                        v[2 * j + 1] += f.y;
-                    }
-                    if (c + 1 < c_end) load_res(c + 1);
-                }
-                if (!row_ok || n0 >= p.e.width) continue;
-                const bool full32 = n0 + 32 <= p.e.width;
+                if (!box_in(c)) continue;
                 if (p.e.out_dtype == FP8L_E4M3) {
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         w[i] = out_e4m3x2(od.quot(v[4 * i]), od.quot(v[4 * i + 1])) |
                                (out_e4m3x2(od.quot(v[4 * i + 2]), od.quot(v[4 * i + 3])) << 16);
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.e.y) +
-                                                           static_cast<size_t>(m) * p.e.width + n0);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (full32) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                } else {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack_out16(v[2 * i], v[2 * i + 1], p.e.out_dtype);
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.e.y) +
-                                                           static_cast<size_t>(m) * p.e.width + n0);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    if (full32) {
-                        dst[2] = make_uint4(w[8], w[9], w[10], w[11]);
-                        dst[3] = make_uint4(w[12], w[13], w[14], w[15]);
+                    if (row_ok) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.e.y) +
+                                                               static_cast<size_t>(m) * p.e.width + n0);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (n0 + 32 <= p.e.width) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     }
+                    __syncwarp();
+                    continue;
                 }
+                const uint32_t box = box0 + buf * kLpBoxBytes;
+                if (p.e.residual != nullptr) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(box_bar + 8u * buf, (box_phase >> buf) & 1u,
+                                                           abort_flag, p.status, p.wait_cycles, peer_abort));
+                    if (!ok) break;  // (the lanes decide together: tcgen05.ld needs the whole warp)
+                    box_phase ^= 1u << buf;
+                    loading = false;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 w = lp_ld_shared(lp_box_piece(box, lane, q));
+                        const uint32_t rw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = widen_pair(rw[j], p.e.out_dtype);
+                            v[8 * q + 2 * j] += f.x;
+                            v[8 * q + 2 * j + 1] += f.y;
+                        }
+                    }
+                } else {
+                    if (lane == 0) lp_stores_read<1>();  // all but the other buffer's store
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st_shared_v4(lp_box_piece(box, lane, q), pack_out16(v[8 * q], v[8 * q + 1], p.e.out_dtype),
+                                 pack_out16(v[8 * q + 2], v[8 * q + 3], p.e.out_dtype),
+                                 pack_out16(v[8 * q + 4], v[8 * q + 5], p.e.out_dtype),
+                                 pack_out16(v[8 * q + 6], v[8 * q + 7], p.e.out_dtype));
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                buf ^= 1;
+                // the next chunk's residual before this one's store, whose
+                // reading it would otherwise wait for
+                if (c + 1 < c_end) load_res(c + 1);
+                if (lane == 0) lp_store_box(&tmap_y, 2 * n0, box_row, box);
             }
+            if (!ok) continue;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -446,6 +504,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
+        // this warp's boxes have landed and left before the CTA exits
+        if (lane == 0) {
+            if (loading) mbar_wait_drain(box_bar + 8u * buf, (box_phase >> buf) & 1u, p.status);
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
     }
 
     // every copy, MMA and TMEM read of the pair is finished before TMEM is
@@ -548,6 +612,17 @@ int launch_linear_pair(const LinearCall &c) {
     if (plan.tail_n > 0 && make_kmajor_map(&mbt, c.w, c.N, c.K, LP_BK, plan.tail_w / 2) != FP8L_OK)
         return FP8L_ECUDA;
 
+    CUtensorMap my = ma, mr = ma;  // (unused ones are any valid map)
+    if (c.e.out_dtype != FP8L_E4M3) {
+        const uint64_t dims[2] = {static_cast<uint64_t>(c.e.width) * 2, static_cast<uint64_t>(c.M)};
+        const uint64_t strides[1] = {static_cast<uint64_t>(c.e.width) * 2};
+        const uint32_t box[2] = {64, 32};
+        if (make_swizzle64_map(&my, c.e.y, 2, dims, strides, box) != FP8L_OK ||
+            (c.e.residual != nullptr &&
+             make_swizzle64_map(&mr, c.e.residual, 2, dims, strides, box) != FP8L_OK))
+            return FP8L_ECUDA;
+    }
+
     const int64_t tiles = int64_t(plan.main_tiles) + int64_t(p.tiles_m) * plan.tail_n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
@@ -563,8 +638,8 @@ int launch_linear_pair(const LinearCall &c) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = c.stable ? 2 : 1;
-    const cudaError_t e = c.gated ? cudaLaunchKernelEx(&cfg, linear_pair_kernel<true>, ma, mb, mbt, p)
-                                  : cudaLaunchKernelEx(&cfg, linear_pair_kernel<false>, ma, mb, mbt, p);
+    const cudaError_t e = c.gated ? cudaLaunchKernelEx(&cfg, linear_pair_kernel<true>, ma, mb, mbt, my, mr, p)
+                                  : cudaLaunchKernelEx(&cfg, linear_pair_kernel<false>, ma, mb, mbt, my, mr, p);
     if (e != cudaSuccess) return FP8L_ECUDA;
     return launch_status();
 }

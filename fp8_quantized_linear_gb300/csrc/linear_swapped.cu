@@ -358,11 +358,13 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
     };
     load_batch(first);
 
+    // (a warp's lanes decide together: tcgen05.ld needs the whole warp)
     bool ok = mbar_wait(done_bar, 0, abort_flag, p.status, p.wait_cycles);
+    ok = __all_sync(0xFFFFFFFFu, ok && !*abort_flag);
     tc_fence_after();
     // accumulator row (weight row) 32 warp + lane, token columns 0 .. T-1 (the
     // parts' columns added), into part[t][row] at the start of the ring
-    if (ok && !*abort_flag) {
+    if (ok) {
         const int row = warp * 32 + lane;
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
         for (int c = 0; c < p.T; c += 16) {
