@@ -9,7 +9,7 @@ kernels; there is no CPU or PyTorch fallback, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 import threading
 from typing import NamedTuple
@@ -114,7 +114,7 @@ def load():
         lib.fp8_w8a16_linear.restype = I
         lib.fp8_w8a16_linear.argtypes = [P, I, P, P, I64, I64, I64, P, I, I, P, P, P, U, P]
         lib.fp8_w8a16_linear_workspace_bytes.restype = ctypes.c_size_t
-        lib.fp8_w8a16_linear_workspace_bytes.argtypes = [I, I64, I64]
+        lib.fp8_w8a16_linear_workspace_bytes.argtypes = [I, I64, I64, I64, U]
         lib.fp8_kv_plan.restype = I
         lib.fp8_kv_plan.argtypes = [P, P, I64, I64, I64, P, I64, P, I64, P, P, P, P, P, P]
         lib.fp8_qk_norm_rope_append.restype = I
@@ -483,8 +483,8 @@ def fp8_w8a16_mm(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     return y
 
 
-# The functions of the paged cache and the linear layers run once per layer and
-# step in front of kernels of a few microseconds, so their checks are written to cost little:
+# The functions of the paged cache run once per layer and step in front of
+# kernels of a few microseconds, so their checks are written to cost little:
 # one pass of plain attribute tests, the stream's handle without a Stream
 # object, no device switch when the device is current already.
 
@@ -831,49 +831,37 @@ def fp8_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
 
 # fp8l_activation
 ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
-ACT_GATED = 16
-_MM_CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.uint8: E4M3}
-_BIAS_CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
-_ws_pointers = {}  # device index: address of workspace(device)
+
+# The linear layers stand in front of kernels of a few microseconds too; their
+# checks, outputs and calls are C functions of the extension _calls.so
+# (csrc/calls.cpp), which the build makes beside the library.
+_calls = None
 
 
-def _workspace_pointer(index: int) -> int:
-    at = _ws_pointers.get(index)
-    if at is None:
-        at = _ws_pointers[index] = workspace(index).data_ptr()
-    return at
+def _load_calls():
+    global _calls
+    load()  # (refuses a library that is missing or stale)
+    path = os.path.join(_PKG, "_calls.so")
+    if not os.path.exists(path):
+        raise RuntimeError(
+            f"{path} is missing: build it with `python -c \"import __graft_entry__ as g; g.build()\"`")
+    spec = importlib.util.spec_from_file_location(f"{__package__}._calls", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.setup(_status_error, lambda index: workspace(index).data_ptr())
+    _calls = module
+    return module
 
 
-def _linear_weights(w: torch.Tensor, w_scale: torch.Tensor, N: int, K: int):
-    """Refuses weights that are not N x K codes, or scales that are not float32."""
-    if w.dtype is not _U8 or w.dim() != 2 or w.shape[0] != N or w.shape[1] != K:
-        raise ValueError("w is [N, K] E4M3 codes (uint8 or float8_e4m3fn) of x's K")
-    if w_scale.dtype is not _F32:
-        raise ValueError("scales are float32")
+def _status_error(status: int, where: str) -> Fp8LinearError:
+    return Fp8LinearError(status, where)
 
 
-def _linear_epilogue(N: int, bias, activation, gated: bool, residual, M: int, dtype):
-    """(bias pointer, bias code, activation code, residual pointer, width)"""
+def _choice(table: dict, key, what: str) -> int:
     try:
-        act = ACTIVATIONS[activation]
+        return table[key]
     except (KeyError, TypeError):
-        raise ValueError("activation is None, 'relu', 'silu', 'gelu' or 'gelu_tanh'") from None
-    width = N
-    if gated:
-        act |= ACT_GATED
-        width = N // 2
-    bias_ptr = res_ptr = None
-    code = F32
-    if bias is not None:
-        code = _BIAS_CODE.get(bias.dtype, -1)
-        if bias.shape != (N,) or code < 0:
-            raise ValueError("bias is [N] of float16, bfloat16 or float32")
-        bias_ptr = bias.data_ptr()
-    if residual is not None:
-        if residual.shape != (M, width) or residual.dtype is not dtype:
-            raise ValueError("residual is [M, N] ([M, N / 2] when gated) of the output's 16-bit type")
-        res_ptr = residual.data_ptr()
-    return bias_ptr, code, act, res_ptr, width
+        raise ValueError(f"{what} is one of {', '.join(repr(k) for k in table)}") from None
 
 
 def fp8_linear(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale: torch.Tensor,
@@ -891,106 +879,26 @@ def fp8_linear(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale:
     else bf16; uint8 for E4M3 codes of the result / out_scale (no residual
     then).  Scales, ws, stable_weights, per_token and kernel as for
     fp8_scaled_mm."""
-    index = _kv_device(a)
-    given = (w, a_scale, w_scale, bias, residual, out_scale, y, ws, a)
-    if not _kv_placed(index, given):
-        _kv_refuse(index, *given)
-    a, w = _codes(a), _codes(w)
-    if a.dtype is not _U8 or a.dim() != 2 or w.dim() != 2:
-        raise ValueError("a and w are 2-D E4M3 codes (uint8 or float8_e4m3fn)")
-    M, K = a.shape
-    N = w.shape[0]
-    _linear_weights(w, w_scale, N, K)
-    scales = w_scale.numel()
-    if scales != N and scales != 1:
-        raise ValueError("w_scale must have 1 or N entries")
-    flags = KERNELS[kernel]
-    if stable_weights:
-        flags |= WEIGHTS_STABLE
-    if per_token is None:
-        per_token = a_scale.numel() == M and M > 1
-    if a_scale.numel() != (M if per_token else 1) or a_scale.dtype is not _F32:
-        raise ValueError("a_scale is float32 with 1 entry, or M with per_token")
-    if per_token:
-        flags |= A_PER_TOKEN
-    if out_dtype is None:
-        out_dtype = (y.dtype if y is not None else
-                     residual.dtype if residual is not None else torch.bfloat16)
-    if out_dtype is torch.float8_e4m3fn:
-        out_dtype = _U8
-    code = _MM_CODE.get(out_dtype, -1)
-    scale_ptr = None
-    if code == E4M3:
-        if out_scale is None or out_scale.dtype is not _F32 or out_scale.numel() != 1:
-            raise ValueError("an E4M3 output needs out_scale, one float32")
-        if residual is not None:
-            raise ValueError("an E4M3 output takes no residual")
-        scale_ptr = out_scale.data_ptr()
-    bias_ptr, bias_code, act, res_ptr, width = _linear_epilogue(N, bias, activation, gated,
-                                                                residual, M, out_dtype)
-    if y is None:
-        y = torch.empty((M, width), dtype=out_dtype, device=a.device)
-    elif y.shape != (M, width) or _codes(y).dtype is not out_dtype:
-        raise ValueError("y is [M, N] ([M, N / 2] when gated) of out_dtype")
-    args = (a.data_ptr(), w.data_ptr(), M, N, K, a_scale.data_ptr(), w_scale.data_ptr(),
-            1 if scales != 1 else 0, bias_ptr, bias_code, act, res_ptr, scale_ptr, y.data_ptr(),
-            code, _workspace_pointer(index) if ws is None else ws.data_ptr(), flags)
-    f = (_lib or load()).fp8_linear
-    st = (f(*args, _stream_handle(index)) if _current_device() == index
-          else _kv_call(f, index, *args))
-    if st:
-        _check(st, "fp8_linear")
-    return y
-
-
-@functools.lru_cache(maxsize=4096)
-def _w8a16_linear_bytes(dtype_code: int, M: int, K: int) -> int:
-    return int((_lib or load()).fp8_w8a16_linear_workspace_bytes(dtype_code, M, K))
+    return (_calls or _load_calls()).linear(
+        a, w, a_scale, w_scale, bias, _choice(ACTIVATIONS, activation, "activation"), gated,
+        residual, out_dtype, out_scale, y, ws,
+        _choice(KERNELS, kernel, "kernel") | (WEIGHTS_STABLE if stable_weights else 0), per_token)
 
 
 def fp8_w8a16_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                      bias: torch.Tensor | None = None, activation: str | None = None,
                      gated: bool = False, residual: torch.Tensor | None = None,
                      y: torch.Tensor | None = None, stable_weights: bool = False,
-                     packed: bool = False) -> torch.Tensor:
+                     packed: bool = False, kernel: str = "auto") -> torch.Tensor:
     """The W8A16 linear layer (fp8_w8a16_linear): fp8_w8a16_mm of fp16/bf16 x
     [M, K] and E4M3 w [N, K] (per-channel w_scale [N]; packed: the output of
     fp8_pack_w8a16_weights) with bias, activation, gate and residual as in
-    fp8_linear; y and residual have x's dtype."""
-    index = _kv_device(x)
-    given = (w, w_scale, bias, residual, y, x)
-    if not _kv_placed(index, given):
-        _kv_refuse(index, *given)
-    w = _codes(w)
-    if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError("x is [M, K], float16 or bfloat16")
-    M, K = x.shape
-    N = w_scale.numel()
-    if packed:
-        if w.dtype is not _U8 or w_scale.dtype is not _F32 or \
-                w.numel() != N * (-(-K // 64) * 64):
-            raise ValueError("packed weights must be fp8_pack_w8a16_weights output for [N, K], "
-                             "w_scale [N] float32")
-    else:
-        _linear_weights(w, w_scale, N, K)
-    bias_ptr, bias_code, act, res_ptr, width = _linear_epilogue(N, bias, activation, gated,
-                                                                residual, M, x.dtype)
-    if y is None:
-        y = torch.empty((M, width), dtype=x.dtype, device=x.device)
-    elif y.shape != (M, width) or y.dtype is not x.dtype:
-        raise ValueError("y is [M, N] ([M, N / 2] when gated) of x's dtype")
-    dtype_code = _DTYPE_CODE[x.dtype]
-    # scratch of this call, from the stream's memory
-    scratch = torch.empty(_w8a16_linear_bytes(dtype_code, M, K), dtype=_U8, device=x.device)
-    args = (x.data_ptr(), dtype_code, w.data_ptr(), w_scale.data_ptr(), M, N, K,
-            bias_ptr, bias_code, act, res_ptr, y.data_ptr(), scratch.data_ptr(),
-            (WEIGHTS_STABLE if stable_weights else 0) | (WEIGHTS_PACKED if packed else 0))
-    f = (_lib or load()).fp8_w8a16_linear
-    st = (f(*args, _stream_handle(index)) if _current_device() == index
-          else _kv_call(f, index, *args))
-    if st:
-        _check(st, "fp8_w8a16_linear")
-    return y
+    fp8_linear; y and residual have x's dtype.  kernel: "auto", "stream" or
+    "swapped" (FP8L_KERNEL_*)."""
+    return (_calls or _load_calls()).w8a16_linear(
+        x, w, w_scale, bias, _choice(ACTIVATIONS, activation, "activation"), gated, residual, y,
+        _choice(KERNELS, kernel, "kernel") | (WEIGHTS_STABLE if stable_weights else 0) |
+        (WEIGHTS_PACKED if packed else 0))
 
 
 _norm_workspaces = {}  # (device, stream): workspace of its eager calls
@@ -1031,56 +939,8 @@ def fp8_add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor, gamma: torch.
     mode, q, scale, h and want_h as for fp8_rmsnorm_quant.  Returns (q uint8 or
     None, scale or None, total, h or None).  ws: needed in dynamic mode only; without it one per
     stream and one per graph capture are kept."""
-    index = _kv_device(x)
-    given = (residual, gamma, total, q, scale, h, ws, x)
-    if not _kv_placed(index, given):
-        _kv_refuse(index, *given)
-    dtype = x.dtype
-    if x.dim() != 2 or dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError("x is [M, K], float16 or bfloat16")
-    shape = x.shape
-    M, K = shape
-    if residual.shape != shape or residual.dtype is not dtype or gamma.shape != (K,) or \
-            gamma.dtype is not dtype:
-        raise ValueError("residual is [M, K] and gamma [K], of x's dtype")
-    m = NQ_MODES.get(mode, -1)
-    if m < 0:
-        raise ValueError("mode is 'dynamic', 'static', 'per_token' or 'norm_only'")
-    if ws is None:
-        ws_ptr = _norm_workspace(index).data_ptr() if m == 0 else None
-    elif ws.dtype is not _U8 or ws.numel() < fp8l_workspace_bytes():
-        raise ValueError("ws is a uint8 tensor of fp8l_workspace_bytes() elements")
-    else:
-        ws_ptr = ws.data_ptr()
-    if total is None:
-        total = torch.empty(shape, dtype=dtype, device=x.device)
-    elif total.shape != shape or total.dtype is not dtype:
-        raise ValueError("total is [M, K] of x's dtype")
-    if h is not None:
-        if h.shape != shape or h.dtype is not dtype:
-            raise ValueError("h is [M, K] of x's dtype")
-    elif want_h or m == 3:
-        h = torch.empty(shape, dtype=dtype, device=x.device)
-    codes_ptr = scale_ptr = None
-    if m != 3:
-        if q is None:
-            q = torch.empty(shape, dtype=_U8, device=x.device)
-        elif q.shape != shape or _codes(q).dtype is not _U8:
-            raise ValueError("q is [M, K] E4M3 codes (uint8 or float8_e4m3fn)")
-        entries = M if m == 2 else 1
-        if scale is None:
-            if m == 1:
-                raise ValueError("static mode needs a scale tensor")
-            scale = torch.empty(entries, dtype=_F32, device=x.device)
-        elif scale.numel() != entries or scale.dtype is not _F32:
-            raise ValueError("scale is float32 with 1 entry, or M per token")
-        codes_ptr, scale_ptr = q.data_ptr(), scale.data_ptr()
-    args = (x.data_ptr(), residual.data_ptr(), _DTYPE_CODE[dtype], gamma.data_ptr(), eps, M, K,
-            total.data_ptr(), codes_ptr, scale_ptr, m, h.data_ptr() if h is not None else None,
-            ws_ptr)
-    f = (_lib or load()).fp8_add_rmsnorm_quant
-    st = (f(*args, _stream_handle(index)) if _current_device() == index
-          else _kv_call(f, index, *args))
-    if st:
-        _check(st, "fp8_add_rmsnorm_quant")
-    return q, scale, total, h
+    m = _choice(NQ_MODES, mode, "mode")
+    if m == 0 and ws is None:
+        ws = _norm_workspace(_kv_device(x))
+    return (_calls or _load_calls()).add_rmsnorm_quant(x, residual, gamma, eps, m, total, q, scale,
+                                                       h, want_h, ws)

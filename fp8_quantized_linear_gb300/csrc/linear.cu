@@ -124,7 +124,10 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     return launch_linear_swapped(c, 1, a_scale);
 }
 
-extern "C" size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t K) {
+extern "C" size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t N, int64_t K,
+                                                   unsigned flags) {
+    (void)N;
+    (void)flags;
     if ((x_dtype != FP8L_F16 && x_dtype != FP8L_BF16) || M <= 0 || M > 0x7FFFFFFF || K <= 0 ||
         K > (1 << 20) || K % 16 != 0)
         return 0;

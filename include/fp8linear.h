@@ -349,12 +349,13 @@ FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N
  * up rows alike) and w_scale as for fp8_w8a16_mm; the other arguments and
  * the rules on y as for fp8_linear.  Without bias, activation and residual
  * the call is fp8_w8a16_mm.  workspace:
- * fp8_w8a16_linear_workspace_bytes(x_dtype, M, K) bytes (16-byte aligned,
- * any contents, sharing memory with no other argument), written by the call
+ * fp8_w8a16_linear_workspace_bytes() bytes for these arguments (16-byte
+ * aligned, any contents; may be NULL when that is 0), sharing memory with no other argument), written by the call
  * and free for other use when it has run; calls that may overlap need one
  * each.  flags: any of FP8L_WEIGHTS_STABLE and FP8L_WEIGHTS_PACKED.  A
  * time-out of a device-side wait is recorded as for fp8_w8a16_mm. */
-FP8L_API size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t K);
+FP8L_API size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t N, int64_t K,
+                                                 unsigned flags);
 FP8L_API int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, const float *w_scale,
                               int64_t M, int64_t N, int64_t K, const void *bias, int bias_dtype,
                               int activation, const void *residual, void *y, void *workspace,
