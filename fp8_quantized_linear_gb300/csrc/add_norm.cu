@@ -14,20 +14,24 @@
 // 7 bytes an element cross HBM (two 16-bit reads, one 16-bit write, one
 // code), so the kernels are streams.  A row lives in the registers of its
 // threads from the loads to the stores; nothing is staged in shared memory
-// and nothing is read twice.  Enough rows are in flight on an SM (2048
-// threads of 2 to 8 pending 16-byte loads each) to cover HBM's latency
-// without a copy pipeline.
-//   add_norm_rows      static, per token, norm only: one row per block (a
-//                      warp per row up to 1024 columns, where a block's
-//                      barriers would cost more than the row).
-//   add_norm_dynamic   one scale for the tensor: blocks persist over their
-//                      rows, meet at a grid maximum (cooperative launch, the
-//                      workspace's barrier words), then cast.  Rows whose h
-//                      fits shared memory are kept there; the others are
-//                      read again from the stream just written, newest
-//                      first, and normalized with the same operations.
-#include <atomic>
-
+// and nothing is read twice.  Enough rows are in flight on an SM (threads of
+// 2 to 8 pending 16-byte loads each) to cover HBM's latency without a copy
+// pipeline.
+//   add_norm_rows  one row per block (a warp per row up to 1024 columns, where
+//                  a block's barriers would cost more than the row).
+//   add_norm_max, add_norm_cast
+//                  one scale for the whole tensor: the first leaves the
+//                  tensor's maximum in the workspace and a row's factor r in
+//                  the row of q that its codes will fill; the second, a
+//                  programmatic dependent, casts h, or makes it again from the
+//                  stream just written, the newest rows (still in L2) first.
+// Measured (GB300, replayed graphs, of the copy bandwidth): 16384 x 8192
+// static or per token 138.5 us, 0.997; 1021 x 8192 per token 10.3 us, 0.84; 16
+// x 4096 per token 1.9 us (launch and one round trip).  Dynamic: 16384 x 8192
+// 188 us (177 for 7 bytes an element and the stream read again), 1021 x 8192
+// with h 16.4 us for 11.1 of traffic, 16 x 4096 4.0 us.  One cooperative kernel
+// with a grid barrier between the halves and h held in shared memory took 221,
+// 17.2 and 4.1 us, and had a wait in it.
 #include "quant_device.cuh"
 #include "skinny_device.cuh"
 
@@ -35,8 +39,19 @@ namespace fp8l {
 namespace {
 
 constexpr int kAddMaxK = 32768;
-constexpr int kAddSmemBudget = 200 * 1024;  // of held rows, per SM
-constexpr int kAddMaxDevices = 64;
+// Workspace words of the dynamic mode: a call counter, the half of the pair of
+// magnitude maxima that the call uses (counter mod 2), and that pair, whose
+// unused half is zero between calls.  add_norm_max reads the counter and names
+// the half; add_norm_cast clears the other half and advances the counter: no
+// word is written in a kernel that other blocks of it still read.  (Counting
+// the blocks that had read the maximum instead, one atomic each, took 4096 x
+// 4096 from 25 to 40 us.)
+constexpr size_t kAddWordsOffset = 32;
+struct AddNormWords {
+    unsigned counter, half, amax[2];
+};
+static_assert(kAddWordsOffset >= kBarrierAreaBytes && kAddWordsOffset + sizeof(AddNormWords) <= kPartialsOffset,
+              "words of their own in the workspace");
 
 struct AddNormArgs {
     const void *x, *res, *gamma;
@@ -47,11 +62,14 @@ struct AddNormArgs {
     float *scale;
     void *h;
     int mode;
-    unsigned *epoch, *arrive, *amax, *status, *lib_status;
-    int slots;  // dynamic: rows a block holds in shared memory
-    long long wait_cycles;
-    unsigned stall;
+    AddNormWords *words;  // dynamic
 };
+
+__device__ __forceinline__ uint32_t ld_relaxed(const unsigned *p) {
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // streamed 16 bytes that this kernel reads once (the preceding kernel may
 // have written them: coherent)
@@ -155,275 +173,232 @@ __device__ __forceinline__ float pair_sum(uint64_t acc) {
                      __uint_as_float(static_cast<uint32_t>(acc >> 32)));
 }
 
-// WARPS warps a row, ROWS rows a block (WARPS == 1, or ROWS == 1), NW words
-// (of 8 elements) a thread.
-template <int DT, int WARPS, int ROWS, int NW>
-__global__ void __launch_bounds__(32 * WARPS * ROWS) add_norm_rows(const AddNormArgs a) {
+// What a row's threads do, WARPS warps a row, NW words (of 8 elements) a
+// thread, words tid, tid + 32 WARPS, ...  Loads go in batches of kBatch words
+// of x and res.
+template <int DT, int WARPS, int NW>
+struct Row {
+    static constexpr int kSpan = 32 * WARPS;
+    static constexpr int kBatch = NW > 4 ? 2 : NW;
+
+    // the sum x + res, stored as the new stream; words beyond the row are zeros
+    __device__ __forceinline__ static void add(const AddNormArgs &a, size_t at, int tid, int words,
+                                               uint4 (&t)[NW]) {
+#pragma unroll
+        for (int j0 = 0; j0 < NW; j0 += kBatch) {
+            uint4 x[kBatch], r[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int w = tid + (j0 + j) * kSpan;
+                x[j] = r[j] = make_uint4(0, 0, 0, 0);
+                if (w < words) {
+                    x[j] = ld_once16(static_cast<const uint4 *>(a.x) + at + w);
+                    r[j] = ld_once16(static_cast<const uint4 *>(a.res) + at + w);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int w = tid + (j0 + j) * kSpan;
+                t[j0 + j] = add_word<DT>(x[j], r[j]);
+                if (w < words) static_cast<uint4 *>(a.total)[at + w] = t[j0 + j];
+            }
+        }
+    }
+
+    // its float pair of squares' sums
+    __device__ __forceinline__ static float squares(const uint4 (&t)[NW]) {
+        uint64_t acc = 0;
+#pragma unroll
+        for (int j = 0; j < NW; ++j) acc = add_squares<DT>(t[j], acc);
+        return pair_sum(acc);
+    }
+
+    // h in place of t
+    __device__ __forceinline__ static void scale(const AddNormArgs &a, int tid, int words, uint64_t r2,
+                                                 uint4 (&t)[NW]) {
+#pragma unroll
+        for (int j0 = 0; j0 < NW; j0 += kBatch) {
+            uint4 g[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int w = tid + (j0 + j) * kSpan;
+                g[j] = w < words ? ld_act16(static_cast<const uint4 *>(a.gamma) + w) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) t[j0 + j] = scaled_word<DT>(t[j0 + j], g[j], r2);
+        }
+    }
+
+    __device__ __forceinline__ static uint32_t magnitude(const uint4 (&t)[NW], uint32_t m) {
+#pragma unroll
+        for (int j = 0; j < NW; ++j) m = word_mag_max<DT>(t[j], m);
+        return m;
+    }
+
+    __device__ __forceinline__ static void store_h(const AddNormArgs &a, size_t at, int tid, int words,
+                                                   const uint4 (&t)[NW]) {
+        if (a.h == nullptr) return;
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            const int w = tid + j * kSpan;
+            if (w < words) static_cast<uint4 *>(a.h)[at + w] = t[j];
+        }
+    }
+
+    template <bool CLAMP>
+    __device__ __forceinline__ static void store_codes(const AddNormArgs &a, size_t at, int tid, int words,
+                                                       const uint4 (&t)[NW], const Quot &d) {
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            const int w = tid + j * kSpan;
+            if (w < words) reinterpret_cast<uint2 *>(a.q)[at + w] = codes_of_word<DT, CLAMP>(t[j], d);
+        }
+    }
+};
+
+// ROWS rows a block (a warp each), or one row (WARPS warps).
+template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
+__global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_rows(const AddNormArgs a) {
     static_assert(WARPS == 1 || ROWS == 1, "a block is one row, or a warp is");
+    using R = Row<DT, WARPS, NW>;
     __shared__ float fpart[WARPS];
     __shared__ uint32_t upart[WARPS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kSpan = 32 * WARPS;  // threads of a row
     const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + (WARPS == 1 ? threadIdx.x >> 5 : 0);
     pdl_wait();
     if (row >= a.M) return;  // a whole warp (ROWS > 1) or no thread
     const int words = a.K / 8;
-    const uint4 *x = static_cast<const uint4 *>(a.x) + row * words;
-    const uint4 *res = static_cast<const uint4 *>(a.res) + row * words;
-    uint4 t[NW], g[NW];
-    {
-        uint4 xv[NW], rv[NW];
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            xv[j] = rv[j] = g[j] = make_uint4(0, 0, 0, 0);
-            if (w < words) {
-                xv[j] = ld_once16(x + w);
-                rv[j] = ld_once16(res + w);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            if (w < words) g[j] = ld_act16(static_cast<const uint4 *>(a.gamma) + w);
-        }
-        uint64_t acc = 0;
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            t[j] = add_word<DT>(xv[j], rv[j]);
-            acc = add_squares<DT>(t[j], acc);
-        }
-        // (the stream's stores before the barrier: they drain while it waits)
-        uint4 *total = static_cast<uint4 *>(a.total) + row * words;
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            if (w < words) total[w] = t[j];
-        }
-        const uint64_t r2 = rms_factor(row_sum<WARPS>(pair_sum(acc), fpart), a.K, a.eps);
-#pragma unroll
-        for (int j = 0; j < NW; ++j) t[j] = scaled_word<DT>(t[j], g[j], r2);
-    }
-    if (a.h != nullptr) {
-        uint4 *h = static_cast<uint4 *>(a.h) + row * words;
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            if (w < words) h[w] = t[j];
-        }
-    }
+    const size_t at = static_cast<size_t>(row) * words;
+    uint4 t[NW];
+    R::add(a, at, tid, words, t);
+    const uint64_t r2 = rms_factor(row_sum<WARPS>(R::squares(t), fpart), a.K, a.eps);
+    R::scale(a, tid, words, r2, t);
+    R::store_h(a, at, tid, words, t);
     if (a.mode == FP8L_NQ_NORM_ONLY) return;
-    float s;
     if (a.mode == FP8L_NQ_PER_TOKEN) {
-        uint32_t m = 0;  // words beyond the row are zeros
-#pragma unroll
-        for (int j = 0; j < NW; ++j) m = word_mag_max<DT>(t[j], m);
-        s = scale_from_amax(mag_bits_to_float<DT>(row_max<WARPS>(fold_mag<DT>(m), upart)));
+        const uint32_t m = fold_mag<DT>(R::magnitude(t, 0));
+        const float s = scale_from_amax(mag_bits_to_float<DT>(row_max<WARPS>(m, upart)));
         if (tid == 0) a.scale[row] = s;
+        R::template store_codes<false>(a, at, tid, words, t, Quot::make<DT>(s));
     } else {
-        s = ld_act_f32(a.scale);
-    }
-    const Quot d = Quot::make<DT>(s);
-    uint2 *q = reinterpret_cast<uint2 *>(a.q) + row * words;
-    if (a.mode == FP8L_NQ_STATIC) {
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            if (w < words) q[w] = codes_of_word<DT, true>(t[j], d);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            if (w < words) q[w] = codes_of_word<DT, false>(t[j], d);
-        }
+        R::template store_codes<true>(a, at, tid, words, t, Quot::make<DT>(ld_act_f32(a.scale)));
     }
 }
 
-template <int DT, int WARPS, int NW>
-__global__ void __launch_bounds__(32 * WARPS) add_norm_dynamic(const AddNormArgs a) {
-    extern __shared__ __align__(16) uint4 held[];  // [slots][words], h of a block's first rows
+// The dynamic mode's first half: the stream, h when it is wanted, the factors
+// and the maximum.  As many blocks as fit at once go through the rows, so that
+// few of them touch the workspace's words (one block a row, 4096 of them, took
+// longer to read those words than to do the rest).
+template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
+__global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_max(const AddNormArgs a) {
+    using R = Row<DT, WARPS, NW>;
     __shared__ float fpart[2][WARPS];
     __shared__ uint32_t red[33];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kSpan = 32 * WARPS;
-    const int tid = threadIdx.x, words = a.K / 8;
-    const int64_t G = gridDim.x, b = blockIdx.x;
-    const unsigned epoch = *reinterpret_cast<volatile unsigned *>(a.epoch), pair = epoch & 1u;
-    if (b == 0 && tid == 0) {
-        a.arrive[pair ^ 1u] = 0u;
-        a.amax[pair ^ 1u] = 0u;
-    }
-    uint4 g[NW];
-#pragma unroll
-    for (int j = 0; j < NW; ++j) {
-        const int w = tid + j * kSpan;
-        g[j] = w < words ? ld_act16(static_cast<const uint4 *>(a.gamma) + w) : make_uint4(0, 0, 0, 0);
-    }
-    int flip = 0;
-    // h of a row of the stream, in place of t; the partials alternate between
-    // two arrays, so one barrier a row is enough
-    auto normalize = [&](uint4(&t)[NW]) {
-        uint64_t acc = 0;
-#pragma unroll
-        for (int j = 0; j < NW; ++j) acc = add_squares<DT>(t[j], acc);
-        const uint64_t r2 = rms_factor(row_sum<WARPS>(pair_sum(acc), fpart[flip]), a.K, a.eps);
-        flip ^= 1;
-#pragma unroll
-        for (int j = 0; j < NW; ++j) t[j] = scaled_word<DT>(t[j], g[j], r2);
-    };
+    const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x, words = a.K / 8;
+    pdl_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + (WARPS == 1 ? threadIdx.x >> 5 : 0);
     uint32_t m = 0;
-    int i = 0;
-    for (int64_t row = b; row < a.M; row += G, ++i) {
+    int flip = 0;  // the partials alternate between two arrays: one barrier a row is enough
+    for (int64_t row = first; row < a.M; row += static_cast<int64_t>(gridDim.x) * ROWS) {
         const size_t at = static_cast<size_t>(row) * words;
-        uint4 xv[NW], t[NW];
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            xv[j] = t[j] = make_uint4(0, 0, 0, 0);
-            if (w < words) {
-                xv[j] = ld_once16(static_cast<const uint4 *>(a.x) + at + w);
-                t[j] = ld_once16(static_cast<const uint4 *>(a.res) + at + w);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            t[j] = add_word<DT>(xv[j], t[j]);
-            if (w < words) static_cast<uint4 *>(a.total)[at + w] = t[j];
-        }
-        normalize(t);
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            m = word_mag_max<DT>(t[j], m);
-            if (w >= words) continue;
-            if (a.h != nullptr) static_cast<uint4 *>(a.h)[at + w] = t[j];
-            // (each thread reads back only its own words)
-            if (i < a.slots) held[static_cast<size_t>(i) * words + w] = t[j];
-        }
+        uint4 t[NW];
+        R::add(a, at, tid, words, t);
+        const uint64_t r2 = rms_factor(row_sum<WARPS>(R::squares(t), fpart[flip]), a.K, a.eps);
+        flip ^= 1;
+        R::scale(a, tid, words, r2, t);
+        m = R::magnitude(t, m);
+        if (a.h != nullptr)
+            R::store_h(a, at, tid, words, t);
+        else if (tid == 0)
+            *reinterpret_cast<uint32_t *>(a.q + at * 8) = static_cast<uint32_t>(r2);
     }
-    const uint32_t bm = block_max_u32(fold_mag<DT>(m), red);
-    const unsigned stalled = (a.stall & kStallGrid) != 0u ? 1u : 0u;
-    const bool barrier = G > 1 || stalled != 0u;  // a single block has the maximum already
-    uint32_t mm = bm;
-    if (barrier && !grid_max(a.arrive + pair, a.amax + pair, bm, a.status, &mm,
-                             static_cast<unsigned>(G) + stalled, a.wait_cycles)) {
-        // (a capture's workspace is read by nobody: the library's word too)
-        if (tid == 0) flag_timeout(a.lib_status);
-        return;
+    m = block_max_u32(fold_mag<DT>(m), red);
+    if (threadIdx.x == 0) {
+        const unsigned half = ld_relaxed(&a.words->counter) & 1u;
+        if (blockIdx.x == 0) a.words->half = half;
+        atomicMax(&a.words->amax[half], m);
     }
-    const float s = scale_from_amax(mag_bits_to_float<DT>(mm));
-    if (b == 0 && tid == 0) {
+}
+
+// Its second half: the scale from the maximum, and the codes.
+template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
+__global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_cast(const AddNormArgs a) {
+    using R = Row<DT, WARPS, NW>;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x, words = a.K / 8;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + (WARPS == 1 ? threadIdx.x >> 5 : 0);
+    pdl_wait();
+    const unsigned half = ld_relaxed(&a.words->half);
+    const float s = scale_from_amax(mag_bits_to_float<DT>(ld_relaxed(&a.words->amax[half])));
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
         *a.scale = s;
-        if (barrier) *a.epoch = epoch + 1u;
+        a.words->amax[half ^ 1u] = 0u;
+        a.words->counter += 1u;
     }
     const Quot d = Quot::make<DT>(s);
-    for (int k = i - 1; k >= 0; --k) {
-        const size_t at = static_cast<size_t>(b + G * k) * words;
+    for (int64_t i = first; i < a.M; i += static_cast<int64_t>(gridDim.x) * ROWS) {
+        const size_t at = static_cast<size_t>(a.M - 1 - i) * words;
         uint4 t[NW];
-        if (k < a.slots) {
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                const int w = tid + j * kSpan;
-                t[j] = w < words ? held[static_cast<size_t>(k) * words + w] : make_uint4(0, 0, 0, 0);
-            }
-        } else {
-            // the stream this thread wrote
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                const int w = tid + j * kSpan;
-                t[j] = w < words ? ld_once16(static_cast<const uint4 *>(a.total) + at + w)
-                                 : make_uint4(0, 0, 0, 0);
-            }
-            normalize(t);
-        }
+        const uint4 *src = static_cast<const uint4 *>(a.h != nullptr ? a.h : a.total) + at;
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
-            const int w = tid + j * kSpan;
-            if (w < words) reinterpret_cast<uint2 *>(a.q)[at + w] = codes_of_word<DT, false>(t[j], d);
+            const int w = tid + j * R::kSpan;
+            t[j] = w < words ? ld_once16(src + w) : make_uint4(0, 0, 0, 0);
         }
+        if (a.h == nullptr) {
+            const uint32_t r = __float_as_uint(ld_act_f32(reinterpret_cast<const float *>(a.q + at * 8)));
+            // every thread has the row's factor before codes overwrite it
+            if constexpr (WARPS > 1)
+                __syncthreads();
+            else
+                __syncwarp();
+            R::scale(a, tid, words, f2_pack(r, r), t);
+        }
+        R::template store_codes<false>(a, at, tid, words, t, d);
     }
 }
 
 __global__ void add_norm_empty_scale(float *scale) { *scale = 1.0f; }
 
-template <int DT, int WARPS, int ROWS, int NW>
-int launch_rows(const AddNormArgs &a, cudaStream_t stream) {
+template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
+int launch_rows(const AddNormArgs &a, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((int64_t(a.M) + ROWS - 1) / ROWS), 1, 1);
     cfg.blockDim = dim3(32 * WARPS * ROWS, 1, 1);
     cfg.stream = stream;
-    if (cudaLaunchKernelEx(&cfg, add_norm_rows<DT, WARPS, ROWS, NW>, a) != cudaSuccess) return FP8L_ECUDA;
-    return launch_status();
-}
-
-// Every block of the grid is resident (cooperative launch): at most one per
-// row, and as many per SM as 2048 threads and the held rows allow.
-template <int DT, int WARPS, int NW>
-int launch_dynamic(AddNormArgs a, int sms, cudaStream_t stream) {
-    auto kernel = add_norm_dynamic<DT, WARPS, NW>;
-    static std::atomic<int> ready[kAddMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kAddMaxDevices) return FP8L_ECUDA;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAddSmemBudget) !=
-            cudaSuccess)
-            return FP8L_ECUDA;
-        ready[dev].store(1, std::memory_order_release);
-    }
-    const size_t row_bytes = static_cast<size_t>(a.K) * 2;
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * WARPS, 0) != cudaSuccess ||
-        per_sm < 1)
-        return FP8L_ECUDA;
-    // rows held: as many as every block's share of the budget takes, and no
-    // more than it has
-    const int64_t most = int64_t(per_sm) * sms;
-    int64_t grid = a.M < most ? a.M : most;
-    const int64_t rows = (a.M + grid - 1) / grid;
-    const int on_sm = static_cast<int>((grid + sms - 1) / sms);
-    int64_t slots = static_cast<int64_t>((kAddSmemBudget / on_sm) / row_bytes);
-    if (slots > rows) slots = rows;
-    int fit = 0;
-    while (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, 32 * WARPS, slots * row_bytes) ==
-               cudaSuccess &&
-           int64_t(fit) * sms < grid && slots > 0)
-        --slots;
-    if (int64_t(fit) * sms < grid) return FP8L_ECUDA;
-    a.slots = static_cast<int>(slots);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(32 * WARPS, 1, 1);
-    cfg.dynamicSmemBytes = slots * row_bytes;
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
+    // (the kernels wait for the preceding one before they touch memory)
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return FP8L_ECUDA;
+    if (a.mode == FP8L_NQ_DYNAMIC) {
+        if (cfg.gridDim.x > static_cast<unsigned>(sms * BLOCKS)) cfg.gridDim.x = sms * BLOCKS;
+        if (cudaLaunchKernelEx(&cfg, add_norm_max<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess ||
+            cudaLaunchKernelEx(&cfg, add_norm_cast<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess)
+            return FP8L_ECUDA;
+    } else if (cudaLaunchKernelEx(&cfg, add_norm_rows<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess) {
+        return FP8L_ECUDA;
+    }
     return launch_status();
 }
 
+// Threads and words a thread by the row's length: rows up to 1024 elements a
+// warp each (a block's barriers would cost more than the row), then the least
+// threads that hold a row in two to four words, with as many blocks an SM as
+// 64 to 80 registers a thread leave.
 template <int DT>
 int dispatch_add_norm(const AddNormArgs &a, int sms, cudaStream_t s) {
     const int words = a.K / 8;
-    if (a.mode == FP8L_NQ_DYNAMIC) {
-        if (words <= 128) return launch_dynamic<DT, 4, 1>(a, sms, s);
-        if (words <= 512) return launch_dynamic<DT, 8, 2>(a, sms, s);
-        if (words <= 1024) return launch_dynamic<DT, 8, 4>(a, sms, s);
-        if (words <= 2048) return launch_dynamic<DT, 16, 4>(a, sms, s);
-        return launch_dynamic<DT, 32, 4>(a, sms, s);
-    }
-    if (words <= 32) return launch_rows<DT, 1, 8, 1>(a, s);
-    if (words <= 128) return launch_rows<DT, 1, 8, 4>(a, s);
-    if (words <= 256) return launch_rows<DT, 4, 1, 2>(a, s);
-    if (words <= 512) return launch_rows<DT, 8, 1, 2>(a, s);
-    if (words <= 1024) return launch_rows<DT, 8, 1, 4>(a, s);
-    if (words <= 2048) return launch_rows<DT, 16, 1, 4>(a, s);
-    return launch_rows<DT, 32, 1, 4>(a, s);
+    if (words <= 32) return launch_rows<DT, 1, 8, 1, 6>(a, sms, s);
+    if (words <= 128) return launch_rows<DT, 1, 8, 4, 3>(a, sms, s);
+    if (words <= 256) return launch_rows<DT, 4, 1, 2, 8>(a, sms, s);
+    if (words <= 512) return launch_rows<DT, 8, 1, 2, 4>(a, sms, s);
+    if (words <= 1024) return launch_rows<DT, 8, 1, 4, 3>(a, sms, s);
+    if (words <= 2048) return launch_rows<DT, 16, 1, 4, 2>(a, sms, s);
+    return launch_rows<DT, 32, 1, 4, 1>(a, sms, s);
 }
 
 // Whether [p, p + n) and [q, q + m) share a byte (a null range shares none).
@@ -498,15 +473,8 @@ extern "C" int fp8_add_rmsnorm_quant(const void *x, const void *residual, int x_
     a.h = h;
     a.mode = mode;
     if (mode == FP8L_NQ_DYNAMIC) {
-        a.epoch = epoch_word(workspace);
-        a.arrive = arrive_words(workspace);
-        a.amax = amax_words(workspace);
-        a.status = status_word(workspace);
-        if (library_status_word(&a.lib_status) != FP8L_OK) return FP8L_ECUDA;
+        a.words = reinterpret_cast<AddNormWords *>(static_cast<char *>(workspace) + kAddWordsOffset);
     }
-    const WaitConfig wc = wait_config();
-    a.wait_cycles = wc.cycles;
-    a.stall = wc.stall;
     return x_dtype == FP8L_BF16 ? dispatch_add_norm<FP8L_BF16>(a, sms, s)
                                 : dispatch_add_norm<FP8L_F16>(a, sms, s);
 }

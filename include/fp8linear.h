@@ -462,8 +462,8 @@ FP8L_API int fp8_rmsnorm_quant(const void *x, int x_dtype, const void *gamma, fl
  * be x or residual itself (updated in place).  gamma, eps, q, scale, mode, h,
  * workspace, M and K as for fp8_rmsnorm_quant.  Apart from that, no output
  * shares memory with an input or another output (FP8L_EINVAL).  workspace is
- * used in FP8L_NQ_DYNAMIC only; a time-out of its grid barrier is recorded in
- * it and in the library's status word.  Deterministic. */
+ * used in FP8L_NQ_DYNAMIC only, by one call at a time (two words of it, zero
+ * between calls); nothing in the call waits.  Deterministic. */
 FP8L_API int fp8_add_rmsnorm_quant(const void *x, const void *residual, int x_dtype,
                                    const void *gamma, float eps, int64_t M, int64_t K, void *total,
                                    uint8_t *q, float *scale, int mode, void *h, void *workspace,
