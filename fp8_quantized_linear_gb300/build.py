@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libfp8linear.so")
 CALLS = os.path.join(PKG, "_calls.so")  # the linear layers' calls from Python
 
 SOURCES = ["api.cu", "quant.cu", "norm_quant.cu", "skinny.cu", "skinny_quant.cu", "gemm_tcgen05.cu",
-           "gemm_swapab.cu", "add_norm.cu", "linear.cu", "linear_swapped.cu", "linear_pair.cu",
+           "gemm_swapab.cu", "add_norm.cu", "linear.cu", "linear_swapped.cu", "linear_pair.cu", "linear_stream.cu",
            "kv_plan.cu", "kv_append.cu", "kv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-Xcompiler", "-fvisibility=hidden",

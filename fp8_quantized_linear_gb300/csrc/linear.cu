@@ -65,12 +65,24 @@ int check_output(const Epilogue &e, int64_t M, int64_t N, const void *x, size_t 
     return FP8L_OK;
 }
 
-// The kernel of fp8_linear: tiles over SM pairs when there are enough tokens
-// for them, else the swapped-operand kernel.
+// The kernel of fp8_linear: weights streamed for a few tokens and small
+// weights, tiles over SM pairs for many tokens, the swapped-operand kernel
+// between.
 unsigned choose_linear(int64_t M, int64_t N, int64_t K) {
+    const int64_t wbytes = N * K;
+    if ((M <= 4 && wbytes <= (int64_t(24) << 20)) || (M <= 16 && wbytes <= (int64_t(16) << 20)))
+        return FP8L_KERNEL_STREAM;
+    return M > 256 ? FP8L_KERNEL_TILED : FP8L_KERNEL_SWAPPED;
+}
+
+// The kernel of fp8_w8a16_linear: weights streamed through registers for a few
+// tokens, else tokens in parts through the swapped-operand kernel.
+unsigned choose_w8a16_linear(int64_t M, int64_t N, int64_t K, unsigned flags) {
     (void)N;
     (void)K;
-    return M > 256 ? FP8L_KERNEL_TILED : FP8L_KERNEL_SWAPPED;
+    const unsigned k = flags & FP8L_KERNEL_MASK;
+    if (k != FP8L_KERNEL_AUTO) return k;
+    return M <= 8 ? FP8L_KERNEL_STREAM : FP8L_KERNEL_SWAPPED;
 }
 
 }  // namespace
@@ -120,14 +132,14 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     c.stream = as_stream(stream);
     unsigned kernel = flags & FP8L_KERNEL_MASK;
     if (kernel == FP8L_KERNEL_AUTO) kernel = choose_linear(M, N, K);
+    if (kernel == FP8L_KERNEL_STREAM) return launch_linear_stream(c);
     if (kernel == FP8L_KERNEL_TILED) return launch_linear_pair(c);
     return launch_linear_swapped(c, 1, a_scale);
 }
 
 extern "C" size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t N, int64_t K,
                                                    unsigned flags) {
-    (void)N;
-    (void)flags;
+    if (fp8l::choose_w8a16_linear(M, N, K, flags) != FP8L_KERNEL_SWAPPED) return 0;
     if ((x_dtype != FP8L_F16 && x_dtype != FP8L_BF16) || M <= 0 || M > 0x7FFFFFFF || K <= 0 ||
         K > (1 << 20) || K % 16 != 0)
         return 0;
@@ -140,7 +152,10 @@ extern "C" int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, co
                                 unsigned flags, void *stream) {
     using namespace fp8l;
     if (x_dtype != FP8L_F16 && x_dtype != FP8L_BF16) return FP8L_EINVAL;
-    if ((flags & ~(FP8L_WEIGHTS_STABLE | FP8L_WEIGHTS_PACKED)) != 0u) return FP8L_EINVAL;
+    if ((flags & ~(FP8L_WEIGHTS_STABLE | FP8L_WEIGHTS_PACKED | FP8L_KERNEL_MASK)) != 0u)
+        return FP8L_EINVAL;
+    const unsigned kernel = choose_w8a16_linear(M, N, K, flags);
+    if (kernel == FP8L_KERNEL_TILED) return FP8L_EINVAL;
     if (w == nullptr || w_scale == nullptr) return FP8L_EINVAL;
     LinearCall c{};
     int st = check_epilogue(M, N, K, bias, bias_dtype, activation, residual, nullptr, y, x_dtype, &c.e,
@@ -155,7 +170,8 @@ extern "C" int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, co
     if (st != FP8L_OK) return st;
     if (bias == nullptr && activation == FP8L_ACT_NONE && residual == nullptr)
         return fp8_w8a16_mm(x, x_dtype, w, w_scale, M, N, K, y, flags, stream);
-    if (M > 0 && workspace == nullptr) return FP8L_EINVAL;
+    const size_t scratch = M > 0 ? fp8_w8a16_linear_workspace_bytes(x_dtype, M, N, K, flags) : 0;
+    if (scratch > 0 && workspace == nullptr) return FP8L_EINVAL;
     if (!aligned16(workspace)) return FP8L_EALIGN;
     st = check_device(&c.sms);
     if (st != FP8L_OK) return st;
@@ -170,6 +186,7 @@ extern "C" int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, co
     c.w_per_channel = 1;
     c.stable = (flags & FP8L_WEIGHTS_STABLE) != 0u;
     c.stream = as_stream(stream);
+    if (kernel == FP8L_KERNEL_STREAM) return launch_linear_stream(c);
     if (library_status_word(&c.status) != FP8L_OK) return FP8L_ECUDA;
     const float *token_scale = nullptr;
     st = linear_split_tokens(c, workspace, &token_scale);

@@ -33,6 +33,9 @@ int make_swizzle64_map(CUtensorMap *map, const void *ptr, int rank, const uint64
 // parts: E4M3 numbers a token value is held in (1: the codes themselves).
 int launch_linear_swapped(const LinearCall &c, int parts, const float *token_scale);
 
+// Weights streamed through registers, up to 16 tokens a CTA (any tokens).
+int launch_linear_stream(const LinearCall &c);
+
 // 256-token by 256-row tiles over pairs of SMs (E4M3 tokens, row-major weights).
 int launch_linear_pair(const LinearCall &c);
 

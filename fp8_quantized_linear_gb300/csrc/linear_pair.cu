@@ -35,8 +35,13 @@
 //              28672 x 4096 with a residual 88.9 us, with boxes 84.6).
 // Tail tiles: 256-wide tiles fill whole rounds of the SM pairs; the columns
 // left over become narrower tiles when that ends the last round sooner.
-// Waits are bounded; a time-out raises both CTAs' abort flags, and both meet
-// at a cluster barrier before TMEM is released.
+// Few tiles: a cluster of two or four pairs shares a tile and splits its
+// k-blocks.  Each pair keeps a share of the tile's columns and sends the float
+// sums of the others to their pairs' (by then idle) stages through distributed
+// shared memory; the owner adds them in pair order, so results are the same
+// bits every time (512 x 4096 x 14336: 41.0 us without, SPL us).
+// Waits are bounded; a time-out raises both CTAs' abort flags, and all CTAs of
+// a cluster meet at its barrier before TMEM is released.
 #include <atomic>
 
 #include "linear_launch.cuh"
@@ -68,6 +73,7 @@ constexpr uint32_t kLpTmemCols = 2 * LP_BN;
 
 struct PairArgs {
     int M, num_k_blocks;
+    int split;  // pairs of a cluster sharing a tile (1: none)
     int tiles_m, main_tiles, n_main, tail_w, tail_n;  // n_main: output columns of the main tiles
     int prefetch;
     const float *a_scale;
@@ -105,13 +111,13 @@ __device__ __forceinline__ void lp_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
         : "memory");
 }
 
-// arrive on the barrier at this offset in both CTAs once the MMAs issued so
-// far have retired
-__device__ __forceinline__ void lp_commit(uint32_t bar) {
+// arrive on the barrier at this offset in both CTAs (a mask of cluster ranks)
+// once the MMAs issued so far have retired
+__device__ __forceinline__ void lp_commit(uint32_t bar, uint32_t ctas) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(ctas))
         : "memory");
 }
 
@@ -161,6 +167,11 @@ __device__ __forceinline__ uint32_t lp_box_piece(uint32_t box, int row, int j) {
     return box + static_cast<uint32_t>(row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
 }
 
+__device__ __forceinline__ void lp_st_cluster(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint4 lp_ld_shared(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -187,7 +198,22 @@ __device__ __forceinline__ void lp_scaled(const uint32_t (&r)[32], const float *
     }
 }
 
-template <bool GATED>
+// The sums of a chunk (32 accumulator columns) that other pairs sent, added to
+// this pair's: 16-byte pieces [source][chunk][piece][row] from `part`.
+__device__ __forceinline__ void lp_add_parts(uint32_t (&r)[32], uint32_t part, int sources, uint32_t source_bytes) {
+    for (int q = 0; q < sources; ++q, part += source_bytes) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 w = lp_ld_shared(part + static_cast<uint32_t>(j * LP_BM * 16));
+            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + __uint_as_float(w.x));
+            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + __uint_as_float(w.y));
+            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + __uint_as_float(w.z));
+            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + __uint_as_float(w.w));
+        }
+    }
+}
+
+template <bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kLpThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                    const __grid_constant__ CUtensorMap tmap_b,
@@ -212,7 +238,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t crank = cluster_rank();
+    const uint32_t rank = crank & 1u;   // in the pair
+    const uint32_t even = crank & ~1u;  // the pair's even CTA
+    const uint32_t both = 3u << even;
     const bool leader = rank == 0;
 
     if (threadIdx.x == 0) {
@@ -242,11 +271,20 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     cluster_sync_all();  // both CTAs' barriers exist before either touches the other's
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1u);
+    const uint32_t peer_abort = map_to_rank(smem_u32(const_cast<int *>(abort_flag)), crank ^ 1u);
 
-    const int pair = static_cast<int>(blockIdx.x) >> 1;
-    const int num_pairs = static_cast<int>(gridDim.x) >> 1;
     const int num_tiles = p.main_tiles + p.tiles_m * p.tail_n;
+    // pairs go round the tiles; or a cluster's one tile, and this pair's share
+    // of its k-blocks
+    const int pair = SPLIT ? static_cast<int>(blockIdx.x) / (2 * p.split) : static_cast<int>(blockIdx.x) >> 1;
+    const int num_pairs = SPLIT ? num_tiles : static_cast<int>(gridDim.x) >> 1;
+    const int kpart = SPLIT ? static_cast<int>(crank >> 1) : 0;
+    int kb0 = 0, nkb = p.num_k_blocks;
+    if constexpr (SPLIT) {
+        const int share = p.num_k_blocks / p.split, rem = p.num_k_blocks % p.split;
+        kb0 = kpart * share + (kpart < rem ? kpart : rem);
+        nkb = share + (kpart < rem ? 1 : 0);
+    }
 
     if (warp == 0) {
         if (lane == 0) {
@@ -255,7 +293,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if (p.tail_n > 0)
                 asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_bt)) : "memory");
             uint32_t armed = 0, armed_parity = 0;  // even CTA: stages armed, their parity
-            const uint32_t full0 = map_to_rank(full_bar(0), 0);  // the even CTA's full barriers
+            const uint32_t full0 = map_to_rank(full_bar(0), even);  // the even CTA's full barriers
             const int a_row = static_cast<int>(rank) * LP_BM;
             // stable weights: the first tile's first stages before the wait
             int pre = 0;
@@ -263,13 +301,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 const LpTile t = lp_tile<GATED>(p, pair);
                 const CUtensorMap *map = t.w != LP_BN ? &tmap_bt : &tmap_b;
                 const int w_row = t.n0 + static_cast<int>(rank) * (GATED ? p.e.width : t.w / 2);
-                pre = p.num_k_blocks < LP_STAGES ? p.num_k_blocks : LP_STAGES;
+                pre = nkb < LP_STAGES ? nkb : LP_STAGES;
                 for (int s = 0; s < pre; ++s) {
                     if (leader) {
                         mbar_expect_tx(full_bar(s), 2 * (kLpABytes + static_cast<uint32_t>(t.w / 2) * LP_BK));
                         armed |= 1u << s;
                     }
-                    lp_tma(sbase + s * kLpStageBytes + kLpABytes, map, s * LP_BK, w_row, full0 + 8u * s);
+                    lp_tma(sbase + s * kLpStageBytes + kLpABytes, map, (kb0 + s) * LP_BK, w_row, full0 + 8u * s);
                 }
             }
             pdl_wait();
@@ -285,13 +323,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 const int w_row = t.n0 + static_cast<int>(rank) * (GATED ? p.e.width : t.w / 2);
                 int kb = 0;
                 for (; kb < pre; ++kb)  // armed, the weights on their way
-                    lp_tma(sbase + kb * kLpStageBytes, &tmap_a, kb * LP_BK, x_row, full0 + 8u * kb);
+                    lp_tma(sbase + kb * kLpStageBytes, &tmap_a, (kb0 + kb) * LP_BK, x_row, full0 + 8u * kb);
                 if (kb > 0) {
                     stage = kb == LP_STAGES ? 0 : kb;
                     phase = kb == LP_STAGES ? 1u : 0u;
                     pre = 0;
                 }
-                for (; kb < p.num_k_blocks; ++kb) {
+                for (; kb < nkb; ++kb) {
                     if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.wait_cycles,
                                    peer_abort)) {
                         ok = false;
@@ -304,8 +342,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         armed |= 1u << stage;
                         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                     }
-                    lp_tma(sa, &tmap_a, kb * LP_BK, x_row, fb);
-                    lp_tma(sa + kLpABytes, map, kb * LP_BK, w_row, fb);
+                    lp_tma(sa, &tmap_a, (kb0 + kb) * LP_BK, x_row, fb);
+                    lp_tma(sa + kLpABytes, map, (kb0 + kb) * LP_BK, w_row, fb);
                     if (++stage == LP_STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -318,6 +356,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 if (armed & (1u << s)) mbar_wait_drain(full_bar(s), (armed_parity >> s) & 1u, p.status);
         }
         __syncwarp();
+        if constexpr (SPLIT) {
+            cluster_sync_all();  // every pair's MMAs are through: stages may be written
+            cluster_sync_all();  // the sums are with their owners
+        }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             int stage = 0;
@@ -334,7 +376,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 tc_fence_after();
                 const uint32_t idesc = lp_idesc(tile < p.main_tiles ? LP_BN : p.tail_w);
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * LP_BN);
-                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+                for (int kb = 0; kb < nkb; ++kb) {
                     if (!mbar_wait_fast(full_bar(stage), phase, abort_flag, p.status, p.wait_cycles,
                                         peer_abort)) {
                         ok = false;
@@ -346,22 +388,26 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         lp_mma(d_tmem, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0 ? 1u : 0u);
-                    lp_commit(empty_bar(stage));
+                    lp_commit(empty_bar(stage), both);
                     if (++stage == LP_STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                lp_commit(tfull_bar(acc));
+                lp_commit(tfull_bar(acc), both);
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
             // every MMA issued has retired
-            lp_commit(done_bar);
+            lp_commit(done_bar, both);
             mbar_wait_drain(done_bar, 0, p.status);
         }
         __syncwarp();
+        if constexpr (SPLIT) {
+            cluster_sync_all();
+            cluster_sync_all();
+        }
     } else {
         pdl_wait();
         const int quarter = warp & 3;     // the TMEM lanes this warp may read
@@ -400,7 +446,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             }
             const float sa = p.a_per_token ? (row_ok ? epi_ld_f32(p.a_scale + m) : 0.0f) : sa0;
             const int chunks = GATED ? half / 32 : t.w / 32;
-            const int c_begin = grp * chunks / 2, c_end = (grp + 1) * chunks / 2;
+            // this pair's share of the chunks, this warp's half of it
+            const int own0 = SPLIT ? chunks * kpart / p.split : 0;
+            const int own = SPLIT ? chunks * (kpart + 1) / p.split - own0 : chunks;
+            const int c_begin = own0 + grp * own / 2, c_end = own0 + (grp + 1) * own / 2;
             // (a box partly outside the matrix is cut by TMA; one wholly outside is left out)
             const int box_row = t.mt * 2 * LP_BM + static_cast<int>(rank) * LP_BM + quarter * 32;
             auto box_in = [&](int c) { return box_row < p.M && t.n0 + c * 32 < p.e.width; };
@@ -418,10 +467,41 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if (ok)
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status,
                                                        p.wait_cycles, peer_abort));
-            if (!ok) continue;  // the others still meet at the barrier above
-            tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                    static_cast<uint32_t>(acc * LP_BN);
+            // split: bytes of the sums one pair sends another, of a chunk's, and
+            // where this row's pieces of the ones received begin
+            const uint32_t chunk_bytes = 32 * 4 * LP_BM;
+            const uint32_t part_bytes = SPLIT ? chunk_bytes * static_cast<uint32_t>((GATED ? 2 : 1) * own) : 0u;
+            const uint32_t part0 = sbase + static_cast<uint32_t>((quarter * 32 + lane) * 16);
+            if constexpr (SPLIT) {
+                tc_fence_after();
+                cluster_sync_all();  // every pair's MMAs are through: stages may be written
+                for (int q = 1; ok && q < p.split; ++q) {
+                    // another pair's chunks, into slot q - 1 .. of that pair: the
+                    // sources of an owner in ring order, the same in every run
+                    const int to = (kpart + q) % p.split;
+                    const int o0 = chunks * to / p.split, o1 = chunks * (to + 1) / p.split;
+                    const uint32_t slot = static_cast<uint32_t>(p.split - 1 - q);
+                    const uint32_t bytes = chunk_bytes * static_cast<uint32_t>((GATED ? 2 : 1) * (o1 - o0));
+                    const uint32_t dst = map_to_rank(part0, 2u * static_cast<uint32_t>(to) + rank) + slot * bytes;
+                    const int n = (GATED ? 2 : 1) * (o1 - o0);
+                    for (int i = grp; i < n; i += 2) {
+                        // gated: the gate's chunks, then the up's
+                        const int col = GATED && i >= o1 - o0 ? half + (o0 + i - (o1 - o0)) * 32 : (o0 + i) * 32;
+                        uint32_t r[32];
+                        tmem_ld32(taddr + static_cast<uint32_t>(col), r);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            lp_st_cluster(dst + static_cast<uint32_t>(i) * chunk_bytes +
+                                              static_cast<uint32_t>(j * LP_BM * 16),
+                                          r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    }
+                }
+                cluster_sync_all();  // the sums are with their owners
+            }
+            if (!ok) continue;  // the others still meet at the barriers above
+            tc_fence_after();
 #pragma unroll 1
             for (int c = c_begin; c < c_end; ++c) {
                 const int n0 = t.n0 + c * 32;
@@ -429,6 +509,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 {
                     uint32_t r[32];
                     tmem_ld32(taddr + static_cast<uint32_t>(c * 32), r);
+                    if constexpr (SPLIT)
+                        lp_add_parts(r, part0 + static_cast<uint32_t>(c - own0) * chunk_bytes, p.split - 1, part_bytes);
                     lp_scaled(r, cols + c * 32, sa, bias, v);
                 }
                 activate(v, p.e.act);
@@ -436,6 +518,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     uint32_t r[32];
                     float u[32];
                     tmem_ld32(taddr + static_cast<uint32_t>(half + c * 32), r);
+                    if constexpr (SPLIT)
+                        lp_add_parts(r, part0 + static_cast<uint32_t>(own + c - own0) * chunk_bytes, p.split - 1,
+                                     part_bytes);
                     lp_scaled(r, cols + half + c * 32, sa, bias, u);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] *= u[j];
@@ -499,7 +584,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 if (leader)
                     mbar_arrive(tempty_bar(acc));
                 else
-                    mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
+                    mbar_arrive_remote(map_to_rank(tempty_bar(acc), even));
             }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
@@ -568,7 +653,46 @@ LpPlan lp_plan(int tiles_m, int cols, int pairs, int step) {
 }
 
 constexpr int kLpMaxDevices = 64;
+constexpr int kLpMaxSplit = 4;  // pairs a cluster: eight CTAs, the portable size
 std::atomic<int> g_lp_ready[kLpMaxDevices];
+std::atomic<int> g_lp_clusters[kLpMaxDevices][kLpMaxSplit + 1];  // of `split` pairs the GPU holds at once
+
+template <bool GATED, bool SPLIT>
+bool lp_prepare() {
+    return cudaFuncSetAttribute(linear_pair_kernel<GATED, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kLpSmemBytes)) == cudaSuccess;
+}
+
+int lp_clusters(int dev, int split) {
+    int n = g_lp_clusters[dev][split].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * split), 1, 1);
+    cfg.blockDim = dim3(kLpThreads, 1, 1);
+    cfg.dynamicSmemBytes = kLpSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel<false, true>, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = 1;
+    }
+    g_lp_clusters[dev][split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Pairs that share a tile: the most whose clusters run at once, a power of
+// two (the tile's eight chunks are dealt to them), each with four k-blocks or
+// more.
+int lp_split(int dev, int64_t tiles, int num_k_blocks) {
+    int split = kLpMaxSplit;
+    while (split > 1 && (tiles > lp_clusters(dev, split) || num_k_blocks < 4 * split)) split /= 2;
+    return split;
+}
 
 }  // namespace
 
@@ -576,10 +700,8 @@ int launch_linear_pair(const LinearCall &c) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kLpMaxDevices || c.sms < 2) return FP8L_ECUDA;
     if (!g_lp_ready[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(linear_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kLpSmemBytes)) != cudaSuccess ||
-            cudaFuncSetAttribute(linear_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kLpSmemBytes)) != cudaSuccess)
+        if (!lp_prepare<false, false>() || !lp_prepare<true, false>() || !lp_prepare<false, true>() ||
+            !lp_prepare<true, true>())
             return FP8L_ECUDA;
         g_lp_ready[dev].store(1, std::memory_order_release);
     }
@@ -588,7 +710,11 @@ int launch_linear_pair(const LinearCall &c) {
     p.num_k_blocks = (c.K + LP_BK - 1) / LP_BK;
     p.tiles_m = static_cast<int>((int64_t(c.M) + 2 * LP_BM - 1) / (2 * LP_BM));
     const int pairs = c.sms / 2;
-    const LpPlan plan = lp_plan(p.tiles_m, c.gated ? 2 * c.e.width : c.e.width, pairs, c.gated ? 64 : 32);
+    const int cols = c.gated ? 2 * c.e.width : c.e.width;
+    const int64_t whole = int64_t(p.tiles_m) * ((cols + LP_BN - 1) / LP_BN);
+    p.split = lp_split(dev, whole, p.num_k_blocks);
+    const LpPlan plan = p.split > 1 ? LpPlan{static_cast<int>(whole), (cols + LP_BN - 1) / LP_BN * LP_BN, 0, 0}
+                                    : lp_plan(p.tiles_m, cols, pairs, c.gated ? 64 : 32);
     p.main_tiles = plan.main_tiles;
     p.n_main = c.gated ? plan.n_main / 2 : plan.n_main;
     p.tail_w = plan.tail_w;
@@ -625,21 +751,22 @@ int launch_linear_pair(const LinearCall &c) {
 
     const int64_t tiles = int64_t(plan.main_tiles) + int64_t(p.tiles_m) * plan.tail_n;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.split > 1 ? tiles * p.split : (tiles < pairs ? tiles : pairs))), 1, 1);
     cfg.blockDim = dim3(kLpThreads, 1, 1);
     cfg.dynamicSmemBytes = kLpSmemBytes;
     cfg.stream = c.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * p.split);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = c.stable ? 2 : 1;
-    const cudaError_t e = c.gated ? cudaLaunchKernelEx(&cfg, linear_pair_kernel<true>, ma, mb, mbt, my, mr, p)
-                                  : cudaLaunchKernelEx(&cfg, linear_pair_kernel<false>, ma, mb, mbt, my, mr, p);
+    const auto launch = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mbt, my, mr, p); };
+    const cudaError_t e = p.split > 1 ? (c.gated ? launch(linear_pair_kernel<true, true>) : launch(linear_pair_kernel<false, true>))
+                                      : (c.gated ? launch(linear_pair_kernel<true, false>) : launch(linear_pair_kernel<false, false>));
     if (e != cudaSuccess) return FP8L_ECUDA;
     return launch_status();
 }

@@ -109,6 +109,29 @@ def test_large(M, N, K):
         check_linear(M, M, N, K, activation="silu", gated=True, out=U8, stable_weights=True)
 
 
+# every kernel over sizes on both sides of its own choices: token tiles, K split
+# over clusters of CTAs and of pairs (few tiles, long K), tail tiles
+@pytest.mark.parametrize("kernel", ["stream", "swapped", "tiled"])
+@pytest.mark.parametrize("M,N,K", [(1, 32, 16), (5, 160, 4096), (40, 2080, 272), (130, 256, 4112),
+                                   (260, 1024, 2064), (300, 512, 1040), (600, 4096, 528),
+                                   (513, 288, 8192), (1030, 4096, 1024), (700, 20480, 144)])
+def test_forced_kernels(kernel, M, N, K):
+    check_linear(M, M, N, K, HF, BF, "gelu_tanh", residual=True, per_token=True, kernel=kernel)
+    check_linear(M, M, N, K, U8, None, "silu", gated=True, kernel=kernel, stable_weights=True)
+    check_linear(M, M, N, K, BF, torch.float32, "relu", gated=True, residual=True, kernel=kernel,
+                 per_channel=False, inplace=True)
+    check_linear(M, M, N, K, U8, HF, "gelu", kernel=kernel, per_token=True)
+
+
+@pytest.mark.parametrize("kernel", ["swapped", "tiled"])
+@pytest.mark.parametrize("M,N,K", [(20, 512, 4096), (300, 512, 4096), (513, 1024, 2048)])
+def test_same_bits_every_time(kernel, M, N, K):
+    """Partial sums are added in one order: repeated calls agree bit for bit."""
+    first = check_linear(M, M, N, K, activation="silu", kernel=kernel)
+    for _ in range(5):
+        assert torch.equal(check_linear(M, M, N, K, activation="silu", kernel=kernel), first)
+
+
 def test_residual_in_place():
     for M in (1, 20, 140, 600):
         check_linear(M, M, 512, 512, residual=True, inplace=True)
@@ -210,6 +233,19 @@ def check_w8a16(seed, M, N, K, dtype=BF, bias=None, activation=None, gated=False
 def test_w8a16_tokens(M, packed):
     check_w8a16(M, M, 528, 272, HF, bias=HF, activation="gelu", residual=True, packed=packed)
     check_w8a16(M, M, 2 * 336, 400, BF, activation="silu", gated=True, packed=packed)
+
+
+@pytest.mark.parametrize("kernel", ["stream", "swapped"])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 32, 16), (3, 96, 4112), (16, 2080, 1040), (49, 256, 528),
+                                   (150, 1056, 80)])
+def test_w8a16_forced_kernels(kernel, packed, M, N, K):
+    for dtype in (BF, HF):
+        check_w8a16(M, M, N, K, dtype, torch.float32, "gelu", residual=True, packed=packed,
+                    kernel=kernel)
+        if N % 32 == 0:
+            check_w8a16(M, M, N, K, dtype, HF, "silu", gated=True, packed=packed, kernel=kernel,
+                        stable_weights=True)
 
 
 @pytest.mark.parametrize("packed", [False, True])

@@ -74,7 +74,7 @@ def test_w8a16_argument_errors(lib):
         return lib.fp8_w8a16_linear(*dict(ok, **kw).values())
     for kw in (dict(dt=b.E4M3), dict(dt=b.F32), dict(act=7), dict(bdt=b.E4M3), dict(flags=4),
                dict(flags=8), dict(x=None), dict(w=None), dict(sw=None), dict(y=None),
-               dict(ws=None)):
+               dict(ws=None), dict(flags=48)):
         assert call(**kw) == b.EINVAL, kw
     for kw in (dict(M=-1), dict(M=1 << 31), dict(N=24), dict(K=24), dict(N=0), dict(K=-16),
                dict(N=272, act=16 + 1)):
