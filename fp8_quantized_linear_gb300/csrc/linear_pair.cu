@@ -463,10 +463,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 loading = true;
             };
             if (ok && c_begin < c_end) load_res(c_begin);
+            // one lane waits for the accumulator, the others for it at the
+            // barrier (polling warps take issue slots from the two that feed
+            // the MMAs)
+            if (et == 0 && ok) {
+                mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status, p.wait_cycles, peer_abort);
+                tc_fence_before();
+            }
+            __syncwarp();
             asm volatile("bar.sync 1, %0;" ::"n"(kLpEpiThreads) : "memory");
-            if (ok)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(tfull_bar(acc), acc_phase, abort_flag, p.status,
-                                                       p.wait_cycles, peer_abort));
+            ok = __all_sync(0xFFFFFFFFu, ok && !*abort_flag);
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                    static_cast<uint32_t>(acc * LP_BN);
             // split: bytes of the sums one pair sends another, of a chunk's, and

@@ -307,8 +307,12 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
                     phase ^= 1u;
                 }
             }
-            // the accumulator is complete (or abandoned) once these retire
+            // the accumulator is complete (or abandoned) once these retire; the
+            // other warps meet this one at a barrier instead of polling for it
+            // (polling warps take issue slots from the two that feed the MMAs)
             mma_commit(done_bar);
+            mbar_wait(done_bar, 0, abort_flag, p.status, p.wait_cycles);
+            tc_fence_before();
         }
         __syncwarp();
     }
@@ -340,28 +344,34 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
         }
     }
     const OutDiv od = OutDiv::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
-    uint2 res[kLsBatch];
-    float sa[kLsBatch];
+    // scale and residual of a batch of items, loaded while the batch before is
+    // computed (the first while the stream runs)
+    struct Batch {
+        uint2 res[kLsBatch];
+        float sa[kLsBatch];
+    };
     auto load_batch = [&](int i) {
+        Batch b;
 #pragma unroll
         for (int u = 0; u < kLsBatch; ++u) {
             const int it = i + u * kLsThreads;
-            res[u] = make_uint2(0, 0);
-            sa[u] = 0.0f;
+            b.res[u] = make_uint2(0, 0);
+            b.sa[u] = 0.0f;
             if (!in || it >= i1) continue;
             const int m = m0 + (it >> gshift);
-            sa[u] = epi_ld_f32(p.token_scale + (p.per_token ? m : 0));
+            b.sa[u] = epi_ld_f32(p.token_scale + (p.per_token ? m : 0));
             if (p.e.residual != nullptr)
-                res[u] = ld_global_uint2(static_cast<const uint16_t *>(p.e.residual) +
-                                         static_cast<size_t>(m) * p.e.width + n);
+                b.res[u] = ld_global_uint2(static_cast<const uint16_t *>(p.e.residual) +
+                                           static_cast<size_t>(m) * p.e.width + n);
         }
+        return b;
     };
-    load_batch(first);
+    Batch next = load_batch(first);
 
-    // (a warp's lanes decide together: tcgen05.ld needs the whole warp)
-    bool ok = mbar_wait(done_bar, 0, abort_flag, p.status, p.wait_cycles);
-    ok = __all_sync(0xFFFFFFFFu, ok && !*abort_flag);
+    __syncthreads();
     tc_fence_after();
+    // (a warp's lanes decide together: tcgen05.ld needs the whole warp)
+    bool ok = __all_sync(0xFFFFFFFFu, !*abort_flag);
     // accumulator row (weight row) 32 warp + lane, token columns 0 .. T-1 (the
     // parts' columns added), into part[t][row] at the start of the ring
     if (ok) {
@@ -394,7 +404,8 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
     ok = !*abort_flag;
 
     for (int i = first; ok && i < i1; i += kLsBatch * kLsThreads) {
-        if (i != first) load_batch(i);
+        const Batch cur = next;
+        if (i + kLsBatch * kLsThreads < i1) next = load_batch(i + kLsBatch * kLsThreads);
 #pragma unroll
         for (int u = 0; u < kLsBatch; ++u) {
             const int it = i + u * kLsThreads;
@@ -402,15 +413,15 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
             const int t = it >> gshift;
             const uint32_t off = sbase + static_cast<uint32_t>((t * kLsPitch + c4) * 4);
             const float4 acc = ls_sum(off, split);
-            float v[4] = {fmaf(acc.x, sa[u] * sw[0], bias[0]), fmaf(acc.y, sa[u] * sw[1], bias[1]),
-                          fmaf(acc.z, sa[u] * sw[2], bias[2]), fmaf(acc.w, sa[u] * sw[3], bias[3])};
+            float v[4] = {fmaf(acc.x, cur.sa[u] * sw[0], bias[0]), fmaf(acc.y, cur.sa[u] * sw[1], bias[1]),
+                          fmaf(acc.z, cur.sa[u] * sw[2], bias[2]), fmaf(acc.w, cur.sa[u] * sw[3], bias[3])};
             activate(v, p.e.act);
             if (p.gated) {
                 const float4 up = ls_sum(off + LS_BM / 2 * 4, split);
-                v[0] *= fmaf(up.x, sa[u] * sw_up[0], bias_up[0]);
-                v[1] *= fmaf(up.y, sa[u] * sw_up[1], bias_up[1]);
-                v[2] *= fmaf(up.z, sa[u] * sw_up[2], bias_up[2]);
-                v[3] *= fmaf(up.w, sa[u] * sw_up[3], bias_up[3]);
+                v[0] *= fmaf(up.x, cur.sa[u] * sw_up[0], bias_up[0]);
+                v[1] *= fmaf(up.y, cur.sa[u] * sw_up[1], bias_up[1]);
+                v[2] *= fmaf(up.z, cur.sa[u] * sw_up[2], bias_up[2]);
+                v[3] *= fmaf(up.w, cur.sa[u] * sw_up[3], bias_up[3]);
             }
             const size_t o = static_cast<size_t>(m0 + t) * p.e.width + n;
             if (p.e.out_dtype == FP8L_E4M3) {
@@ -419,7 +430,7 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
                 *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.e.y) + o) = lo | (hi << 16);
             } else {
                 if (p.e.residual != nullptr) {
-                    const float2 a = widen_pair(res[u].x, p.e.out_dtype), b = widen_pair(res[u].y, p.e.out_dtype);
+                    const float2 a = widen_pair(cur.res[u].x, p.e.out_dtype), b = widen_pair(cur.res[u].y, p.e.out_dtype);
                     v[0] += a.x;
                     v[1] += a.y;
                     v[2] += b.x;
