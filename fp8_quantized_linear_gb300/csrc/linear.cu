@@ -65,24 +65,34 @@ int check_output(const Epilogue &e, int64_t M, int64_t N, const void *x, size_t 
     return FP8L_OK;
 }
 
-// The kernel of fp8_linear: weights streamed for a few tokens and small
-// weights, tiles over SM pairs for many tokens, the swapped-operand kernel
-// between.
+// The kernel of fp8_linear (times of each product alone in a replayed graph
+// over rotating operands, us):
+//   - weights streamed through registers for a few tokens and small weights,
+//     whose time is the start of the kernel (M = 1 at 4096 x 4096 5.1 against
+//     7.4 swapped, M = 8 at 4096 x 11008 10.8 against 11.6; but M = 1 at 10240
+//     x 8192 19.2 against 17.6, M = 16 at 6144 x 4096 11.3 against 9.6);
+//   - swapped operands up to 128 tokens, and beyond while tokens x weight rows
+//     stay below 2^20, too few 256 x 256 tiles for the SM pairs (M = 144 at
+//     6144 x 4096 13.3 against 14.6 tiled, M = 200 at 6144 x 4096 16.2 against
+//     14.9, M = 128 at 28672 x 4096 32.7 against 32.5);
+//   - tiles over SM pairs otherwise.
 unsigned choose_linear(int64_t M, int64_t N, int64_t K) {
     const int64_t wbytes = N * K;
-    if ((M <= 4 && wbytes <= (int64_t(24) << 20)) || (M <= 16 && wbytes <= (int64_t(16) << 20)))
+    if ((M <= 8 && wbytes <= (int64_t(48) << 20)) || (M <= 16 && wbytes <= (int64_t(16) << 20)))
         return FP8L_KERNEL_STREAM;
-    return M > 256 ? FP8L_KERNEL_TILED : FP8L_KERNEL_SWAPPED;
+    return M > 128 && M * N > (1 << 20) ? FP8L_KERNEL_TILED : FP8L_KERNEL_SWAPPED;
 }
 
 // The kernel of fp8_w8a16_linear: weights streamed through registers for a few
-// tokens, else tokens in parts through the swapped-operand kernel.
+// tokens (M = 1 at 12288 x 4096, packed, 11.2 us against 13.1 swapped; M = 8 at
+// 28672 x 8192 44.2 against 41.7; M = 12 at 4096 x 11008 13.4 against 14.0, at
+// 12288 x 4096 16.2 against 18.6), else tokens in parts through the
+// swapped-operand kernel (M = 16 at 22016 x 4096 gated 20.6 against 25.0, M =
+// 32 at 4096 x 11008 15.7 against 26.6).
 unsigned choose_w8a16_linear(int64_t M, int64_t N, int64_t K, unsigned flags) {
-    (void)N;
-    (void)K;
     const unsigned k = flags & FP8L_KERNEL_MASK;
     if (k != FP8L_KERNEL_AUTO) return k;
-    return M <= 8 ? FP8L_KERNEL_STREAM : FP8L_KERNEL_SWAPPED;
+    return M <= 8 || (M <= 16 && N * K <= (int64_t(44) << 20)) ? FP8L_KERNEL_STREAM : FP8L_KERNEL_SWAPPED;
 }
 
 }  // namespace

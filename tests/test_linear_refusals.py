@@ -67,7 +67,7 @@ def test_linear_output_over_inputs(lib):
 
 
 def test_w8a16_argument_errors(lib):
-    ok = dict(x=at(0), dt=b.F16, w=at(1), sw=at(2), M=9, N=256, K=64, bias=at(3), bdt=b.F16, act=1,
+    ok = dict(x=at(0), dt=b.F16, w=at(1), sw=at(2), M=17, N=256, K=64, bias=at(3), bdt=b.F16, act=1,
               res=at(4), y=at(5), ws=at(6), flags=0, st=None)
 
     def call(**kw):
