@@ -14,6 +14,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "common.cuh"
 
@@ -80,6 +81,28 @@ __device__ __forceinline__ void activate(float (&v)[COUNT], int act) {
         for (int i = 0; i < COUNT; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
     }
 }
+
+// Codes of t / out_scale: t times the rounded reciprocal (2^-23 of t off the
+// quotient at most, where t itself carries the product's float32 rounding),
+// the division itself where the reciprocal leaves the normal range.  (The
+// correctly rounded quotient of fp8_scaled_mm takes eight instructions for
+// this one: 0.5 us of a tile's epilogue.)
+struct OutScale {
+    float os, inv;
+    __device__ __forceinline__ static OutScale make(float os) {
+        const bool plain = os >= 0x1p-120f && os <= 0x1p120f;
+        return OutScale{os, plain ? __frcp_rn(os) : 0.0f};
+    }
+    __device__ __forceinline__ float of(float t) const { return inv != 0.0f ? t * inv : __fdiv_rn(t, os); }
+    // four codes, the first in the low byte
+    __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
+        return static_cast<uint32_t>(
+                   __nv_cvt_float2_to_fp8x2(make_float2(of(a), of(b)), __NV_SATFINITE, __NV_E4M3)) |
+               (static_cast<uint32_t>(
+                    __nv_cvt_float2_to_fp8x2(make_float2(of(c), of(d)), __NV_SATFINITE, __NV_E4M3))
+                << 16);
+    }
+};
 
 // Loads of what the preceding kernel on the stream may have written:
 // coherent, and kept after griddepcontrol.wait.

@@ -58,12 +58,13 @@ constexpr int LP_STAGES = 5;  // (six: the same, and no room for the boxes)
 constexpr int kLpABytes = LP_BM * LP_BK;
 constexpr int kLpBBytes = (LP_BN / 2) * LP_BK;
 constexpr int kLpStageBytes = kLpABytes + kLpBBytes;
-constexpr int kLpEpiWarps = 8;
+constexpr int kLpEpiWarps = 16;
+constexpr int kLpEpiGroups = kLpEpiWarps / 4;  // warps of a TMEM lane quarter
 constexpr int kLpEpiThreads = 32 * kLpEpiWarps;
 constexpr int kLpThreads = 64 + kLpEpiThreads;
 constexpr int kLpBarriers = 2 * LP_STAGES + 2 + 2 + 1;
 constexpr int kLpBoxBytes = 32 * 64;             // 32 rows of 32 16-bit values
-constexpr int kLpBoxes = 2 * kLpEpiWarps;
+constexpr int kLpBoxes = kLpEpiWarps;
 constexpr int kLpColBytes = 2 * 2 * LP_BN * 4;  // two tiles' scales and biases
 constexpr int kLpBoxOffset = LP_STAGES * kLpStageBytes;  // from the 1024-aligned base
 constexpr int kLpColOffset = kLpBoxOffset + kLpBoxes * kLpBoxBytes;
@@ -155,6 +156,17 @@ __device__ __forceinline__ void lp_store_box(const CUtensorMap *map, int x, int 
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
+__device__ __forceinline__ void lp_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // until at most N of this thread's stores have still to read shared memory
 template <int N>
 __device__ __forceinline__ void lp_stores_read() {
@@ -181,14 +193,15 @@ __device__ __forceinline__ uint4 lp_ld_shared(uint32_t addr) {
     return v;
 }
 
-// z = acc * (sa * scale) + bias of 32 columns; cols: the tile's scales, then
+// z = acc * (sa * scale) + bias of COUNT columns; cols: the tile's scales, then
 // its biases LP_BN floats on, in shared memory (all lanes read one address)
-__device__ __forceinline__ void lp_scaled(const uint32_t (&r)[32], const float *cols, float sa, bool bias,
-                                          float (&v)[32]) {
+template <int COUNT>
+__device__ __forceinline__ void lp_scaled(const uint32_t (&r)[COUNT], const float *cols, float sa, bool bias,
+                                          float (&v)[COUNT]) {
     const float4 *s4 = reinterpret_cast<const float4 *>(cols);
     const float4 *b4 = reinterpret_cast<const float4 *>(cols + LP_BN);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < COUNT / 4; ++q) {
         const float4 s = s4[q];
         const float4 b = bias ? b4[q] : make_float4(0.f, 0.f, 0.f, 0.f);
         v[4 * q] = fmaf(__uint_as_float(r[4 * q]), sa * s.x, b.x);
@@ -200,10 +213,11 @@ __device__ __forceinline__ void lp_scaled(const uint32_t (&r)[32], const float *
 
 // The sums of a chunk (32 accumulator columns) that other pairs sent, added to
 // this pair's: 16-byte pieces [source][chunk][piece][row] from `part`.
-__device__ __forceinline__ void lp_add_parts(uint32_t (&r)[32], uint32_t part, int sources, uint32_t source_bytes) {
+template <int COUNT>
+__device__ __forceinline__ void lp_add_parts(uint32_t (&r)[COUNT], uint32_t part, int sources, uint32_t source_bytes) {
     for (int q = 0; q < sources; ++q, part += source_bytes) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < COUNT / 4; ++j) {
             const uint4 w = lp_ld_shared(part + static_cast<uint32_t>(j * LP_BM * 16));
             r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + __uint_as_float(w.x));
             r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + __uint_as_float(w.y));
@@ -415,13 +429,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         const int et = static_cast<int>(threadIdx.x) - 64;
         const int row = static_cast<int>(rank) * LP_BM + quarter * 32 + lane;
         const float sa0 = epi_ld_f32(p.a_scale);
-        const OutDiv od = OutDiv::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
+        const OutScale os = OutScale::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
         const bool bias = p.e.bias != nullptr;
-        const uint32_t box0 = sbase + kLpBoxOffset + static_cast<uint32_t>((warp - 2) * 2 * kLpBoxBytes);
-        const uint32_t box_bar = box_bar0 + 16u * (warp - 2);
-        int buf = 0;             // the box of the next chunk
-        uint32_t box_phase = 0;  // parities of the two boxes' barriers
-        bool loading = false;    // a residual box on its way into `buf`
+        const uint32_t box = sbase + kLpBoxOffset + static_cast<uint32_t>((warp - 2) * kLpBoxBytes);
+        const uint32_t box_bar = box_bar0 + 8u * (warp - 2);
+        uint32_t box_phase = 0;  // parity of the box's barrier
+        bool loading = false;    // a residual on its way into the box
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -441,24 +454,25 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     if (et >= half) n = p.e.width + t.n0 + et - half;
                     in = et < t.w && t.n0 + (et >= half ? et - half : et) < p.e.width;
                 }
-                cols[et] = in ? epi_ld_f32(p.w_scale + (p.w_per_channel ? n : 0)) : 0.0f;
-                if (bias) cols[LP_BN + et] = in ? epi_bias(p.e, n) : 0.0f;
+                if (et < LP_BN) {
+                    cols[et] = in ? epi_ld_f32(p.w_scale + (p.w_per_channel ? n : 0)) : 0.0f;
+                    if (bias) cols[LP_BN + et] = in ? epi_bias(p.e, n) : 0.0f;
+                }
             }
             const float sa = p.a_per_token ? (row_ok ? epi_ld_f32(p.a_scale + m) : 0.0f) : sa0;
             const int chunks = GATED ? half / 32 : t.w / 32;
             // this pair's share of the chunks, this warp's half of it
             const int own0 = SPLIT ? chunks * kpart / p.split : 0;
             const int own = SPLIT ? chunks * (kpart + 1) / p.split - own0 : chunks;
-            const int c_begin = own0 + grp * own / 2, c_end = own0 + (grp + 1) * own / 2;
+            const int c_begin = own0 + grp * own / kLpEpiGroups, c_end = own0 + (grp + 1) * own / kLpEpiGroups;
             // (a box partly outside the matrix is cut by TMA; one wholly outside is left out)
             const int box_row = t.mt * 2 * LP_BM + static_cast<int>(rank) * LP_BM + quarter * 32;
             auto box_in = [&](int c) { return box_row < p.M && t.n0 + c * 32 < p.e.width; };
             auto load_res = [&](int c) {
                 if (p.e.residual == nullptr || !box_in(c)) return;
                 if (lane == 0) {
-                    lp_stores_read<0>();  // the buffer's last store is through with it
-                    lp_load_box(box0 + buf * kLpBoxBytes, &tmap_r, 2 * (t.n0 + c * 32), box_row,
-                                box_bar + 8u * buf);
+                    lp_stores_read<0>();  // the last store is through with the box
+                    lp_load_box(box, &tmap_r, 2 * (t.n0 + c * 32), box_row, box_bar);
                 }
                 loading = true;
             };
@@ -492,7 +506,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     const uint32_t bytes = chunk_bytes * static_cast<uint32_t>((GATED ? 2 : 1) * (o1 - o0));
                     const uint32_t dst = map_to_rank(part0, 2u * static_cast<uint32_t>(to) + rank) + slot * bytes;
                     const int n = (GATED ? 2 : 1) * (o1 - o0);
-                    for (int i = grp; i < n; i += 2) {
+                    for (int i = grp; i < n; i += kLpEpiGroups) {
                         // gated: the gate's chunks, then the up's
                         const int col = GATED && i >= o1 - o0 ? half + (o0 + i - (o1 - o0)) * 32 : (o0 + i) * 32;
                         uint32_t r[32];
@@ -521,23 +535,25 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 }
                 activate(v, p.e.act);
                 if constexpr (GATED) {
-                    uint32_t r[32];
-                    float u[32];
-                    tmem_ld32(taddr + static_cast<uint32_t>(half + c * 32), r);
-                    if constexpr (SPLIT)
-                        lp_add_parts(r, part0 + static_cast<uint32_t>(own + c - own0) * chunk_bytes, p.split - 1,
-                                     part_bytes);
-                    lp_scaled(r, cols + half + c * 32, sa, bias, u);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= u[j];
+                    for (int h = 0; h < 2; ++h) {  // (sixteen columns at a time: registers)
+                        uint32_t r[16];
+                        float u[16];
+                        lp_tmem_ld16(taddr + static_cast<uint32_t>(half + c * 32 + 16 * h), r);
+                        if constexpr (SPLIT)
+                            lp_add_parts(r, part0 + static_cast<uint32_t>(own + c - own0) * chunk_bytes +
+                                                static_cast<uint32_t>(4 * h * LP_BM * 16),
+                                         p.split - 1, part_bytes);
+                        lp_scaled(r, cols + half + c * 32 + 16 * h, sa, bias, u);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[16 * h + j] *= u[j];
+                    }
                 }
                 if (!box_in(c)) continue;
                 if (p.e.out_dtype == FP8L_E4M3) {
                     uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        w[i] = out_e4m3x2(od.quot(v[4 * i]), od.quot(v[4 * i + 1])) |
-                               (out_e4m3x2(od.quot(v[4 * i + 2]), od.quot(v[4 * i + 3])) << 16);
+                    for (int i = 0; i < 8; ++i) w[i] = os.codes(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     if (row_ok) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.e.y) +
                                                                static_cast<size_t>(m) * p.e.width + n0);
@@ -547,12 +563,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     __syncwarp();
                     continue;
                 }
-                const uint32_t box = box0 + buf * kLpBoxBytes;
                 if (p.e.residual != nullptr) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(box_bar + 8u * buf, (box_phase >> buf) & 1u,
-                                                           abort_flag, p.status, p.wait_cycles, peer_abort));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(box_bar, box_phase, abort_flag, p.status,
+                                                           p.wait_cycles, peer_abort));
                     if (!ok) break;  // (the lanes decide together: tcgen05.ld needs the whole warp)
-                    box_phase ^= 1u << buf;
+                    box_phase ^= 1u;
                     loading = false;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -566,7 +581,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                         }
                     }
                 } else {
-                    if (lane == 0) lp_stores_read<1>();  // all but the other buffer's store
+                    if (lane == 0) lp_stores_read<0>();
                     __syncwarp();
                 }
 #pragma unroll
@@ -577,11 +592,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
                                  pack_out16(v[8 * q + 6], v[8 * q + 7], p.e.out_dtype));
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                buf ^= 1;
-                // the next chunk's residual before this one's store, whose
-                // reading it would otherwise wait for
-                if (c + 1 < c_end) load_res(c + 1);
                 if (lane == 0) lp_store_box(&tmap_y, 2 * n0, box_row, box);
+                if (c + 1 < c_end) load_res(c + 1);
             }
             if (!ok) continue;
             tc_fence_before();
@@ -597,7 +609,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
         // this warp's boxes have landed and left before the CTA exits
         if (lane == 0) {
-            if (loading) mbar_wait_drain(box_bar + 8u * buf, (box_phase >> buf) & 1u, p.status);
+            if (loading) mbar_wait_drain(box_bar, box_phase, p.status);
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
         __syncwarp();

@@ -343,7 +343,7 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
             bias_up[j] = epi_bias(p.e, p.e.width + n + j);
         }
     }
-    const OutDiv od = OutDiv::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
+    const OutScale os = OutScale::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
     // scale and residual of a batch of items, loaded while the batch before is
     // computed (the first while the stream runs)
     struct Batch {
@@ -425,9 +425,7 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
             }
             const size_t o = static_cast<size_t>(m0 + t) * p.e.width + n;
             if (p.e.out_dtype == FP8L_E4M3) {
-                const uint32_t lo = out_e4m3x2(od.quot(v[0]), od.quot(v[1]));
-                const uint32_t hi = out_e4m3x2(od.quot(v[2]), od.quot(v[3]));
-                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.e.y) + o) = lo | (hi << 16);
+                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.e.y) + o) = os.codes(v[0], v[1], v[2], v[3]);
             } else {
                 if (p.e.residual != nullptr) {
                     const float2 a = widen_pair(cur.res[u].x, p.e.out_dtype), b = widen_pair(cur.res[u].y, p.e.out_dtype);
