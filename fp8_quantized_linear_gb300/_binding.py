@@ -848,13 +848,9 @@ def _load_calls():
     spec = importlib.util.spec_from_file_location(f"{__package__}._calls", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
-    module.setup(_status_error, lambda index: workspace(index).data_ptr())
+    module.setup(Fp8LinearError)
     _calls = module
     return module
-
-
-def _status_error(status: int, where: str) -> Fp8LinearError:
-    return Fp8LinearError(status, where)
 
 
 def _choice(table: dict, key, what: str) -> int:
@@ -877,8 +873,9 @@ def fp8_linear(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale:
     N / 2].  residual: [M, N] ([M, N / 2]) of the output's 16-bit type, added
     last; y may be the residual itself.  out_dtype: y's, else the residual's,
     else bf16; uint8 for E4M3 codes of the result / out_scale (no residual
-    then).  Scales, ws, stable_weights, per_token and kernel as for
-    fp8_scaled_mm."""
+    then).  ws: where a time-out is recorded (None: the library's status word;
+    fp8l_read_status reports both).  Scales, stable_weights, per_token and
+    kernel as for fp8_scaled_mm."""
     return (_calls or _load_calls()).linear(
         a, w, a_scale, w_scale, bias, _choice(ACTIVATIONS, activation, "activation"), gated,
         residual, out_dtype, out_scale, y, ws,

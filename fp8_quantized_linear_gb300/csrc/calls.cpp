@@ -3,9 +3,8 @@
 //
 // These calls stand in front of kernels of two to fifteen microseconds, and the
 // same checks written in Python took longer than that (13 to 20 us a call on
-// the GB300's host cores; 5 to 9 us here).  The extension holds no state but the
-// addresses of the devices' workspaces, and every error is a Python exception:
-// a C++ one does not leave it.
+// the GB300's host cores; 4 to 8 us here).  The extension holds no state, and
+// every error is a Python exception: a C++ one does not leave it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -23,10 +22,7 @@ namespace {
 using at::ScalarType;
 using at::Tensor;
 
-constexpr int kMaxDevices = 64;
-void *g_workspace[kMaxDevices];        // workspace(device), set from Python
-PyObject *g_status_error = nullptr;    // called with (status, entry point): the exception
-PyObject *g_workspace_of = nullptr;    // called with a device index: workspace(device)'s address
+PyObject *g_status_error = nullptr;  // called with (status, entry point): the exception
 
 struct Refusal {
     PyObject *type;
@@ -86,19 +82,6 @@ struct Output {
         return given;
     }
 };
-
-void *workspace_of(int index) {
-    if (index >= kMaxDevices) value_error("device index out of range");
-    if (g_workspace[index] == nullptr) {
-        PyObject *at = PyObject_CallFunction(g_workspace_of, "i", index);
-        if (at == nullptr) throw python_error();
-        void *p = PyLong_AsVoidPtr(at);
-        Py_DECREF(at);
-        if (p == nullptr) throw python_error();
-        g_workspace[index] = p;
-    }
-    return g_workspace[index];
-}
 
 // Null, with the exception set, unless status is FP8L_OK.
 bool failed(int status, const char *where) {
@@ -206,7 +189,7 @@ PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t count) {
         scales != 1 ? 1 : 0, e.bias, e.bias_code,
         static_cast<int>(number(args[5])) | (gated ? FP8L_ACT_GATED : 0), e.residual,
         codes ? static_cast<const float *>(out_scale->data_ptr()) : nullptr, result.ptr(),
-        codes ? FP8L_E4M3 : code16(out), ws != nullptr ? ws->data_ptr() : workspace_of(index), flags,
+        codes ? FP8L_E4M3 : code16(out), address(ws), flags,
         c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
     if (failed(status, "fp8_linear")) return nullptr;
     return result.result();
@@ -332,16 +315,11 @@ PyObject *add_rmsnorm_quant(PyObject *, PyObject *const *args, Py_ssize_t count)
     CALL_END
 }
 
-// setup(status_error, workspace_of)
-PyObject *setup(PyObject *, PyObject *args) {
-    PyObject *error = nullptr, *workspace = nullptr;
-    if (!PyArg_ParseTuple(args, "OO", &error, &workspace)) return nullptr;
+// setup(status_error)
+PyObject *setup(PyObject *, PyObject *error) {
     Py_INCREF(error);
-    Py_INCREF(workspace);
     Py_XDECREF(g_status_error);
-    Py_XDECREF(g_workspace_of);
     g_status_error = error;
-    g_workspace_of = workspace;
     Py_RETURN_NONE;
 }
 
@@ -351,7 +329,7 @@ PyMethodDef kMethods[] = {
      METH_FASTCALL, nullptr},
     {"add_rmsnorm_quant", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(add_rmsnorm_quant)),
      METH_FASTCALL, nullptr},
-    {"setup", setup, METH_VARARGS, nullptr},
+    {"setup", setup, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

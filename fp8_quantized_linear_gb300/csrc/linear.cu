@@ -106,8 +106,7 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     using namespace fp8l;
     if (out_dtype != FP8L_F16 && out_dtype != FP8L_BF16 && out_dtype != FP8L_E4M3) return FP8L_EINVAL;
     if ((flags & ~(FP8L_WEIGHTS_STABLE | FP8L_A_PER_TOKEN | FP8L_KERNEL_MASK)) != 0u) return FP8L_EINVAL;
-    if (a_scale == nullptr || w_scale == nullptr || workspace == nullptr || w == nullptr)
-        return FP8L_EINVAL;
+    if (a_scale == nullptr || w_scale == nullptr || w == nullptr) return FP8L_EINVAL;
     if (out_dtype == FP8L_E4M3 && out_scale == nullptr) return FP8L_EINVAL;
     LinearCall c{};
     int st = check_epilogue(M, N, K, bias, bias_dtype, activation, residual, out_scale, y, out_dtype,
@@ -121,12 +120,18 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     st = check_output(c.e, M, N, a, static_cast<size_t>(M) * K, w, static_cast<size_t>(N) * K, a_scale,
                       pt ? M : 1, w_scale, pc ? N : 1);
     if (st != FP8L_OK) return st;
-    if (bias == nullptr && activation == FP8L_ACT_NONE && residual == nullptr)
-        return fp8_scaled_mm(a, w, M, N, K, a_scale, w_scale, w_per_channel, out_scale, y, out_dtype,
-                             workspace, flags, stream);
     st = check_device(&c.sms);
     if (st != FP8L_OK) return st;
     if (M == 0) return FP8L_OK;
+    unsigned *status = nullptr;
+    if (workspace == nullptr) {  // the library's status word in its place
+        if (library_status_word(&status) != FP8L_OK) return FP8L_ECUDA;
+        workspace = status;
+    }
+    const unsigned choice = flags & FP8L_KERNEL_MASK;
+    if (choice == FP8L_KERNEL_AUTO && bias == nullptr && activation == FP8L_ACT_NONE && residual == nullptr)
+        return fp8_scaled_mm(a, w, M, N, K, a_scale, w_scale, w_per_channel, out_scale, y, out_dtype,
+                             workspace, flags, stream);
     c.x = a;
     c.x_dtype = FP8L_E4M3;
     c.w = w;
@@ -140,8 +145,7 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     c.status = status_word(workspace);
     c.stable = (flags & FP8L_WEIGHTS_STABLE) != 0u;
     c.stream = as_stream(stream);
-    unsigned kernel = flags & FP8L_KERNEL_MASK;
-    if (kernel == FP8L_KERNEL_AUTO) kernel = choose_linear(M, N, K);
+    const unsigned kernel = choice != FP8L_KERNEL_AUTO ? choice : choose_linear(M, N, K);
     if (kernel == FP8L_KERNEL_STREAM) return launch_linear_stream(c);
     if (kernel == FP8L_KERNEL_TILED) return launch_linear_pair(c);
     return launch_linear_swapped(c, 1, a_scale);
@@ -178,11 +182,19 @@ extern "C" int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, co
                       c.packed ? fp8_packed_weight_bytes(N, K) : static_cast<size_t>(N) * K, nullptr, 0,
                       w_scale, N);
     if (st != FP8L_OK) return st;
-    if (bias == nullptr && activation == FP8L_ACT_NONE && residual == nullptr)
+    if ((flags & FP8L_KERNEL_MASK) == FP8L_KERNEL_AUTO && bias == nullptr &&
+        activation == FP8L_ACT_NONE && residual == nullptr)
         return fp8_w8a16_mm(x, x_dtype, w, w_scale, M, N, K, y, flags, stream);
     const size_t scratch = M > 0 ? fp8_w8a16_linear_workspace_bytes(x_dtype, M, N, K, flags) : 0;
     if (scratch > 0 && workspace == nullptr) return FP8L_EINVAL;
     if (!aligned16(workspace)) return FP8L_EALIGN;
+    const size_t w_bytes = c.packed ? fp8_packed_weight_bytes(N, K) : static_cast<size_t>(N) * K;
+    const size_t y_bytes = static_cast<size_t>(M) * static_cast<size_t>(c.e.width) * 2;
+    if (overlap(workspace, scratch, x, static_cast<size_t>(M) * K * 2) ||
+        overlap(workspace, scratch, w, w_bytes) || overlap(workspace, scratch, y, y_bytes) ||
+        overlap(workspace, scratch, residual, y_bytes) || overlap(workspace, scratch, w_scale, 4 * N) ||
+        overlap(workspace, scratch, bias, static_cast<size_t>(N) * (bias_dtype == FP8L_F32 ? 4 : 2)))
+        return FP8L_EINVAL;
     st = check_device(&c.sms);
     if (st != FP8L_OK) return st;
     if (M == 0) return FP8L_OK;

@@ -66,6 +66,14 @@ constexpr size_t kLsSmem = 112 * 1024;
 // with parts so many that three stages of weights and parts fit kLsSmem
 constexpr int ls_max_tokens(int parts) { return parts == 1 ? 128 : (parts == 2 ? 64 : 48); }
 
+// Tiles that M tokens take, and the tokens of each (a multiple of 16).
+int tokens_a_tile(int parts, int64_t M, int *tiles) {
+    const int64_t most = ls_max_tokens(parts);
+    const int64_t n = (M + most - 1) / most;
+    *tiles = static_cast<int>(n);
+    return static_cast<int>(((M + n - 1) / n + 15) & ~int64_t(15));
+}
+
 struct SwappedArgs {
     int M, K, T;  // T: tokens a tile, a multiple of 16
     int parts;    // MMA N = parts * T
@@ -514,10 +522,9 @@ int launch_linear_swapped(const LinearCall &c, int parts, const float *token_sca
     p.M = c.M;
     p.K = c.K;
     p.parts = parts;
-    const int most = ls_max_tokens(parts);
-    p.m_tiles = (c.M + most - 1) / most;
-    p.T = ((c.M + p.m_tiles - 1) / p.m_tiles + 15) & ~15;
+    p.T = tokens_a_tile(parts, c.M, &p.m_tiles);
     const int cols = parts * p.T;
+    if (int64_t(p.m_tiles) * cols > 0x7FFFFFFF) return FP8L_ESHAPE;  // rows of the parts
     p.stage_bytes = kLsWBytes + cols * LS_BK;
     // the most stages that fit; the float tile reuses the ring
     int stages = static_cast<int>((kLsSmem - 1024 - 24) / (p.stage_bytes + 16));
@@ -656,12 +663,6 @@ split_tokens_kernel(const uint4 *x, int K, int T, uint8_t *codes, float *scale) 
     }
 }
 
-int tokens_a_tile(int parts, int M, int *tiles) {
-    const int most = ls_max_tokens(parts);
-    *tiles = (M + most - 1) / most;
-    return ((M + *tiles - 1) / *tiles + 15) & ~15;
-}
-
 }  // namespace
 
 int linear_parts(int x_dtype) { return x_dtype == FP8L_BF16 ? 2 : 3; }
@@ -669,7 +670,7 @@ int linear_parts(int x_dtype) { return x_dtype == FP8L_BF16 ? 2 : 3; }
 size_t linear_parts_bytes(int x_dtype, int64_t M, int64_t K) {
     const int parts = linear_parts(x_dtype);
     int tiles = 0;
-    const int T = tokens_a_tile(parts, static_cast<int>(M), &tiles);
+    const int T = tokens_a_tile(parts, M, &tiles);
     return size_t(tiles) * parts * T * size_t(K) + ((size_t(M) * 4 + 15) & ~size_t(15));
 }
 

@@ -324,8 +324,11 @@ enum fp8l_activation {
  *   out_dtype FP8L_BF16 / FP8L_F16: y[m,n] = RN(t[m,n] + residual[m,n])
  *   out_dtype FP8L_E4M3:            y[m,n] = E4M3(t[m,n] / out_scale[0])
  *
- * in float32 throughout, rounded once.  a, w, a_scale, w_scale,
- * w_per_channel, out_scale and workspace as for fp8_scaled_mm; w (and bias,
+ * in float32 throughout, rounded once (t / out_scale within 2^-23 of t /
+ * out_scale before the cast).  a, w, a_scale, w_scale, w_per_channel and
+ * out_scale as for fp8_scaled_mm; workspace: fp8l_workspace_bytes() bytes for
+ * the status word, or NULL, when a time-out is recorded in the library's
+ * status word (fp8l_read_status reports both); w (and bias,
  * and a per-channel w_scale) hold the N/2 gate rows first, then the N/2 up
  * rows, when gated.  bias: N values of bias_dtype (FP8L_F16, FP8L_BF16 or
  * FP8L_F32, aligned to their size), or NULL.  activation: an
@@ -335,7 +338,11 @@ enum fp8l_activation {
  * and shares memory with nothing else that is read (FP8L_EINVAL).  N is a
  * multiple of 16 (32 when gated), K of 16, both positive and at most 2^20;
  * 0 <= M <= 2^31 - 1 (M == 0 launches nothing).  flags: any of
- * FP8L_WEIGHTS_STABLE and FP8L_A_PER_TOKEN. */
+ * FP8L_WEIGHTS_STABLE (the bias is not part of the promise) and
+ * FP8L_A_PER_TOKEN, and one FP8L_KERNEL_* choice (a tuning and testing
+ * option; every kernel takes every call, FP8L_KERNEL_STREAM up to 1048560
+ * tokens, FP8L_ESHAPE above).  With FP8L_KERNEL_AUTO a call without bias,
+ * activation and residual is fp8_scaled_mm. */
 FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N, int64_t K,
                         const float *a_scale, const float *w_scale, int w_per_channel,
                         const void *bias, int bias_dtype, int activation, const void *residual,
@@ -347,13 +354,18 @@ FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N
  * fp8_linear, with y and residual of x_dtype.  x, w (row-major, or packed
  * with FP8L_WEIGHTS_PACKED: the packed layout of the whole [N, K], gate and
  * up rows alike) and w_scale as for fp8_w8a16_mm; the other arguments and
- * the rules on y as for fp8_linear.  Without bias, activation and residual
- * the call is fp8_w8a16_mm.  workspace:
+ * the rules on y as for fp8_linear.  Up to 8 tokens (16 with few weights) the
+ * weights are streamed through the CUDA cores; above, a token is held as a
+ * sum of E4M3 parts (two for bf16, three for fp16), whose products with the
+ * weights are exact: what the parts leave out of a value is below 2^-21
+ * (bf16) or 2^-25 (fp16) of the token's largest magnitude.  With
+ * FP8L_KERNEL_AUTO a call without bias, activation and residual is
+ * fp8_w8a16_mm.  workspace:
  * fp8_w8a16_linear_workspace_bytes() bytes for these arguments (16-byte
  * aligned, any contents; may be NULL when that is 0), sharing memory with no other argument), written by the call
  * and free for other use when it has run; calls that may overlap need one
- * each.  flags: any of FP8L_WEIGHTS_STABLE and FP8L_WEIGHTS_PACKED.  A
- * time-out of a device-side wait is recorded as for fp8_w8a16_mm. */
+ * each.  flags: any of FP8L_WEIGHTS_STABLE and FP8L_WEIGHTS_PACKED, and
+ * FP8L_KERNEL_STREAM or FP8L_KERNEL_SWAPPED (any M).  A time-out of a device-side wait is recorded as for fp8_w8a16_mm. */
 FP8L_API size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t N, int64_t K,
                                                  unsigned flags);
 FP8L_API int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, const float *w_scale,

@@ -35,7 +35,7 @@ def test_linear_argument_errors(lib):
                dict(act=32), dict(bdt=b.E4M3), dict(bdt=9), dict(flags=2), dict(flags=8),
                dict(flags=64), dict(out=b.E4M3, res=None), dict(out=b.E4M3, os=at(8))):
         assert call(**kw) == b.EINVAL, kw
-    for name in ("a", "w", "sa", "sw", "y", "ws"):
+    for name in ("a", "w", "sa", "sw", "y"):
         assert call(**{name: None}) == b.EINVAL, name
     for kw in (dict(M=-1), dict(M=1 << 31), dict(N=0), dict(N=8), dict(N=-16), dict(K=0), dict(K=8),
                dict(N=(1 << 20) + 16), dict(K=(1 << 20) + 16), dict(N=48, act=16 + 2)):
@@ -83,6 +83,8 @@ def test_w8a16_argument_errors(lib):
         assert call(**{name: at(0) + 4}) == b.EALIGN, name
     assert call(sw=at(2) + 2) == b.EALIGN and call(bias=at(3) + 1) == b.EALIGN
     y = at(5)
+    for name in ("x", "w", "sw", "bias", "res", "y"):
+        assert call(**{"ws": ok[name] + 16}) == b.EINVAL, name
     for kw in (dict(x=y), dict(w=y + 512), dict(sw=y + 16), dict(bias=y + 16), dict(res=y + 16)):
         assert call(**kw) == b.EINVAL, kw
 
