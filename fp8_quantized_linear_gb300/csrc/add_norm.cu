@@ -163,8 +163,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *part) {
     return v;
 }
 
+// r = 1 / sqrt(ms): a reciprocal of a root, and one Newton step with the
+// residual 1 - ms y^2 to twice the precision (ms y = hi + lo), which leaves
+// little more than r's own rounding
 __device__ __forceinline__ uint64_t rms_factor(float ss, int K, float eps) {
-    const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(K)), eps)));
+    const float ms = __fadd_rn(__fdiv_rn(ss, static_cast<float>(K)), eps);
+    const float y = __frcp_rn(__fsqrt_rn(ms));
+    const float hi = __fmul_rn(ms, y), lo = __fmaf_rn(ms, y, -hi);
+    const float e = __fmaf_rn(-lo, y, __fmaf_rn(-hi, y, 1.0f));
+    // (a zero row without eps has y infinite and stays that)
+    const float r = ms > 0x1p-100f ? __fmaf_rn(0.5f * y, e, y) : y;
     return f2_pack(__float_as_uint(r), __float_as_uint(r));
 }
 
