@@ -24,22 +24,32 @@
 //              kernel.
 //   warp 1     TMEM; in the even CTA one lane issues the MMAs, whose commits
 //              arrive on the barriers of both CTAs.
-//   warps 2-9  epilogue in each CTA, two warps a TMEM lane quarter (each half
-//              of the tile's 32-column chunks).  A tile's scales and biases
-//              are spread over the 256 threads once and read back from shared
-//              memory (any type, any alignment, one load a column).  16-bit
-//              results and residuals cross global memory as TMA boxes of 32
-//              rows by 32 columns through a warp's own two buffers (a lane
-//              has a row: plain 16-byte accesses of 32 different lines each
-//              took the load/store unit from the MMA's operand reads; 1024 x
-//              28672 x 4096 with a residual 88.9 us, with boxes 84.6).
+//   warps 2-17 epilogue in each CTA, four warps a TMEM lane quarter (each a
+//              quarter of the tile's 32-column chunks; with two, a tile with
+//              SiLU and E4M3 output took 0.8 us longer, which a product of one
+//              or two rounds shows in full).  One lane waits for the
+//              accumulator.  A tile's scales and biases are spread over the
+//              threads once and read back from shared memory (any type, any
+//              alignment, one load a column).  16-bit results and residuals
+//              cross global memory as TMA boxes of 32 rows by 32 columns
+//              through a warp's own buffer: a lane has a row, and plain 16-byte
+//              accesses of 32 different lines each took the load/store unit
+//              from the MMA's operand reads (4096 x 8192 x 28672 with a
+//              residual 1007k cycles, with boxes 949k, the plain product's).
 // Tail tiles: 256-wide tiles fill whole rounds of the SM pairs; the columns
 // left over become narrower tiles when that ends the last round sooner.
 // Few tiles: a cluster of two or four pairs shares a tile and splits its
 // k-blocks.  Each pair keeps a share of the tile's columns and sends the float
 // sums of the others to their pairs' (by then idle) stages through distributed
 // shared memory; the owner adds them in pair order, so results are the same
-// bits every time (512 x 4096 x 14336: 41.0 us without, SPL us).
+// bits every time (512 x 4096 x 14336: 41.0 us without, 29 with).
+// The producer's loop does nothing but wait, arm and load: with its addresses
+// computed in the loop the same product took 985k cycles instead of 965k.
+// Measured (GB300, replayed graphs): gate/up of 1021 tokens, 28672 x 4096, SiLU
+// and E4M3 output, 78.4 to 79.2 us (0.79 of twice the bf16 burst peak; tensor
+// pipe 68 % active), down of 4096 tokens, 8192 x 28672 with bias and residual,
+// 560 to 568 us cool (0.89; 84 %), 620 to 660 under the power cap; 4096 x 28672
+// x 4096 with a residual 299 us (330 for fp8_scaled_mm).
 // Waits are bounded; a time-out raises both CTAs' abort flags, and all CTAs of
 // a cluster meet at its barrier before TMEM is released.
 #include <atomic>

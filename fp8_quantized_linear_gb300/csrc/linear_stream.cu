@@ -14,8 +14,8 @@
 // operand, tokens the 8-column B operand; the k order inside a chunk is the
 // same permutation for both).  Nothing is staged, so the first bytes reach the
 // tensor cores one round trip after the launch: that start is where this form
-// beats the swapped tcgen05 kernel (4096 x 4096 of one token STREAM1 against
-// 7.2 us), which takes over where a product is long enough to hide its own.
+// beats the swapped tcgen05 kernel (4096 x 4096 of one token 5.1 against 7.4
+// us, 16.8 MB at 0.48 of HBM), which takes over where a product is long enough to hide its own.
 //
 // With a gate rows g are gate rows and rows g + 8 the up rows of the same
 // eight outputs: an accumulator holds both, and whole 512-byte halves of the
@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kStWarps * 32, 2) linear_stream_kernel(const S
 
 // Chunks a warp loads before it computes: four where 64 registers hold them
 // (one token tile of codes, or of packed weights without a gate), else two
-// (four spilled with a gate: 22016 x 4096 28.1 us against GP2).
+// (four spilled with a gate: 22016 x 4096 28.1 us, three 23.6,
+// against 19.0).
 template <int XDT, int NT, bool PACKED, bool GATED>
 int launch_stream(const StreamArgs &p, bool stable, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};

@@ -358,7 +358,8 @@ FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N
  * weights are streamed through the CUDA cores; above, a token is held as a
  * sum of E4M3 parts (two for bf16, three for fp16), whose products with the
  * weights are exact: what the parts leave out of a value is below 2^-21
- * (bf16) or 2^-25 (fp16) of the token's largest magnitude.  With
+ * (bf16) or 2^-25 (fp16) of the token's largest magnitude (of 2^-119, where
+ * that is more).  With
  * FP8L_KERNEL_AUTO a call without bias, activation and residual is
  * fp8_w8a16_mm.  workspace:
  * fp8_w8a16_linear_workspace_bytes() bytes for these arguments (16-byte
