@@ -156,7 +156,7 @@ PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t count) {
     const int64_t N = w.size(0), scales = w_scale.numel(), tokens = a_scale.numel();
     if (w_scale.scalar_type() != ScalarType::Float || (scales != N && scales != 1))
         value_error("w_scale is float32 with 1 or N entries");
-    const bool per_token = args[13] == Py_None ? tokens == M && M > 1 : truth(args[13]);
+    const bool per_token = args[13] == Py_None ? tokens == M && M != 1 : truth(args[13]);
     if (a_scale.scalar_type() != ScalarType::Float || tokens != (per_token ? M : 1))
         value_error("a_scale is float32 with 1 entry, or M with per_token");
     if (per_token) flags |= FP8L_A_PER_TOKEN;

@@ -106,7 +106,8 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     using namespace fp8l;
     if (out_dtype != FP8L_F16 && out_dtype != FP8L_BF16 && out_dtype != FP8L_E4M3) return FP8L_EINVAL;
     if ((flags & ~(FP8L_WEIGHTS_STABLE | FP8L_A_PER_TOKEN | FP8L_KERNEL_MASK)) != 0u) return FP8L_EINVAL;
-    if (a_scale == nullptr || w_scale == nullptr || w == nullptr) return FP8L_EINVAL;
+    const int pt = (flags & FP8L_A_PER_TOKEN) != 0u ? 1 : 0, pc = w_per_channel ? 1 : 0;
+    if ((a_scale == nullptr && !(pt && M == 0)) || w_scale == nullptr || w == nullptr) return FP8L_EINVAL;
     if (out_dtype == FP8L_E4M3 && out_scale == nullptr) return FP8L_EINVAL;
     LinearCall c{};
     int st = check_epilogue(M, N, K, bias, bias_dtype, activation, residual, out_scale, y, out_dtype,
@@ -116,10 +117,12 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     if (!aligned16(w) || !aligned16(workspace) || (M > 0 && !aligned16(a)) || misaligned(a_scale, 4) ||
         misaligned(w_scale, 4) || (out_dtype == FP8L_E4M3 && misaligned(out_scale, 4)))
         return FP8L_EALIGN;
-    const int pt = (flags & FP8L_A_PER_TOKEN) != 0u ? 1 : 0, pc = w_per_channel ? 1 : 0;
     st = check_output(c.e, M, N, a, static_cast<size_t>(M) * K, w, static_cast<size_t>(N) * K, a_scale,
                       pt ? M : 1, w_scale, pc ? N : 1);
     if (st != FP8L_OK) return st;
+    if (overlap(y, static_cast<size_t>(M) * c.e.width * (out_dtype == FP8L_E4M3 ? 1 : 2), workspace,
+                workspace != nullptr ? kWorkspaceBytes : 0))
+        return FP8L_EINVAL;
     st = check_device(&c.sms);
     if (st != FP8L_OK) return st;
     if (M == 0) return FP8L_OK;

@@ -386,6 +386,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
+            pdl_wait();  // (the waits below are limited, the preceding kernel's time is not)
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;

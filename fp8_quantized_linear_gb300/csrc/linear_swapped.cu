@@ -295,6 +295,8 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
+            // (the waits below are limited, the preceding kernel's time is not)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             // kind::f8f6f4, D f32, A and B E4M3 K-major, N = parts * T, M = 128
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(cols >> 3) << 17) |
                                    (static_cast<uint32_t>(LS_BM >> 4) << 24);
@@ -329,7 +331,8 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
             // other warps meet this one at a barrier instead of polling for it
             // (polling warps take issue slots from the two that feed the MMAs)
             mma_commit(done_bar);
-            mbar_wait(done_bar, 0, abort_flag, p.status, p.wait_cycles);
+            if (!mbar_wait(done_bar, 0, abort_flag, p.status, p.wait_cycles))
+                mbar_wait_drain(done_bar, 0, p.status);  // none in flight when the CTA exits
             tc_fence_before();
         }
         __syncwarp();
@@ -646,7 +649,9 @@ split_tokens_kernel(const uint4 *x, int K, int T, uint8_t *codes, float *scale) 
     int e = amax > 0.0f ? 7 - ilogbf(amax) : 0;
     e = e > 126 ? 126 : (e < -126 ? -126 : e);
     const float up = __int_as_float((e + 127) << 23);
-    if (blockIdx.y == 0 && threadIdx.x == 0) scale[m] = __int_as_float((127 - e) << 23);
+    // (codes are finite: a row with a value that is not has NaN as its scale)
+    if (blockIdx.y == 0 && threadIdx.x == 0)
+        scale[m] = amax <= 3.4e38f ? __int_as_float((127 - e) << 23) : __int_as_float(0x7FC00000);
     if (mine >= words) return;
     const uint32_t w4[4] = {own.x, own.y, own.z, own.w};
     float f[8];

@@ -132,6 +132,8 @@ def test_no_tokens():
     y = fl.fp8_linear(a[:0], w, sa, sw, activation="relu", gated=True)
     assert y.shape == (0, 32)
     assert fl.fp8_linear(a[:0], w, sa, sw).shape == (0, 64)
+    assert fl.fp8_linear(a[:0], w, sa[:0], sw, activation="relu").shape == (0, 64)
+    assert fl.fp8_linear(a[:0], w, sa[:0], sw, activation="relu", per_token=True).shape == (0, 64)
     x = torch.empty(0, 64, dtype=HF, device=DEV)
     assert fl.fp8_w8a16_linear(x, w, sw, activation="relu").shape == (0, 64)
 
@@ -150,6 +152,59 @@ def test_rows_behind_the_batch_stay():
         fl.fp8_add_rmsnorm_quant(x, x, torch.ones(512, dtype=BF, device=DEV), mode="norm_only",
                                  h=rows[:M])
         assert (rows[M:] == 7).all()
+
+
+@pytest.mark.parametrize("kernel", ["stream", "swapped", "tiled"])
+def test_rows_behind_the_batch_stay_in_every_kernel(kernel):
+    os = torch.ones(1, device=DEV)
+    for M in (1, 37, 300):
+        gen, a, w, sa, sw = operands(M, M, 320, 512)
+        r = torch.randn(M, 320, generator=gen, device=DEV).to(BF)
+        for dtype, kw in ((BF, dict(residual=r)), (U8, dict(out_scale=os))):
+            big = torch.full((M + 300, 320), 7, dtype=dtype, device=DEV)
+            fl.fp8_linear(a, w, sa, sw, bias=r[0].contiguous(), y=big[:M], kernel=kernel, **kw)
+            assert (big[M:] == 7).all()
+
+
+def test_values_that_are_not_finite_show():
+    """W8A16: a token with an infinity or a NaN has no finite result, whatever
+    the kernel, and the others are what they are without it."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    w = normal_codes(gen, 96, 256)
+    sw = torch.full((96,), 2.0 ** -12, device=DEV)
+    for dtype in (BF, HF):
+        x = torch.randn(24, 256, generator=gen, device=DEV).to(dtype)
+        bad = x.clone()
+        bad[3, 7], bad[11, 200], bad[20, 0] = float("inf"), float("nan"), float("-inf")
+        rows = [i for i in range(24) if i not in (3, 11, 20)]
+        for kernel in ("stream", "swapped"):
+            want = fl.fp8_w8a16_linear(x, w, sw, activation="silu", kernel=kernel)
+            got = fl.fp8_w8a16_linear(bad, w, sw, activation="silu", kernel=kernel)
+            assert torch.equal(got[rows], want[rows])
+            # (silu of minus infinity is 0 times infinity, of infinity infinity)
+            assert not torch.isfinite(got[[3, 11, 20]]).any()
+
+
+def test_a_long_call_before_is_no_time_out():
+    """A dependent that is resident early does not count the preceding kernel's
+    time: the waits limited to 0.13 ms, behind a call of about half a millisecond
+    that leaves SMs free."""
+    K = 1 << 20
+    long_a = torch.zeros(1, K, dtype=U8, device=DEV)
+    long_w = torch.zeros(2048, K, dtype=U8, device=DEV)
+    one = torch.ones(1, device=DEV)
+    gen, a, w, sa, sw = operands(5, 40, 512, 256)
+    want = {k: fl.fp8_linear(a, w, sa, sw, activation="silu", kernel=k) for k in ("swapped", "tiled")}
+    fl.fp8l_debug_waits(wait_cycles=1 << 18)
+    try:
+        for k in ("swapped", "tiled"):
+            fl.fp8_linear(long_a, long_w, one, one, activation="relu", kernel="stream",
+                          stable_weights=True)
+            got = fl.fp8_linear(a, w, sa, sw, activation="silu", kernel=k, stable_weights=True)
+            assert torch.equal(got, want[k])
+            assert_status_ok()
+    finally:
+        fl.fp8l_debug_waits()
 
 
 def test_codes_as_float8_and_offsets():

@@ -56,6 +56,7 @@ def test_linear_output_over_inputs(lib):
     for name in ("a", "w", "sa", "sw", "bias"):
         assert linear(lib, **{name: y}) == b.EINVAL, name
     assert linear(lib, res=y - 16) == b.EINVAL
+    assert linear(lib, ws=y + 32) == b.EINVAL
     assert linear(lib, res=None, out=b.E4M3, os=y + 4) == b.EINVAL
     # (adjacent buffers and the residual itself pass on to the device check)
     past = (b.ECUDA, b.EUNSUPPORTED)
