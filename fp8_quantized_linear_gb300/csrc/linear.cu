@@ -69,17 +69,18 @@ int check_output(const Epilogue &e, int64_t M, int64_t N, const void *x, size_t 
 // over rotating operands, us):
 //   - weights streamed through registers for a few tokens and small weights,
 //     whose time is the start of the kernel (M = 1 at 4096 x 4096 5.1 against
-//     7.4 swapped, M = 8 at 4096 x 11008 10.8 against 11.6; but M = 1 at 10240
-//     x 8192 19.2 against 17.6, M = 16 at 6144 x 4096 11.3 against 9.6);
+//     7.4 swapped, M = 8 at 8192 x 4096 9.5 against 9.9; but M = 8 at 5120 x
+//     8192 12.5 against 11.1, M = 1 at 6144 x 6144 gated 11.7 against 10.6, M =
+//     16 at 6144 x 4096 11.3 against 9.5); up to 4096 weight rows all CTAs run
+//     at once and it pays for longer (M = 8 at 4096 x 11008 10.6 against 11.6);
 //   - swapped operands up to 128 tokens, and beyond while tokens x weight rows
-//     stay below 2^20, too few 256 x 256 tiles for the SM pairs (M = 144 at
-//     6144 x 4096 13.3 against 14.6 tiled, M = 200 at 6144 x 4096 16.2 against
-//     14.9, M = 128 at 28672 x 4096 32.7 against 32.5);
+//     stay below 2^20, too few 256 x 256 tiles for the SM pairs (M = 256 at
+//     4096 x 4096 13.5 against 14.3 tiled, M = 192 at 11008 x 4096 21.3 against
+//     17.6, M = 128 at 28672 x 4096 31.1 against 32.7);
 //   - tiles over SM pairs otherwise.
 unsigned choose_linear(int64_t M, int64_t N, int64_t K) {
-    const int64_t wbytes = N * K;
-    if ((M <= 8 && wbytes <= (int64_t(48) << 20)) || (M <= 16 && wbytes <= (int64_t(16) << 20)))
-        return FP8L_KERNEL_STREAM;
+    const int64_t wbytes = N * K, few = int64_t(N <= 4096 ? 48 : 32) << 20;
+    if ((M <= 8 && wbytes <= few) || (M <= 16 && wbytes <= (int64_t(16) << 20))) return FP8L_KERNEL_STREAM;
     return M > 128 && M * N > (1 << 20) ? FP8L_KERNEL_TILED : FP8L_KERNEL_SWAPPED;
 }
 

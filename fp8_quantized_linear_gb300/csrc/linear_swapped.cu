@@ -44,13 +44,17 @@
 // distributed shared memory in a fixed order.  Every wait is bounded.
 //
 // Measured (GB300, replayed graphs over rotating weights; of the copy
-// bandwidth): gate/up of 16 tokens, 28672 x 4096 with E4M3 output, 22.9 us, 0.76
-// (DRAM reads the weights once); 4096 x 14336 of 16 tokens 14.4 us, 0.60;
-// W8A16 4096 x 11008 of 16 tokens 14.0 us, 0.48 (17.6 through fp8_w8a16_mm,
-// without the addition), 11008 x 4096 of 47 fp16 tokens 17.4 us.  Short
+// bandwidth): gate/up of 16 tokens, 28672 x 4096 with E4M3 output, 22.6 us, 0.77
+// (DRAM reads the weights once), of 128 tokens 29.0 us; 4096 x 14336 of 16
+// tokens 14.4 us, 0.60; W8A16 4096 x 11008 of 16 tokens 14.1 us, 0.48 (17.6
+// through fp8_w8a16_mm, without the addition), 11008 x 4096 of 47 fp16 tokens
+// 17.1 us.  Short
 // streams are bound by their ends: launch, first bytes, the cluster's sums.
-// Tried: 256 threads (27.2 us for the 22.9: the second CTA's start), three
-// CTAs of 75 KB an SM (23.3), one of 112 KB (23.2; 4096 x 14336 15.0).
+// Tried (16 tokens of 28672 x 4096 at 22.9 us): 256 threads (27.2: the second
+// CTA's start), three CTAs of 75 KB an SM (23.3), one of 112 KB (23.2; 4096 x
+// 14336 15.0); at 128 tokens of 28672 x 4096 (33.5 us then), pairs of SMs that
+// share the tokens (33.5; a few tokens 5 to 10 % slower), rings of their own for
+// weights and tokens (37.6).
 #include <atomic>
 
 #include "linear_launch.cuh"
@@ -68,7 +72,7 @@ constexpr int kLsWBytes = LS_BM * LS_BK;
 constexpr int kLsMaxStages = 16;
 constexpr int kLsMaxSplit = 8;        // portable cluster size
 constexpr int kLsPitch = LS_BM + 4;   // floats a token row of the float tile
-constexpr int kLsBatch = 4;           // epilogue items in flight a thread
+constexpr int kLsBatch = 4;           // epilogue items a thread takes together, where it has so many
 // two CTAs per SM: 233472 bytes of shared memory per SM, 1024 reserved per CTA
 constexpr size_t kLsSmem = 112 * 1024;
 
@@ -146,12 +150,13 @@ __device__ __forceinline__ void st_shared_float(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// (no memory clobber: the float tile does not change between the barriers
+// around its reads, which may pass the results' stores)
 __device__ __forceinline__ float4 ld_shared_float4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
 }
 
@@ -161,26 +166,39 @@ __device__ __forceinline__ uint2 ld_global_uint2(const void *p) {
     return v;
 }
 
-// Four columns of the float tile, the cluster's partials added in rank order.
-__device__ __forceinline__ float4 ls_sum(uint32_t off, int split) {
-    if (split == 1) return ld_shared_float4(off);
-    float4 part[kLsMaxSplit];
+// Four columns of the float tile for each of B items (from another CTA: for
+// the first `valid` of them), the cluster's partials added in rank order.
+template <int B>
+__device__ __forceinline__ void ls_sums(const uint32_t (&off)[B], int valid, uint32_t shift, int split,
+                                        float (&v)[4 * B]) {
 #pragma unroll
-    for (int q = 0; q < kLsMaxSplit; ++q)
-        if (q < split) part[q] = ld_cluster_v4(off, static_cast<uint32_t>(q));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < B; ++u) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (split == 1) {
+            a = ld_shared_float4(off[u] + shift);
+        } else if (u < valid) {
+            float4 part[kLsMaxSplit];
 #pragma unroll
-    for (int q = 0; q < kLsMaxSplit; ++q) {
-        if (q < split) {
-            acc.x += part[q].x;
-            acc.y += part[q].y;
-            acc.z += part[q].z;
-            acc.w += part[q].w;
+            for (int q = 0; q < kLsMaxSplit; ++q)
+                if (q < split) part[q] = ld_cluster_v4(off[u] + shift, static_cast<uint32_t>(q));
+#pragma unroll
+            for (int q = 0; q < kLsMaxSplit; ++q) {
+                if (q < split) {
+                    a.x += part[q].x;
+                    a.y += part[q].y;
+                    a.z += part[q].z;
+                    a.w += part[q].w;
+                }
+            }
         }
+        v[4 * u] = a.x;
+        v[4 * u + 1] = a.y;
+        v[4 * u + 2] = a.z;
+        v[4 * u + 3] = a.w;
     }
-    return acc;
 }
 
+template <int B>  // epilogue items a thread takes together
 __global__ void __launch_bounds__(kLsThreads, 2)
 linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
                       const __grid_constant__ CUtensorMap tmap_x, const SwappedArgs p) {
@@ -199,6 +217,7 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
     const uint32_t done_bar = bar0 + 8u * (2 * S);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + ring_bytes + (2 * S + 1) * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *sa_sh = reinterpret_cast<float *>(tmem_slot + 2);  // [T]: the tokens' scales
     const int cols = p.parts * p.T;
     const uint32_t tmem_cols = cols <= 32 ? 32u : (cols <= 64 ? 64u : (cols <= 128 ? 128u : 256u));
 
@@ -365,29 +384,26 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
         }
     }
     const OutScale os = OutScale::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
-    // scale and residual of a batch of items, loaded while the batch before is
-    // computed (the first while the stream runs)
+    for (int t = threadIdx.x; t < rows; t += kLsThreads)
+        sa_sh[t] = epi_ld_f32(p.token_scale + (p.per_token ? m0 + t : 0));
+    // residuals of a batch of items, loaded two batches ahead
     struct Batch {
-        uint2 res[kLsBatch];
-        float sa[kLsBatch];
+        uint2 res[B];
     };
     auto load_batch = [&](int i) {
         Batch b;
 #pragma unroll
-        for (int u = 0; u < kLsBatch; ++u) {
+        for (int u = 0; u < B; ++u) {
             const int it = i + u * kLsThreads;
             b.res[u] = make_uint2(0, 0);
-            b.sa[u] = 0.0f;
-            if (!in || it >= i1) continue;
-            const int m = m0 + (it >> gshift);
-            b.sa[u] = epi_ld_f32(p.token_scale + (p.per_token ? m : 0));
-            if (p.e.residual != nullptr)
+            if (p.e.residual != nullptr && in && it < i1)
                 b.res[u] = ld_global_uint2(static_cast<const uint16_t *>(p.e.residual) +
-                                           static_cast<size_t>(m) * p.e.width + n);
+                                           static_cast<size_t>(m0 + (it >> gshift)) * p.e.width + n);
         }
         return b;
     };
-    Batch next = load_batch(first);
+    constexpr int kStep = B * kLsThreads;
+    Batch next = load_batch(first), after = load_batch(first + kStep);
 
     __syncthreads();
     tc_fence_after();
@@ -424,39 +440,62 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
         __syncthreads();
     ok = !*abort_flag;
 
-    for (int i = first; ok && i < i1; i += kLsBatch * kLsThreads) {
+    // a batch's items (i, i + kLsThreads, ...) in stages, so that the branches
+    // on what the epilogue does are taken once for all of them: one item after
+    // the other took 500 cycles each (128 tokens of 28672 x 128 12.7 us, 7.7 in
+    // fours; of 28672 x 4096 33.4 and 30.8)
+    for (int i = first; ok && in && i < i1; i += kStep) {
         const Batch cur = next;
-        if (i + kLsBatch * kLsThreads < i1) next = load_batch(i + kLsBatch * kLsThreads);
+        next = after;
+        if (p.e.residual != nullptr) after = load_batch(i + 2 * kStep);
+        uint32_t off[B];
+        float sa[B], v[4 * B];
 #pragma unroll
-        for (int u = 0; u < kLsBatch; ++u) {
-            const int it = i + u * kLsThreads;
-            if (!in || it >= i1) break;
-            const int t = it >> gshift;
-            const uint32_t off = sbase + static_cast<uint32_t>((t * kLsPitch + c4) * 4);
-            const float4 acc = ls_sum(off, split);
-            float v[4] = {fmaf(acc.x, cur.sa[u] * sw[0], bias[0]), fmaf(acc.y, cur.sa[u] * sw[1], bias[1]),
-                          fmaf(acc.z, cur.sa[u] * sw[2], bias[2]), fmaf(acc.w, cur.sa[u] * sw[3], bias[3])};
-            activate(v, p.e.act);
-            if (p.gated) {
-                const float4 up = ls_sum(off + LS_BM / 2 * 4, split);
-                v[0] *= fmaf(up.x, cur.sa[u] * sw_up[0], bias_up[0]);
-                v[1] *= fmaf(up.y, cur.sa[u] * sw_up[1], bias_up[1]);
-                v[2] *= fmaf(up.z, cur.sa[u] * sw_up[2], bias_up[2]);
-                v[3] *= fmaf(up.w, cur.sa[u] * sw_up[3], bias_up[3]);
+        for (int u = 0; u < B; ++u) {
+            const int it = i + u * kLsThreads < i1 ? i + u * kLsThreads : i;  // (beyond the last: any)
+            off[u] = sbase + static_cast<uint32_t>(((it >> gshift) * kLsPitch + c4) * 4);
+            sa[u] = sa_sh[it >> gshift];
+        }
+        const int valid = (i1 - i + kLsThreads - 1) / kLsThreads;
+        ls_sums(off, valid, 0, split, v);
+#pragma unroll
+        for (int j = 0; j < 4 * B; ++j) v[j] = fmaf(v[j], sa[j / 4] * sw[j % 4], bias[j % 4]);
+        activate(v, p.e.act);
+        if (p.gated) {
+            float up[4 * B];
+            ls_sums(off, valid, LS_BM / 2 * 4, split, up);
+#pragma unroll
+            for (int j = 0; j < 4 * B; ++j) v[j] *= fmaf(up[j], sa[j / 4] * sw_up[j % 4], bias_up[j % 4]);
+        }
+        const size_t o0 = static_cast<size_t>(m0) * p.e.width + n;
+        if (p.e.out_dtype == FP8L_E4M3) {
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                const int it = i + u * kLsThreads;
+                const uint32_t c = os.codes(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+                if (it < i1)
+                    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.e.y) + o0 +
+                                                  static_cast<size_t>(it >> gshift) * p.e.width) = c;
             }
-            const size_t o = static_cast<size_t>(m0 + t) * p.e.width + n;
-            if (p.e.out_dtype == FP8L_E4M3) {
-                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.e.y) + o) = os.codes(v[0], v[1], v[2], v[3]);
-            } else {
-                if (p.e.residual != nullptr) {
+        } else {
+            if (p.e.residual != nullptr) {
+#pragma unroll
+                for (int u = 0; u < B; ++u) {
                     const float2 a = widen_pair(cur.res[u].x, p.e.out_dtype), b = widen_pair(cur.res[u].y, p.e.out_dtype);
-                    v[0] += a.x;
-                    v[1] += a.y;
-                    v[2] += b.x;
-                    v[3] += b.y;
+                    v[4 * u] += a.x;
+                    v[4 * u + 1] += a.y;
+                    v[4 * u + 2] += b.x;
+                    v[4 * u + 3] += b.y;
                 }
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.y) + o) =
-                    make_uint2(pack_out16(v[0], v[1], p.e.out_dtype), pack_out16(v[2], v[3], p.e.out_dtype));
+            }
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                const int it = i + u * kLsThreads;
+                const uint2 w = make_uint2(pack_out16(v[4 * u], v[4 * u + 1], p.e.out_dtype),
+                                           pack_out16(v[4 * u + 2], v[4 * u + 3], p.e.out_dtype));
+                if (it < i1)
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.y) + o0 +
+                                               static_cast<size_t>(it >> gshift) * p.e.width) = w;
             }
         }
     }
@@ -486,11 +525,13 @@ std::atomic<int> g_ls_clusters[kLsMaxDevices][kLsSmem / 1024 + 1][kLsMaxSplit + 
 int ls_prepare(int dev) {
     if (g_ls_smem_per_sm[dev].load(std::memory_order_acquire) > 0) return FP8L_OK;
     int per_sm = 0, reserved = 0;
-    if (cudaFuncSetAttribute(linear_swapped_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kLsSmem)) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_swapped_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_swapped_twin, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (const auto kernel : {linear_swapped_kernel<1>, linear_swapped_kernel<kLsBatch>})
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLsSmem)) !=
+                cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+            return FP8L_ECUDA;
+    if (cudaFuncSetAttribute(linear_swapped_twin, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kLsSmem)) != cudaSuccess ||
         cudaFuncSetAttribute(linear_swapped_twin, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
@@ -540,10 +581,10 @@ int launch_linear_swapped(const LinearCall &c, int parts, const float *token_sca
     if (int64_t(p.m_tiles) * cols > 0x7FFFFFFF) return FP8L_ESHAPE;  // rows of the parts
     p.stage_bytes = kLsWBytes + cols * LS_BK;
     // the most stages that fit; the float tile reuses the ring
-    int stages = static_cast<int>((kLsSmem - 1024 - 24) / (p.stage_bytes + 16));
+    int stages = static_cast<int>((kLsSmem - 1024 - 24 - 4 * p.T) / (p.stage_bytes + 16));
     if (stages > kLsMaxStages) stages = kLsMaxStages;
     p.stages = stages;
-    const size_t smem = 1024 + size_t(stages) * p.stage_bytes + size_t(2 * stages + 1) * 8 + 16;
+    const size_t smem = 1024 + size_t(stages) * p.stage_bytes + size_t(2 * stages + 1) * 8 + 16 + 4 * size_t(p.T);
     if (stages < 2 || smem > kLsSmem || size_t(p.T) * kLsPitch * 4 > size_t(stages) * p.stage_bytes)
         return FP8L_ESHAPE;
     p.num_k_blocks = (c.K + LS_BK - 1) / LS_BK;
@@ -606,7 +647,12 @@ int launch_linear_swapped(const LinearCall &c, int parts, const float *token_sca
     }
     cfg.attrs = attr;
     cfg.numAttrs = nattr;
-    if (cudaLaunchKernelEx(&cfg, linear_swapped_kernel, mw, mx, p) != cudaSuccess) return FP8L_ECUDA;
+    // items a CTA of a full tile (see the kernel) has: taken in fours where a
+    // thread has more than two, else one by one (4096 x 4096 of one token, split
+    // eight ways, 7.4 us, 7.8 in fours)
+    const int items = (c.M < p.T ? c.M : p.T) * (span / 4) / split;
+    const auto kernel = items > 2 * kLsThreads ? linear_swapped_kernel<kLsBatch> : linear_swapped_kernel<1>;
+    if (cudaLaunchKernelEx(&cfg, kernel, mw, mx, p) != cudaSuccess) return FP8L_ECUDA;
     return launch_status();
 }
 
