@@ -73,27 +73,43 @@ int check_output(const Epilogue &e, int64_t M, int64_t N, const void *x, size_t 
 //     8192 12.5 against 11.1, M = 1 at 6144 x 6144 gated 11.7 against 10.6, M =
 //     16 at 6144 x 4096 11.3 against 9.5); up to 4096 weight rows all CTAs run
 //     at once and it pays for longer (M = 8 at 4096 x 11008 10.6 against 11.6);
+//     a CTA reads its rows whole, so not where they are long (M = 8 at 2048 x
+//     22016 15.4 against 12.9, x 12288 9.4 against 9.8; M = 16 at 1024 x 8192
+//     9.0 against 6.7, x 4096 4.4 against 5.7);
 //   - swapped operands up to 128 tokens, and beyond while tokens x weight rows
 //     stay below 2^20, too few 256 x 256 tiles for the SM pairs (M = 256 at
 //     4096 x 4096 13.5 against 14.3 tiled, M = 192 at 11008 x 4096 21.3 against
 //     17.6, M = 128 at 28672 x 4096 31.1 against 32.7);
+//   - swapped operands, too, where the 256 x 256 tiles begin a second round
+//     over the pairs and two CTAs an SM hold all 128 x 128 tiles (M = 333 at
+//     11008 x 4096 22.9 against 26.9 tiled, at 12288 x 12288 53 against 70; M =
+//     400, a second wave, 39.6 against 27.3), if rows of K fill their 128-byte
+//     lines (K = 4112 33.4 against 29.4: each box row takes two lines, and
+//     smaller tiles load more of them);
 //   - tiles over SM pairs otherwise.
-unsigned choose_linear(int64_t M, int64_t N, int64_t K) {
+unsigned choose_linear(int64_t M, int64_t N, int64_t K, int sms) {
     const int64_t wbytes = N * K, few = int64_t(N <= 4096 ? 48 : 32) << 20;
-    if ((M <= 8 && wbytes <= few) || (M <= 16 && wbytes <= (int64_t(16) << 20))) return FP8L_KERNEL_STREAM;
-    return M > 128 && M * N > (1 << 20) ? FP8L_KERNEL_TILED : FP8L_KERNEL_SWAPPED;
+    if (M <= 8 ? wbytes <= few && K < 16384 : M <= 16 && wbytes <= (int64_t(16) << 20) && K <= 4096)
+        return FP8L_KERNEL_STREAM;
+    if (M <= 128 || M * N <= (1 << 20)) return FP8L_KERNEL_SWAPPED;
+    const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
+    const int64_t swapped_tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    return K % 128 == 0 && pair_tiles > sms / 2 && swapped_tiles <= 2 * int64_t(sms) ? FP8L_KERNEL_SWAPPED
+                                                                                      : FP8L_KERNEL_TILED;
 }
 
 // The kernel of fp8_w8a16_linear: weights streamed through registers for a few
 // tokens (M = 1 at 12288 x 4096, packed, 11.2 us against 13.1 swapped; M = 8 at
-// 28672 x 8192 44.2 against 41.7; M = 16 at 4096 x 4096 6.8 against 9.5), else
-// tokens in parts through the swapped-operand kernel (M = 16 at 4096 x 11008
-// 14.0 against 14.1 to 18.2, at 22016 x 4096 gated 20.6 against 25.0; M = 32 at
-// 4096 x 11008 15.7 against 26.6).
+// 28672 x 8192 44.2 against 41.7; M = 16 at 4096 x 4096 6.8 against 9.5, at 2048
+// x 6144 8.0 against 9.2, but at 2048 x 12288 13.4 against 11.7), else tokens in
+// parts through the swapped-operand kernel (M = 16 at 4096 x 11008 14.0 against
+// 14.1 to 18.2, at 22016 x 4096 gated 20.6 against 25.0; M = 32 at 4096 x 11008
+// 15.7 against 26.6).
 unsigned choose_w8a16_linear(int64_t M, int64_t N, int64_t K, unsigned flags) {
     const unsigned k = flags & FP8L_KERNEL_MASK;
     if (k != FP8L_KERNEL_AUTO) return k;
-    return M <= 8 || (M <= 16 && N * K <= (int64_t(32) << 20)) ? FP8L_KERNEL_STREAM : FP8L_KERNEL_SWAPPED;
+    return M <= 8 || (M <= 16 && N * K <= (int64_t(32) << 20) && K <= 8192) ? FP8L_KERNEL_STREAM
+                                                                            : FP8L_KERNEL_SWAPPED;
 }
 
 }  // namespace
@@ -149,7 +165,7 @@ extern "C" int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t
     c.status = status_word(workspace);
     c.stable = (flags & FP8L_WEIGHTS_STABLE) != 0u;
     c.stream = as_stream(stream);
-    const unsigned kernel = choice != FP8L_KERNEL_AUTO ? choice : choose_linear(M, N, K);
+    const unsigned kernel = choice != FP8L_KERNEL_AUTO ? choice : choose_linear(M, N, K, c.sms);
     if (kernel == FP8L_KERNEL_STREAM) return launch_linear_stream(c);
     if (kernel == FP8L_KERNEL_TILED) return launch_linear_pair(c);
     return launch_linear_swapped(c, 1, a_scale);

@@ -45,7 +45,7 @@
 //
 // Measured (GB300, replayed graphs over rotating weights; of the copy
 // bandwidth): gate/up of 16 tokens, 28672 x 4096 with E4M3 output, 22.6 us, 0.77
-// (DRAM reads the weights once), of 128 tokens 29.0 us; 4096 x 14336 of 16
+// (DRAM reads the weights once), of 128 tokens 28.6 us; 4096 x 14336 of 16
 // tokens 14.4 us, 0.60; W8A16 4096 x 11008 of 16 tokens 14.1 us, 0.48 (17.6
 // through fp8_w8a16_mm, without the addition), 11008 x 4096 of 47 fp16 tokens
 // 17.1 us.  Short
@@ -386,24 +386,32 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
     const OutScale os = OutScale::make(p.e.out_dtype == FP8L_E4M3 ? epi_ld_f32(p.e.out_scale) : 1.0f);
     for (int t = threadIdx.x; t < rows; t += kLsThreads)
         sa_sh[t] = epi_ld_f32(p.token_scale + (p.per_token ? m0 + t : 0));
+    // from one of a thread's items to the next: tokens, bytes of y
+    const int t0 = first >> gshift, t_step = kLsThreads >> gshift;
+    const int es = p.e.out_dtype == FP8L_E4M3 ? 1 : 2;
+    const size_t y_step = static_cast<size_t>(t_step) * p.e.width * es;
+    const size_t y0 = (static_cast<size_t>(m0 + t0) * p.e.width + n) * es;
     // residuals of a batch of items, loaded two batches ahead
     struct Batch {
         uint2 res[B];
     };
+    const uint8_t *r_next = static_cast<const uint8_t *>(p.e.residual) + y0;  // (16-bit output)
     auto load_batch = [&](int i) {
         Batch b;
 #pragma unroll
         for (int u = 0; u < B; ++u) {
-            const int it = i + u * kLsThreads;
             b.res[u] = make_uint2(0, 0);
-            if (p.e.residual != nullptr && in && it < i1)
-                b.res[u] = ld_global_uint2(static_cast<const uint16_t *>(p.e.residual) +
-                                           static_cast<size_t>(m0 + (it >> gshift)) * p.e.width + n);
+            if (in && i + u * kLsThreads < i1) b.res[u] = ld_global_uint2(r_next);
+            r_next += y_step;
         }
         return b;
     };
     constexpr int kStep = B * kLsThreads;
-    Batch next = load_batch(first), after = load_batch(first + kStep);
+    Batch next{}, after{};
+    if (p.e.residual != nullptr) {
+        next = load_batch(first);
+        after = load_batch(first + kStep);
+    }
 
     __syncthreads();
     tc_fence_after();
@@ -442,8 +450,12 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
 
     // a batch's items (i, i + kLsThreads, ...) in stages, so that the branches
     // on what the epilogue does are taken once for all of them: one item after
-    // the other took 500 cycles each (128 tokens of 28672 x 128 12.7 us, 7.7 in
-    // fours; of 28672 x 4096 33.4 and 30.8)
+    // the other took 500 cycles each (128 tokens of 28672 x 128 12.7 us, 7.2 in
+    // fours; of 28672 x 4096 33.4 and 30.5)
+    uint32_t at = sbase + static_cast<uint32_t>((t0 * kLsPitch + c4) * 4);
+    const uint32_t at_step = static_cast<uint32_t>(t_step * kLsPitch * 4);
+    const float *scale = sa_sh + t0;
+    uint8_t *y = static_cast<uint8_t *>(p.e.y) + y0;
     for (int i = first; ok && in && i < i1; i += kStep) {
         const Batch cur = next;
         next = after;
@@ -452,10 +464,12 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
         float sa[B], v[4 * B];
 #pragma unroll
         for (int u = 0; u < B; ++u) {
-            const int it = i + u * kLsThreads < i1 ? i + u * kLsThreads : i;  // (beyond the last: any)
-            off[u] = sbase + static_cast<uint32_t>(((it >> gshift) * kLsPitch + c4) * 4);
-            sa[u] = sa_sh[it >> gshift];
+            const bool valid = i + u * kLsThreads < i1;  // (else the first once more)
+            off[u] = valid ? at + u * at_step : at;
+            sa[u] = scale[valid ? u * t_step : 0];
         }
+        at += B * at_step;
+        scale += B * t_step;
         const int valid = (i1 - i + kLsThreads - 1) / kLsThreads;
         ls_sums(off, valid, 0, split, v);
 #pragma unroll
@@ -467,15 +481,12 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
 #pragma unroll
             for (int j = 0; j < 4 * B; ++j) v[j] *= fmaf(up[j], sa[j / 4] * sw_up[j % 4], bias_up[j % 4]);
         }
-        const size_t o0 = static_cast<size_t>(m0) * p.e.width + n;
         if (p.e.out_dtype == FP8L_E4M3) {
 #pragma unroll
             for (int u = 0; u < B; ++u) {
-                const int it = i + u * kLsThreads;
                 const uint32_t c = os.codes(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-                if (it < i1)
-                    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.e.y) + o0 +
-                                                  static_cast<size_t>(it >> gshift) * p.e.width) = c;
+                if (i + u * kLsThreads < i1) *reinterpret_cast<uint32_t *>(y) = c;
+                y += y_step;
             }
         } else {
             if (p.e.residual != nullptr) {
@@ -488,14 +499,15 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
                     v[4 * u + 3] += b.y;
                 }
             }
+            uint2 w[B];
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                w[u] = make_uint2(pack_out16(v[4 * u], v[4 * u + 1], p.e.out_dtype),
+                                  pack_out16(v[4 * u + 2], v[4 * u + 3], p.e.out_dtype));
 #pragma unroll
             for (int u = 0; u < B; ++u) {
-                const int it = i + u * kLsThreads;
-                const uint2 w = make_uint2(pack_out16(v[4 * u], v[4 * u + 1], p.e.out_dtype),
-                                           pack_out16(v[4 * u + 2], v[4 * u + 3], p.e.out_dtype));
-                if (it < i1)
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.e.y) + o0 +
-                                               static_cast<size_t>(it >> gshift) * p.e.width) = w;
+                if (i + u * kLsThreads < i1) *reinterpret_cast<uint2 *>(y) = w[u];
+                y += y_step;
             }
         }
     }

@@ -109,6 +109,17 @@ def test_large(M, N, K):
         check_linear(M, M, N, K, activation="silu", gated=True, out=U8, stable_weights=True)
 
 
+# sizes on both sides of each change of kernel
+@pytest.mark.parametrize("M,N,K", [(8, 4096, 12288), (8, 4128, 8192), (8, 512, 16384), (8, 512, 16368),
+                                   (16, 512, 4096), (16, 512, 4112), (16, 4160, 4096), (128, 12288, 128),
+                                   (129, 12288, 128), (333, 11008, 256), (333, 11008, 272),
+                                   (400, 11008, 256), (260, 9728, 128), (260, 9760, 128), (256, 4096, 256),
+                                   (257, 4096, 256)])
+def test_changes_of_kernel(M, N, K):
+    check_linear(M, M, N, K, bias=BF, residual=True, per_token=True, stable_weights=True)
+    check_linear(M, M, N, K, activation="silu", gated=True, out=U8, stable_weights=True)
+
+
 # every kernel over sizes on both sides of its own choices: token tiles, K split
 # over clusters of CTAs and of pairs (few tiles, long K), tail tiles
 @pytest.mark.parametrize("kernel", ["stream", "swapped", "tiled"])
@@ -275,6 +286,13 @@ def test_w8a16_large(M, N, K):
         check_w8a16(M, M, N, K, HF, residual=True, packed=packed, stable_weights=True)
         check_w8a16(M, M, N, K, BF, activation="silu", gated=True, packed=packed,
                     stable_weights=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 512, 22016), (9, 4096, 8192), (9, 4128, 8192), (16, 512, 8192),
+                                   (16, 512, 8208), (17, 512, 4096)])
+def test_w8a16_changes_of_kernel(M, N, K):
+    check_w8a16(M, M, N, K, HF, residual=True, packed=True, stable_weights=True)
+    check_w8a16(M, M, N, K, BF, activation="silu", gated=True, stable_weights=True)
 
 
 def test_w8a16_packed_is_the_same():
