@@ -25,13 +25,18 @@
 //                  the row of q that its codes will fill; the second, a
 //                  programmatic dependent, casts h, or makes it again from the
 //                  stream just written, the newest rows (still in L2) first.
+//   add_norm_cluster
+//                  the same for so few rows that one cluster of CTAs holds
+//                  them: the maximum goes through distributed shared memory.
 // Measured (GB300, replayed graphs, of the copy bandwidth): 16384 x 8192
 // static or per token 138.5 us, 0.997; 1021 x 8192 per token 10.3 us, 0.84; 16
 // x 4096 per token 1.9 us (launch and one round trip).  Dynamic: 16384 x 8192
 // 188 us (177 for 7 bytes an element and the stream read again), 1021 x 8192
-// with h 16.4 us for 11.1 of traffic, 16 x 4096 4.0 us.  One cooperative kernel
+// with h 16.4 us for 11.1 of traffic, 16 x 4096 2.7 us (4.3 in two kernels).  One cooperative kernel
 // with a grid barrier between the halves and h held in shared memory took 221,
 // 17.2 and 4.1 us, and had a wait in it.
+#include <atomic>
+
 #include "quant_device.cuh"
 #include "skinny_device.cuh"
 
@@ -50,6 +55,8 @@ constexpr size_t kAddWordsOffset = 32;
 struct AddNormWords {
     unsigned counter, half, amax[2];
 };
+constexpr int kAddMaxCluster = 16;  // CTAs (above 8 opted in)
+constexpr int kAddMaxDevices = 64;
 static_assert(kAddWordsOffset >= kBarrierAreaBytes && kAddWordsOffset + sizeof(AddNormWords) <= kPartialsOffset,
               "words of their own in the workspace");
 
@@ -294,6 +301,48 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_rows(const
     }
 }
 
+// The dynamic mode for a few rows, one cluster of CTAs (ROWS rows each): every
+// CTA pushes its maximum to all, and the rows never leave the registers.
+template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
+__global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_cluster(const AddNormArgs a) {
+    using R = Row<DT, WARPS, NW>;
+    __shared__ float fpart[WARPS];
+    __shared__ uint32_t red[33], peak[kAddMaxCluster];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (arrived here, waited for before a peer's memory is written)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x, words = a.K / 8;
+    const int row = static_cast<int>(blockIdx.x) * ROWS + (WARPS == 1 ? threadIdx.x >> 5 : 0);
+    const size_t at = static_cast<size_t>(row) * words;
+    const bool in = row < a.M;  // a whole warp (ROWS > 1) or no thread is not
+    uint4 t[NW];
+    uint32_t m = 0;
+    pdl_wait();
+    if (in) {
+        R::add(a, at, tid, words, t);
+        const uint64_t r2 = rms_factor(row_sum<WARPS>(R::squares(t), fpart), a.K, a.eps);
+        R::scale(a, tid, words, r2, t);
+        m = fold_mag<DT>(R::magnitude(t, 0));
+    }
+    m = block_max_u32(m, red);
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    const unsigned ctas = gridDim.x;  // one cluster
+    if (threadIdx.x < ctas) {
+        uint32_t remote = static_cast<uint32_t>(__cvta_generic_to_shared(&peak[blockIdx.x]));
+        asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(remote) : "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(m) : "memory");
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (in) R::store_h(a, at, tid, words, t);
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const unsigned lane = threadIdx.x & 31;
+    const uint32_t all = __reduce_max_sync(0xFFFFFFFFu, lane < ctas ? peak[lane] : 0u);
+    const float s = scale_from_amax(mag_bits_to_float<DT>(all));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = s;
+    if (in) R::template store_codes<false>(a, at, tid, words, t, Quot::make<DT>(s));
+}
+
 // The dynamic mode's first half: the stream, h when it is wanted, the factors
 // and the maximum.  As many blocks as fit at once go through the rows, so that
 // few of them touch the workspace's words (one block a row, 4096 of them, took
@@ -370,19 +419,58 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_cast(const
 
 __global__ void add_norm_empty_scale(float *scale) { *scale = 1.0f; }
 
+// The largest cluster of add_norm_cluster that the GPU holds, 16, 8 or 1.
+template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
+int largest_cluster() {
+    static std::atomic<int> known[kAddMaxDevices];  // 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kAddMaxDevices) return 1;
+    int most = known[dev].load(std::memory_order_relaxed);
+    if (most > 0) return most;
+    const auto kernel = add_norm_cluster<DT, WARPS, ROWS, NW, BLOCKS>;
+    most = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess
+               ? kAddMaxCluster : 8;
+    for (; most > 1; most = most > 8 ? 8 : 1) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(most), 1, 1);
+        cfg.blockDim = dim3(32 * WARPS * ROWS, 1, 1);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(most);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) break;
+        (void)cudaGetLastError();
+    }
+    known[dev].store(most, std::memory_order_relaxed);
+    return most;
+}
+
 template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
 int launch_rows(const AddNormArgs &a, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((int64_t(a.M) + ROWS - 1) / ROWS), 1, 1);
     cfg.blockDim = dim3(32 * WARPS * ROWS, 1, 1);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     // (the kernels wait for the preceding one before they touch memory)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (a.mode == FP8L_NQ_DYNAMIC) {
+    if (a.mode == FP8L_NQ_DYNAMIC &&
+        cfg.gridDim.x <= static_cast<unsigned>(largest_cluster<DT, WARPS, ROWS, NW, BLOCKS>())) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cfg.gridDim.x;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+        if (cudaLaunchKernelEx(&cfg, add_norm_cluster<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess)
+            return FP8L_ECUDA;
+    } else if (a.mode == FP8L_NQ_DYNAMIC) {
         if (cfg.gridDim.x > static_cast<unsigned>(sms * BLOCKS)) cfg.gridDim.x = sms * BLOCKS;
         if (cudaLaunchKernelEx(&cfg, add_norm_max<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess ||
             cudaLaunchKernelEx(&cfg, add_norm_cast<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess)
