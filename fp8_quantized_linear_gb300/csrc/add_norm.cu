@@ -32,9 +32,9 @@
 // static or per token 138.5 us, 0.997; 1021 x 8192 per token 10.3 us, 0.84; 16
 // x 4096 per token 1.9 us (launch and one round trip).  Dynamic: 16384 x 8192
 // 188 us (177 for 7 bytes an element and the stream read again), 1021 x 8192
-// with h 16.4 us for 11.1 of traffic, 16 x 4096 2.7 us (4.3 in two kernels).  One cooperative kernel
-// with a grid barrier between the halves and h held in shared memory took 221,
-// 17.2 and 4.1 us, and had a wait in it.
+// with h 16.4 us for 11.1 of traffic, 16 x 4096 2.6 us (4.2 in two kernels).
+// One cooperative kernel with a grid barrier between the halves and h held in
+// shared memory took 221, 17.2 and 4.1 us, and had a wait in it.
 #include <atomic>
 
 #include "quant_device.cuh"
@@ -148,7 +148,7 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if constexpr (WARPS > 1) {
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+        if ((threadIdx.x & 31) == 0) part[(threadIdx.x >> 5) % WARPS] = v;
         __syncthreads();
         v = 0.0f;
 #pragma unroll
@@ -303,28 +303,25 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_rows(const
 
 // The dynamic mode for a few rows, one cluster of CTAs (ROWS rows each): every
 // CTA pushes its maximum to all, and the rows never leave the registers.
-template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
-__global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_cluster(const AddNormArgs a) {
+template <int DT, int WARPS, int ROWS, int NW>
+__global__ void __launch_bounds__(32 * WARPS * ROWS, 1) add_norm_cluster(const AddNormArgs a) {
     using R = Row<DT, WARPS, NW>;
-    __shared__ float fpart[WARPS];
+    __shared__ float fpart[ROWS][WARPS];
     __shared__ uint32_t red[33], peak[kAddMaxCluster];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // (arrived here, waited for before a peer's memory is written)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    const int tid = WARPS == 1 ? (threadIdx.x & 31) : threadIdx.x, words = a.K / 8;
-    const int row = static_cast<int>(blockIdx.x) * ROWS + (WARPS == 1 ? threadIdx.x >> 5 : 0);
-    const size_t at = static_cast<size_t>(row) * words;
-    const bool in = row < a.M;  // a whole warp (ROWS > 1) or no thread is not
+    const int tid = threadIdx.x % (32 * WARPS), sub = threadIdx.x / (32 * WARPS);
+    const int row = static_cast<int>(blockIdx.x) * ROWS + sub;
+    const bool in = row < a.M;
+    const int words = in ? a.K / 8 : 0;  // a row beyond the last has none
+    const size_t at = static_cast<size_t>(row) * (a.K / 8);
     uint4 t[NW];
-    uint32_t m = 0;
     pdl_wait();
-    if (in) {
-        R::add(a, at, tid, words, t);
-        const uint64_t r2 = rms_factor(row_sum<WARPS>(R::squares(t), fpart), a.K, a.eps);
-        R::scale(a, tid, words, r2, t);
-        m = fold_mag<DT>(R::magnitude(t, 0));
-    }
-    m = block_max_u32(m, red);
+    R::add(a, at, tid, words, t);
+    const uint64_t r2 = rms_factor(row_sum<WARPS>(R::squares(t), fpart[sub]), a.K, a.eps);
+    R::scale(a, tid, words, r2, t);
+    const uint32_t m = block_max_u32(in ? fold_mag<DT>(R::magnitude(t, 0)) : 0u, red);
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     const unsigned ctas = gridDim.x;  // one cluster
     if (threadIdx.x < ctas) {
@@ -334,13 +331,13 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_cluster(co
     }
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (in) R::store_h(a, at, tid, words, t);
+    R::store_h(a, at, tid, words, t);
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const unsigned lane = threadIdx.x & 31;
     const uint32_t all = __reduce_max_sync(0xFFFFFFFFu, lane < ctas ? peak[lane] : 0u);
     const float s = scale_from_amax(mag_bits_to_float<DT>(all));
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = s;
-    if (in) R::template store_codes<false>(a, at, tid, words, t, Quot::make<DT>(s));
+    R::template store_codes<false>(a, at, tid, words, t, Quot::make<DT>(s));
 }
 
 // The dynamic mode's first half: the stream, h when it is wanted, the factors
@@ -420,14 +417,14 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, BLOCKS) add_norm_cast(const
 __global__ void add_norm_empty_scale(float *scale) { *scale = 1.0f; }
 
 // The largest cluster of add_norm_cluster that the GPU holds, 16, 8 or 1.
-template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
+template <int DT, int WARPS, int ROWS, int NW>
 int largest_cluster() {
     static std::atomic<int> known[kAddMaxDevices];  // 0: not asked yet
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kAddMaxDevices) return 1;
     int most = known[dev].load(std::memory_order_relaxed);
     if (most > 0) return most;
-    const auto kernel = add_norm_cluster<DT, WARPS, ROWS, NW, BLOCKS>;
+    const auto kernel = add_norm_cluster<DT, WARPS, ROWS, NW>;
     most = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess
                ? kAddMaxCluster : 8;
     for (; most > 1; most = most > 8 ? 8 : 1) {
@@ -449,28 +446,59 @@ int largest_cluster() {
     return most;
 }
 
+// One cluster's launch, where its CTAs hold all rows and the GPU holds it.
+template <int DT, int WARPS, int ROWS, int NW>
+bool launch_cluster(const AddNormArgs &a, cudaStream_t stream, int *status) {
+    const int ctas = static_cast<int>((int64_t(a.M) + ROWS - 1) / ROWS);
+    if (ctas > kAddMaxCluster || ctas > largest_cluster<DT, WARPS, ROWS, NW>()) return false;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(32 * WARPS * ROWS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cfg.gridDim.x;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    *status = cudaLaunchKernelEx(&cfg, add_norm_cluster<DT, WARPS, ROWS, NW>, a) == cudaSuccess
+                  ? launch_status() : FP8L_ECUDA;
+    return true;
+}
+
+// By the row's length and the rows that 16 CTAs hold: few threads a CTA first
+// (17 rows of 4096: two a CTA 3.0 us, four 4.1, in two kernels 4.2; 17 of 8192
+// 3.9, four a CTA 5.8, in two kernels 4.7; 128 of 128 2.2, 512 2.9 and 3.9).
+template <int DT>
+bool dispatch_cluster(const AddNormArgs &a, cudaStream_t s, int *st) {
+    const int words = a.K / 8;
+    if (words <= 32) return launch_cluster<DT, 1, 8, 1>(a, s, st) || launch_cluster<DT, 1, 32, 1>(a, s, st);
+    if (words <= 128) return launch_cluster<DT, 4, 4, 1>(a, s, st) || launch_cluster<DT, 1, 8, 4>(a, s, st);
+    if (words <= 256)
+        return launch_cluster<DT, 4, 1, 2>(a, s, st) || launch_cluster<DT, 4, 2, 2>(a, s, st) ||
+               launch_cluster<DT, 4, 4, 2>(a, s, st);
+    if (words <= 512) return launch_cluster<DT, 8, 1, 2>(a, s, st) || launch_cluster<DT, 8, 2, 2>(a, s, st);
+    if (words <= 1024) return launch_cluster<DT, 8, 1, 4>(a, s, st) || launch_cluster<DT, 8, 2, 4>(a, s, st);
+    if (words <= 2048) return launch_cluster<DT, 16, 1, 4>(a, s, st);
+    return launch_cluster<DT, 32, 1, 4>(a, s, st);
+}
+
 template <int DT, int WARPS, int ROWS, int NW, int BLOCKS>
 int launch_rows(const AddNormArgs &a, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((int64_t(a.M) + ROWS - 1) / ROWS), 1, 1);
     cfg.blockDim = dim3(32 * WARPS * ROWS, 1, 1);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     // (the kernels wait for the preceding one before they touch memory)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (a.mode == FP8L_NQ_DYNAMIC &&
-        cfg.gridDim.x <= static_cast<unsigned>(largest_cluster<DT, WARPS, ROWS, NW, BLOCKS>())) {
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = cfg.gridDim.x;
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.numAttrs = 2;
-        if (cudaLaunchKernelEx(&cfg, add_norm_cluster<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess)
-            return FP8L_ECUDA;
-    } else if (a.mode == FP8L_NQ_DYNAMIC) {
+    if (a.mode == FP8L_NQ_DYNAMIC) {
         if (cfg.gridDim.x > static_cast<unsigned>(sms * BLOCKS)) cfg.gridDim.x = sms * BLOCKS;
         if (cudaLaunchKernelEx(&cfg, add_norm_max<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess ||
             cudaLaunchKernelEx(&cfg, add_norm_cast<DT, WARPS, ROWS, NW, BLOCKS>, a) != cudaSuccess)
@@ -488,6 +516,8 @@ int launch_rows(const AddNormArgs &a, int sms, cudaStream_t stream) {
 template <int DT>
 int dispatch_add_norm(const AddNormArgs &a, int sms, cudaStream_t s) {
     const int words = a.K / 8;
+    int st = FP8L_OK;
+    if (a.mode == FP8L_NQ_DYNAMIC && dispatch_cluster<DT>(a, s, &st)) return st;
     if (words <= 32) return launch_rows<DT, 1, 8, 1, 6>(a, sms, s);
     if (words <= 128) return launch_rows<DT, 1, 8, 4, 3>(a, sms, s);
     if (words <= 256) return launch_rows<DT, 4, 1, 2, 8>(a, sms, s);

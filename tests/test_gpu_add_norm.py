@@ -88,6 +88,37 @@ def test_many_rows(mode, M, K):
     assert_status_ok()
 
 
+# rows and lengths on both sides of what one cluster of CTAs takes; the rows
+# behind the batch stay
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("K", [256, 272, 1024, 1040, 2048, 2064, 4096, 4112, 8192, 8208, 16384, 16400])
+def test_few_rows_with_one_scale(K, dtype):
+    for M in (1, 15, 16, 17, 32, 33, 63, 64, 65, 128, 129, 512, 513):
+        if M > 130 and K > 1024:
+            continue
+        x, res, gamma = inputs(M + K, M, K, dtype)
+        x[M // 2, K - 1] = 300.0  # the maximum in any CTA
+        q, s, total, h = run(x, res, gamma, "dynamic")
+        check(x, res, gamma, "dynamic", q, s, total, h)
+        big_q = torch.full((M + 3, K), 7, dtype=torch.uint8, device=DEV)
+        big_t = torch.full((M + 3, K), 7, dtype=dtype, device=DEV)
+        q2, s2, _, _ = run(x, res, gamma, "dynamic", False, q=big_q[:M], total=big_t[:M])
+        assert torch.equal(big_q[:M], q) and torch.equal(s2, s) and torch.equal(big_t[:M], total)
+        assert (big_q[M:] == 7).all() and (big_t[M:] == 7).all()
+
+
+def test_few_rows_that_are_not_finite():
+    """A NaN or an infinity in one CTA's row shows in the scale as it does for
+    many rows."""
+    for bad in (float("nan"), float("inf")):
+        x, res, gamma = inputs(3, 600, 256, HF)
+        x[5, 9] = bad
+        many = run(x, res, gamma, "dynamic")
+        few = run(x[:20].contiguous(), res[:20].contiguous(), gamma, "dynamic")
+        assert torch.equal(many[1].view(torch.int32), few[1].view(torch.int32))
+        assert torch.equal(many[0][:20], few[0])
+
+
 @pytest.mark.parametrize("mode", MODES)
 def test_in_place(mode):
     """The stream updated in its own tensor, or in x's."""
