@@ -359,14 +359,15 @@ FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N
  * sum of E4M3 parts (two for bf16, three for fp16), whose products with the
  * weights are exact: what the parts leave out of a value is below 2^-21
  * (bf16) or 2^-25 (fp16) of the token's largest magnitude (of 2^-119, where
- * that is more).  With
- * FP8L_KERNEL_AUTO a call without bias, activation and residual is
- * fp8_w8a16_mm.  workspace:
- * fp8_w8a16_linear_workspace_bytes() bytes for these arguments (16-byte
- * aligned, any contents; may be NULL when that is 0), sharing memory with no other argument), written by the call
+ * that is more).  With FP8L_KERNEL_AUTO a call without bias, activation and
+ * residual is fp8_w8a16_mm up to 16 tokens of bf16 and 64 of fp16.
+ * workspace: fp8_w8a16_linear_workspace_bytes() bytes for these arguments
+ * (16-byte aligned, any contents; may be NULL when that is 0 or the call is
+ * fp8_w8a16_mm), sharing memory with no other argument, written by the call
  * and free for other use when it has run; calls that may overlap need one
  * each.  flags: any of FP8L_WEIGHTS_STABLE and FP8L_WEIGHTS_PACKED, and
- * FP8L_KERNEL_STREAM or FP8L_KERNEL_SWAPPED (any M).  A time-out of a device-side wait is recorded as for fp8_w8a16_mm. */
+ * FP8L_KERNEL_STREAM or FP8L_KERNEL_SWAPPED (any M).  A time-out of a
+ * device-side wait is recorded as for fp8_w8a16_mm. */
 FP8L_API size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t N, int64_t K,
                                                  unsigned flags);
 FP8L_API int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, const float *w_scale,

@@ -304,8 +304,16 @@ def test_w8a16_packed_is_the_same():
 
 
 def test_w8a16_plain_call_is_the_product():
-    for M in (1, 16, 40, 70):
+    for M, dtype in ((1, HF), (16, HF), (40, HF), (64, HF), (1, BF), (16, BF)):
         gen = torch.Generator(device=DEV).manual_seed(M)
-        x = torch.randn(M, 400, generator=gen, device=DEV).to(HF)
+        x = torch.randn(M, 400, generator=gen, device=DEV).to(dtype)
         w, sw = normal_codes(gen, 96, 400), torch.rand(96, generator=gen, device=DEV) / 100
         assert torch.equal(fl.fp8_w8a16_linear(x, w, sw), fl.fp8_w8a16_mm(x, w, sw))
+
+
+def test_w8a16_plain_calls_of_more_tokens():
+    for packed in (False, True):
+        check_w8a16(1, 65, 1024, 4096, HF, packed=packed, stable_weights=True)
+        check_w8a16(2, 700, 96, 400, HF, packed=packed)
+        check_w8a16(3, 17, 96, 400, BF, packed=packed)
+        check_w8a16(4, 130, 1024, 4096, BF, packed=packed, stable_weights=True)
