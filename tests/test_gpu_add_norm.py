@@ -190,3 +190,38 @@ def test_graph_beside_eager_calls():
             for u, v in zip(one, w):
                 assert torch.equal(u, v)
     assert_status_ok()
+
+
+def test_few_rows_in_graphs_and_streams():
+    """Dynamic calls of one cluster among calls of two kernels: captured, on
+    three streams at once, and each call's stream read by the next."""
+    sizes = [(1, 4096), (20, 8192), (300, 2048), (16, 16384), (400, 128)]
+    args = [inputs(i, M, K, BF if i & 1 else HF) for i, (M, K) in enumerate(sizes)]
+
+    def chain():
+        out = []
+        for x, res, gamma in args:
+            first = run(x, res, gamma, "dynamic")
+            out += [first, run(first[2], res, gamma, "dynamic", False)]
+        return out
+
+    want = chain()
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(chain())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = chain()
+    torch.cuda.synchronize()
+    for one in got + [eager]:
+        for u, v in zip(one, want):
+            assert all(torch.equal(a, b) for a, b in zip(u, v) if a is not None)
+    assert_status_ok()
