@@ -178,8 +178,10 @@ __device__ __forceinline__ uint64_t rms_factor(float ss, int K, float eps) {
     const float y = __frcp_rn(__fsqrt_rn(ms));
     const float hi = __fmul_rn(ms, y), lo = __fmaf_rn(ms, y, -hi);
     const float e = __fmaf_rn(-lo, y, __fmaf_rn(-hi, y, 1.0f));
-    // (a zero row without eps has y infinite and stays that)
-    const float r = ms > 0x1p-100f ? __fmaf_rn(0.5f * y, e, y) : y;
+    // (a zero row without eps has y infinite and stays that; a mean square past
+    // float32's range has y = 0 and stays that, as in fp8_rmsnorm_quant: ms y
+    // would be infinity times 0)
+    const float r = ms > 0x1p-100f && ms <= 3.4e38f ? __fmaf_rn(0.5f * y, e, y) : y;
     return f2_pack(__float_as_uint(r), __float_as_uint(r));
 }
 

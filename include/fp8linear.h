@@ -471,7 +471,9 @@ FP8L_API int fp8_rmsnorm_quant(const void *x, int x_dtype, const void *gamma, fl
  *   r, h and the codes from total as fp8_rmsnorm_quant takes them from x
  *
  * (the float32 sum of squares adds in an order of its own, so h agrees with
- * the two calls up to one rounding where h is next to a border).  x,
+ * the two calls up to one rounding where h is next to a border; a row whose
+ * sum of squares passes float32's range has r = 0 in both, its finite values
+ * become zeros).  x,
  * residual: [M, K] of x_dtype; total: [M, K], the new residual stream; it may
  * be x or residual itself (updated in place).  gamma, eps, q, scale, mode, h,
  * workspace, M and K as for fp8_rmsnorm_quant.  Apart from that, no output
