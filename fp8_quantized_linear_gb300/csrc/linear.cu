@@ -195,6 +195,9 @@ extern "C" int fp8_w8a16_linear(const void *x, int x_dtype, const uint8_t *w, co
     int st = check_epilogue(M, N, K, bias, bias_dtype, activation, residual, nullptr, y, x_dtype, &c.e,
                             &c.gated);
     if (st != FP8L_OK) return st;
+    // what the kernels' grids and tensor maps count, before the tokens are split
+    if (kernel == FP8L_KERNEL_STREAM ? M > kLinearStreamTokens : M > 0 && !linear_parts_fit(x_dtype, M, N))
+        return FP8L_ESHAPE;
     if (M > 0 && x == nullptr) return FP8L_EINVAL;
     if (!aligned16(w) || (M > 0 && !aligned16(x)) || misaligned(w_scale, 4)) return FP8L_EALIGN;
     c.packed = (flags & FP8L_WEIGHTS_PACKED) != 0u ? 1 : 0;

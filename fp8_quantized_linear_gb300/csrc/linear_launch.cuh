@@ -33,7 +33,9 @@ int make_swizzle64_map(CUtensorMap *map, const void *ptr, int rank, const uint64
 // parts: E4M3 numbers a token value is held in (1: the codes themselves).
 int launch_linear_swapped(const LinearCall &c, int parts, const float *token_scale);
 
-// Weights streamed through registers, up to 16 tokens a CTA (any tokens).
+// Weights streamed through registers, up to 16 tokens a CTA: as many tokens as
+// the grid's second dimension holds.
+constexpr int64_t kLinearStreamTokens = 65535 * 16;
 int launch_linear_stream(const LinearCall &c);
 
 // 256-token by 256-row tiles over pairs of SMs (E4M3 tokens, row-major weights).
@@ -42,6 +44,7 @@ int launch_linear_pair(const LinearCall &c);
 // 16-bit tokens as sums of E4M3 parts: bytes of the scratch that
 // linear_split_tokens fills and launch_linear_swapped reads.
 int linear_parts(int x_dtype);
+bool linear_parts_fit(int x_dtype, int64_t M, int64_t N);  // tensor map and grid count that many
 size_t linear_parts_bytes(int x_dtype, int64_t M, int64_t K);
 int linear_split_tokens(const LinearCall &c, void *scratch, const float **token_scale);
 

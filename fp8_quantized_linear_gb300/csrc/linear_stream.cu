@@ -255,7 +255,7 @@ int dispatch_stream(const StreamArgs &p, const LinearCall &c) {
 }  // namespace
 
 int launch_linear_stream(const LinearCall &c) {
-    if (c.M > 65535 * 16) return FP8L_ESHAPE;  // the grid's second dimension
+    if (c.M > kLinearStreamTokens) return FP8L_ESHAPE;
     const StreamArgs p{c.w, c.x, c.M, c.N, c.K, c.a_scale, c.a_per_token, c.w_scale, c.w_per_channel, c.e};
     if (c.x_dtype == FP8L_E4M3) return dispatch_stream<FP8L_E4M3, false>(p, c);
     if (c.x_dtype == FP8L_BF16)

@@ -590,7 +590,7 @@ int launch_linear_swapped(const LinearCall &c, int parts, const float *token_sca
     p.parts = parts;
     p.T = tokens_a_tile(parts, c.M, &p.m_tiles);
     const int cols = parts * p.T;
-    if (int64_t(p.m_tiles) * cols > 0x7FFFFFFF) return FP8L_ESHAPE;  // rows of the parts
+    if (int64_t(p.m_tiles) * cols > 0x7FFFFFFF) return FP8L_ESHAPE;  // token rows of all tiles
     p.stage_bytes = kLsWBytes + cols * LS_BK;
     // the most stages that fit; the float tile reuses the ring
     int stages = static_cast<int>((kLsSmem - 1024 - 24 - 4 * p.T) / (p.stage_bytes + 16));
@@ -739,6 +739,14 @@ split_tokens_kernel(const uint4 *x, int K, int T, uint8_t *codes, float *scale) 
 }  // namespace
 
 int linear_parts(int x_dtype) { return x_dtype == FP8L_BF16 ? 2 : 3; }
+
+bool linear_parts_fit(int x_dtype, int64_t M, int64_t N) {
+    const int parts = linear_parts(x_dtype);
+    int tiles = 0;
+    const int T = tokens_a_tile(parts, M, &tiles);
+    // rows of the parts, and CTAs (of 128 weight rows, gated or not)
+    return int64_t(tiles) * parts * T <= 0x7FFFFFFF && tiles * ((N + LS_BM - 1) / LS_BM) <= 0x7FFFFFFF;
+}
 
 size_t linear_parts_bytes(int x_dtype, int64_t M, int64_t K) {
     const int parts = linear_parts(x_dtype);

@@ -341,7 +341,7 @@ enum fp8l_activation {
  * FP8L_WEIGHTS_STABLE (the bias is not part of the promise) and
  * FP8L_A_PER_TOKEN, and one FP8L_KERNEL_* choice (a tuning and testing
  * option; every kernel takes every call, FP8L_KERNEL_STREAM up to 1048560
- * tokens, FP8L_ESHAPE above).  With FP8L_KERNEL_AUTO a call without bias,
+ * tokens, FP8L_KERNEL_SWAPPED up to 2^31 - 128, FP8L_ESHAPE above).  With FP8L_KERNEL_AUTO a call without bias,
  * activation and residual is fp8_scaled_mm. */
 FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N, int64_t K,
                         const float *a_scale, const float *w_scale, int w_per_channel,
@@ -366,7 +366,9 @@ FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N
  * fp8_w8a16_mm), sharing memory with no other argument, written by the call
  * and free for other use when it has run; calls that may overlap need one
  * each.  flags: any of FP8L_WEIGHTS_STABLE and FP8L_WEIGHTS_PACKED, and
- * FP8L_KERNEL_STREAM or FP8L_KERNEL_SWAPPED (any M).  A time-out of a
+ * FP8L_KERNEL_STREAM (up to 1048560 tokens, which it takes whole: no parts)
+ * or FP8L_KERNEL_SWAPPED (up to 1073741760 tokens of bf16, 715827840 of
+ * fp16; as many are AUTO's limit); FP8L_ESHAPE above.  A time-out of a
  * device-side wait is recorded as for fp8_w8a16_mm. */
 FP8L_API size_t fp8_w8a16_linear_workspace_bytes(int x_dtype, int64_t M, int64_t N, int64_t K,
                                                  unsigned flags);
