@@ -579,6 +579,8 @@ extern "C" int fp8_add_rmsnorm_quant(const void *x, const void *residual, int x_
         for (int j = i + 1; j < 4; ++j)
             if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return FP8L_EINVAL;
     }
+    for (int j = 0; j < 3; ++j)  // (the workspace is written too)
+        if (overlap(in[j].p, in[j].n, in[4].p, in[4].n)) return FP8L_EINVAL;
     int sms = 0;
     const int st = check_device(&sms);
     if (st != FP8L_OK) return st;

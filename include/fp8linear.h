@@ -479,7 +479,8 @@ FP8L_API int fp8_rmsnorm_quant(const void *x, int x_dtype, const void *gamma, fl
  * residual: [M, K] of x_dtype; total: [M, K], the new residual stream; it may
  * be x or residual itself (updated in place).  gamma, eps, q, scale, mode, h,
  * workspace, M and K as for fp8_rmsnorm_quant.  Apart from that, no output
- * shares memory with an input or another output (FP8L_EINVAL).  workspace is
+ * shares memory with an input or another output, nor in FP8L_NQ_DYNAMIC the
+ * workspace with anything (FP8L_EINVAL).  workspace is
  * used in FP8L_NQ_DYNAMIC only, by one call at a time (two words of it, zero
  * between calls); nothing in the call waits.  Deterministic. */
 FP8L_API int fp8_add_rmsnorm_quant(const void *x, const void *residual, int x_dtype,

@@ -29,3 +29,11 @@ def test_more_parts_than_the_tensor_map_counts(lib):
                 assert w8a16(lib, dt=dt, M=M, flags=flags) == b.ESHAPE, (dt, M)
     assert w8a16(lib, M=65535 * 16 + 1, flags=16) == b.ESHAPE
 
+
+def test_norm_workspace_over_an_input(lib):
+    """The dynamic mode writes into its workspace."""
+    ok = dict(x=at(0), res=at(1), dt=b.BF16, g=at(2), eps=1e-5, M=9, K=64, total=at(3), q=at(4),
+              s=at(5), mode=0, h=at(6), ws=at(7), st=None)
+    for name in ("x", "res", "g"):
+        assert lib.fp8_add_rmsnorm_quant(*dict(ok, ws=ok[name]).values()) == b.EINVAL, name
+        assert lib.fp8_add_rmsnorm_quant(*dict(ok, ws=ok[name] + 64).values()) == b.EINVAL, name
