@@ -3,8 +3,8 @@
 //
 // These calls stand in front of kernels of two to fifteen microseconds, and the
 // same checks written in Python took longer than that (13 to 20 us a call on
-// the GB300's host cores; 4 to 8 us here).  The extension holds no state, and
-// every error is a Python exception: a C++ one does not leave it.
+// the GB300's host cores; 4 to 8 us here).  Every error is a Python exception:
+// a C++ one does not leave the extension.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -14,6 +14,8 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <mutex>
 
 #include "fp8linear.h"
 
@@ -64,13 +66,33 @@ bool shaped(const Tensor &t, int64_t rows, int64_t cols) {
     return t.dim() == 2 && t.size(0) == rows && t.size(1) == cols;
 }
 
+// Other Python threads run while this one allocates and launches: a launch
+// waits where the queue of the GPU is full, and what it waits for may need the
+// interpreter.  (Nothing below an instance touches a Python object's count.)
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+    Unlocked &operator=(const Unlocked &) = delete;
+};
+
+// The two kernels of a dynamic norm stand behind each other on their stream,
+// also where two threads share it (and with it the workspace).
+std::mutex g_norm_order;
+
+Tensor empty(at::IntArrayRef size, ScalarType s, int index) {
+    return at::detail::empty_cuda(size, s, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)),
+                                  std::nullopt);
+}
+
 // A tensor that this call makes, or the one given.
 struct Output {
     Tensor made;
     PyObject *given;
-    Output(PyObject *o, bool want, int64_t rows, int64_t cols, ScalarType s, int index) : given(o) {
-        if (o == Py_None && want)
-            made = at::detail::empty_cuda({rows, cols}, s, c10::Device(c10::kCUDA, index), std::nullopt);
+    explicit Output(PyObject *o) : given(o) {}
+    void make(bool want, int64_t rows, int64_t cols, ScalarType s, int index) {
+        if (given == Py_None && want) made = empty({rows, cols}, s, index);
     }
     void *ptr() const {
         if (made.defined()) return made.data_ptr();
@@ -181,16 +203,21 @@ PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t count) {
     if (ws != nullptr && (ws->scalar_type() != ScalarType::Byte ||
                           static_cast<size_t>(ws->numel()) < fp8l_workspace_bytes()))
         value_error("ws is a uint8 tensor of fp8l_workspace_bytes() elements");
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-    const Output result(args[10], true, M, e.width, out, index);
-    const int status = fp8_linear(
-        static_cast<const uint8_t *>(a.data_ptr()), static_cast<const uint8_t *>(w.data_ptr()), M, N, K,
-        static_cast<const float *>(a_scale.data_ptr()), static_cast<const float *>(w_scale.data_ptr()),
-        scales != 1 ? 1 : 0, e.bias, e.bias_code,
-        static_cast<int>(number(args[5])) | (gated ? FP8L_ACT_GATED : 0), e.residual,
-        codes ? static_cast<const float *>(out_scale->data_ptr()) : nullptr, result.ptr(),
-        codes ? FP8L_E4M3 : code16(out), address(ws), flags,
-        c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
+    const int act = static_cast<int>(number(args[5])) | (gated ? FP8L_ACT_GATED : 0);
+    Output result(args[10]);
+    int status;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+        result.make(true, M, e.width, out, index);
+        status = fp8_linear(
+            static_cast<const uint8_t *>(a.data_ptr()), static_cast<const uint8_t *>(w.data_ptr()), M, N, K,
+            static_cast<const float *>(a_scale.data_ptr()), static_cast<const float *>(w_scale.data_ptr()),
+            scales != 1 ? 1 : 0, e.bias, e.bias_code, act, e.residual,
+            codes ? static_cast<const float *>(out_scale->data_ptr()) : nullptr, result.ptr(),
+            codes ? FP8L_E4M3 : code16(out), address(ws), flags,
+            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
+    }
     if (failed(status, "fp8_linear")) return nullptr;
     return result.result();
     CALL_END
@@ -220,22 +247,23 @@ PyObject *w8a16_linear(PyObject *, PyObject *const *args, Py_ssize_t count) {
     const Epilogue e = epilogue(bias, residual, gated, M, N, out);
     if (y != nullptr && (!shaped(*y, M, e.width) || y->scalar_type() != out))
         value_error("y is [M, N] ([M, N / 2] when gated) of x's dtype");
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-    const Output result(args[7], true, M, e.width, out, index);
-    const int code = code16(out);
-    // scratch of this call, from the stream's memory
-    const size_t bytes = fp8_w8a16_linear_workspace_bytes(code, M, N, K, flags);
-    Tensor scratch;
-    if (bytes > 0)
-        scratch = at::detail::empty_cuda({static_cast<int64_t>(bytes)}, ScalarType::Byte,
-                                         c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)),
-                                         std::nullopt);
-    const int status = fp8_w8a16_linear(
-        x.data_ptr(), code, static_cast<const uint8_t *>(w.data_ptr()),
-        static_cast<const float *>(w_scale.data_ptr()), M, N, K, e.bias, e.bias_code,
-        static_cast<int>(number(args[4])) | (gated ? FP8L_ACT_GATED : 0), e.residual, result.ptr(),
-        bytes > 0 ? scratch.data_ptr() : nullptr, flags,
-        c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
+    const int code = code16(out), act = static_cast<int>(number(args[4])) | (gated ? FP8L_ACT_GATED : 0);
+    Output result(args[7]);
+    int status;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+        result.make(true, M, e.width, out, index);
+        // scratch of this call, from the stream's memory
+        const size_t bytes = fp8_w8a16_linear_workspace_bytes(code, M, N, K, flags);
+        Tensor scratch;
+        if (bytes > 0) scratch = empty({static_cast<int64_t>(bytes)}, ScalarType::Byte, index);
+        status = fp8_w8a16_linear(
+            x.data_ptr(), code, static_cast<const uint8_t *>(w.data_ptr()),
+            static_cast<const float *>(w_scale.data_ptr()), M, N, K, e.bias, e.bias_code, act, e.residual,
+            result.ptr(), bytes > 0 ? scratch.data_ptr() : nullptr, flags,
+            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
+    }
     if (failed(status, "fp8_w8a16_linear")) return nullptr;
     return result.result();
     CALL_END
@@ -277,22 +305,27 @@ PyObject *add_rmsnorm_quant(PyObject *, PyObject *const *args, Py_ssize_t count)
     if (ws != nullptr && (ws->scalar_type() != ScalarType::Byte ||
                           static_cast<size_t>(ws->numel()) < fp8l_workspace_bytes()))
         value_error("ws is a uint8 tensor of fp8l_workspace_bytes() elements");
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-    const Output total_out(args[5], true, M, K, s, index);
-    const Output q_out(args[6], codes, M, K, ScalarType::Byte, index);
+    const bool want_h = !codes || truth(args[9]);
+    Output total_out(args[5]), q_out(args[6]), h_out(args[8]);
     Tensor made_scale;
-    if (codes && scale == nullptr)
-        made_scale = at::detail::empty_cuda({entries}, ScalarType::Float,
-                                            c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)),
-                                            std::nullopt);
-    const Output h_out(args[8], !codes || truth(args[9]), M, K, s, index);
-    void *scale_ptr = scale != nullptr ? scale->data_ptr()
-                                       : (made_scale.defined() ? made_scale.data_ptr() : nullptr);
-    const int status = fp8_add_rmsnorm_quant(
-        x.data_ptr(), residual.data_ptr(), code16(s), gamma.data_ptr(), static_cast<float>(eps), M, K,
-        total_out.ptr(), codes ? static_cast<uint8_t *>(q_out.ptr()) : nullptr,
-        codes ? static_cast<float *>(scale_ptr) : nullptr, mode, h_out.ptr(), address(ws),
-        c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
+    int status;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+        total_out.make(true, M, K, s, index);
+        q_out.make(codes, M, K, ScalarType::Byte, index);
+        if (codes && scale == nullptr) made_scale = empty({entries}, ScalarType::Float, index);
+        h_out.make(want_h, M, K, s, index);
+        void *scale_ptr = scale != nullptr ? scale->data_ptr()
+                                           : (made_scale.defined() ? made_scale.data_ptr() : nullptr);
+        std::unique_lock<std::mutex> order(g_norm_order, std::defer_lock);
+        if (mode == FP8L_NQ_DYNAMIC) order.lock();
+        status = fp8_add_rmsnorm_quant(
+            x.data_ptr(), residual.data_ptr(), code16(s), gamma.data_ptr(), static_cast<float>(eps), M, K,
+            total_out.ptr(), codes ? static_cast<uint8_t *>(q_out.ptr()) : nullptr,
+            codes ? static_cast<float *>(scale_ptr) : nullptr, mode, h_out.ptr(), address(ws),
+            c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
+    }
     if (failed(status, "fp8_add_rmsnorm_quant")) return nullptr;
     PyObject *scale_result = args[7];
     if (made_scale.defined())
