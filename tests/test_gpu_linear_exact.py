@@ -148,6 +148,31 @@ def test_w8a16_rows_with_an_outlier(dtype, ratio, M):
     assert_status_ok()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("packed", [False, True])
+def test_w8a16_every_value_alone(dtype, packed):
+    """Rows of two values, the largest against zero weights, the other against
+    one: the result is what the parts hold of it, the value itself down to 2^-13
+    of the largest."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    M, K = 4000, 32
+    at, size = torch.arange(M, device=DEV) % (K - 1) + 1, torch.exp2(-24.0 * torch.arange(M, device=DEV) / M)
+    x = torch.zeros(M, K, dtype=dtype, device=DEV)
+    x[:, 0] = (1 + 30 * torch.rand(M, generator=gen, device=DEV)).to(dtype)
+    value = (x[:, 0].float() * size * (0.5 + 0.5 * torch.rand(M, generator=gen, device=DEV))).to(dtype)
+    x[torch.arange(M, device=DEV), at] = value
+    w = torch.full((32, K), 0x38, dtype=U8, device=DEV)
+    w[:, 0] = 0
+    y = w8a16(x, w, torch.ones(32, device=DEV), residual=torch.zeros(M, 32, dtype=dtype, device=DEV),
+              packed=packed, kernel="swapped")
+    want = held(x)[torch.arange(M, device=DEV), at]
+    assert torch.equal(y, want.to(dtype)[:, None].expand(M, 32))
+    whole = value.double() >= x[:, 0].double() * 2.0 ** -13
+    assert whole.sum() > M // 3 and torch.equal(want[whole], value.double()[whole])
+    assert (want != value.double()).any()
+    assert_status_ok()
+
+
 @pytest.mark.parametrize("dtype,size", [(BF, 2.0 ** -126), (BF, 2.0 ** -120), (BF, 2.0 ** -112), (BF, 2.0 ** -100),
                                         (BF, 2.0 ** 100), (HF, 2.0 ** -20), (HF, 2.0 ** -15), (HF, 2.0 ** 12)])
 @pytest.mark.parametrize("kernel", ["stream", "swapped"])
