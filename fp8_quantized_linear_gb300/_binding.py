@@ -891,7 +891,10 @@ def fp8_w8a16_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     [M, K] and E4M3 w [N, K] (per-channel w_scale [N]; packed: the output of
     fp8_pack_w8a16_weights) with bias, activation, gate and residual as in
     fp8_linear; y and residual have x's dtype.  kernel: "auto", "stream" or
-    "swapped" (FP8L_KERNEL_*)."""
+    "swapped" (FP8L_KERNEL_*); above 8 tokens (16 with few weights) "auto" holds
+    x in E4M3 parts, cut at 2^-21 (bf16) or 2^-25 (fp16) of a row's largest
+    magnitude, where "stream" takes it whole (and reads the weights once for
+    every 16 tokens)."""
     return (_calls or _load_calls()).w8a16_linear(
         x, w, w_scale, bias, _choice(ACTIVATIONS, activation, "activation"), gated, residual, y,
         _choice(KERNELS, kernel, "kernel") | (WEIGHTS_STABLE if stable_weights else 0) |
@@ -904,8 +907,8 @@ _norm_capture_workspaces = {}  # (device, stream): (capture, workspace) of its l
 
 def _norm_workspace(index: int) -> torch.Tensor:
     """A workspace of a dynamic fp8_add_rmsnorm_quant for the current stream:
-    its grid barrier's words belong to one call at a time, so streams do not
-    share one, and a graph capture gets its own from the graph's memory, zeroed
+    the words through which the tensor's maximum passes belong to one call at
+    a time, so streams do not share one, and a graph capture gets its own from the graph's memory, zeroed
     by every replay (a graph may run beside eager calls and other graphs)."""
     key = (index, _stream_handle(index))
     capture = _capture_id(*key)

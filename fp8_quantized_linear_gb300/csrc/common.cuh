@@ -18,6 +18,8 @@ namespace fp8l {
 //   [24, 32)                 uint32[2] its maximum-magnitude words
 //                            (the pair of index `counter & 1` is zero when a
 //                            call starts; that call clears the other pair)
+//   [32, 48)                 uint32[4] fp8_add_rmsnorm_quant: call counter, half in
+//                            use, a pair of maxima (the other half is zero)
 //   [256, 256 + 4*kMaxParts) float per-block partial maxima (two-launch quantizer)
 constexpr size_t kStatusOffset = 0;
 constexpr size_t kBarrierAreaBytes = 32;  // [0, 32): status and barrier words

@@ -42,7 +42,7 @@ __device__ __forceinline__ float silu_of(float z) { return __fdividef(z, 1.0f + 
 // polynomial of degree 6 with the least largest relative error over 0 <= a <=
 // 14, fitted by reweighted least squares: 9e-7, below the exponential's own
 // error.  (erfcf in its place cost 20 to 30 % of a product with K = 4096: 1024
-// x 28672 112 us against 80 without an activation.)
+// x 28672 112 us against 80 without an activation; this form takes 97.)
 // The tail's argument stops at z = 20, where it is zero beside z: of an
 // infinite z it would be infinity times 0.  (Minus infinity and NaN stay: NaN,
 // the formula's infinity times 0.)

@@ -99,12 +99,14 @@ unsigned choose_linear(int64_t M, int64_t N, int64_t K, int sms) {
 }
 
 // The kernel of fp8_w8a16_linear: weights streamed through registers for a few
-// tokens (M = 1 at 12288 x 4096, packed, 11.2 us against 13.1 swapped; M = 8 at
-// 28672 x 8192 44.2 against 41.7; M = 16 at 4096 x 4096 6.8 against 9.5, at 2048
-// x 6144 8.0 against 9.2, but at 2048 x 12288 13.4 against 11.7), else tokens in
-// parts through the swapped-operand kernel (M = 16 at 4096 x 11008 14.0 against
-// 14.1 to 18.2, at 22016 x 4096 gated 20.6 against 25.0; M = 32 at 4096 x 11008
-// 15.7 against 26.6).
+// tokens (M = 1 at 12288 x 4096, packed, 11.2 us against 13.1 swapped), up to 8
+// for any weights, since it takes the tokens whole (at most 8 % are lost by
+// that: M = 5 at 28672 x 8192 42.3 us against 42.3, M = 8 45.4 against 42.3), up
+// to 16 where it is the faster one (4096 x 4096 6.8 against 9.5, 2048 x 6144 8.0
+// against 9.2, but 2048 x 12288 13.4 against 11.7), else tokens in parts through
+// the swapped-operand kernel (M = 16 at 4096 x 11008 14.0 against 14.1 to 18.2,
+// at 22016 x 4096 gated 20.6 against 25.0; M = 32 at 4096 x 11008 15.7 against
+// 26.6).
 unsigned choose_w8a16_linear(int64_t M, int64_t N, int64_t K, unsigned flags) {
     const unsigned k = flags & FP8L_KERNEL_MASK;
     if (k != FP8L_KERNEL_AUTO) return k;

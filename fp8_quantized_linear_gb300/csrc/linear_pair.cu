@@ -256,7 +256,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * LP_STAGES + b); };
     auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * LP_STAGES + 2 + b); };
     const uint32_t done_bar = bar0 + 8u * (2 * LP_STAGES + 4);
-    const uint32_t box_bar0 = done_bar + 8u;  // residual boxes: two an epilogue warp
+    const uint32_t box_bar0 = done_bar + 8u;  // residual boxes: one an epilogue warp
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kLpBarOffset + (kLpBarriers + kLpBoxes) * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -436,7 +436,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     } else {
         pdl_wait();
         const int quarter = warp & 3;     // the TMEM lanes this warp may read
-        const int grp = (warp - 2) >> 2;  // its half of each tile's chunks
+        const int grp = (warp - 2) >> 2;  // its quarter of each tile's chunks
         const int et = static_cast<int>(threadIdx.x) - 64;
         const int row = static_cast<int>(rank) * LP_BM + quarter * 32 + lane;
         const float sa0 = epi_ld_f32(p.a_scale);
@@ -472,7 +472,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             }
             const float sa = p.a_per_token ? (row_ok ? epi_ld_f32(p.a_scale + m) : 0.0f) : sa0;
             const int chunks = GATED ? half / 32 : t.w / 32;
-            // this pair's share of the chunks, this warp's half of it
+            // this pair's share of the chunks, this warp's quarter of it
             const int own0 = SPLIT ? chunks * kpart / p.split : 0;
             const int own = SPLIT ? chunks * (kpart + 1) / p.split - own0 : chunks;
             const int c_begin = own0 + grp * own / kLpEpiGroups, c_end = own0 + (grp + 1) * own / kLpEpiGroups;

@@ -359,7 +359,9 @@ FP8L_API int fp8_linear(const uint8_t *a, const uint8_t *w, int64_t M, int64_t N
  * sum of E4M3 parts (two for bf16, three for fp16), whose products with the
  * weights are exact: what the parts leave out of a value is below 2^-21
  * (bf16) or 2^-25 (fp16) of the token's largest magnitude (of 2^-119, where
- * that is more).  With FP8L_KERNEL_AUTO a call without bias, activation and
+ * that is more): values down to 2^-13 of a row's largest are held whole, the
+ * smaller ones lose a bit for every factor of two.  With
+ * FP8L_KERNEL_STREAM every token is taken whole, at any M.  With FP8L_KERNEL_AUTO a call without bias, activation and
  * residual is fp8_w8a16_mm up to 16 tokens of bf16 and 64 of fp16.
  * workspace: fp8_w8a16_linear_workspace_bytes() bytes for these arguments
  * (16-byte aligned, any contents; may be NULL when that is 0 or the call is
@@ -481,8 +483,10 @@ FP8L_API int fp8_rmsnorm_quant(const void *x, int x_dtype, const void *gamma, fl
  * workspace, M and K as for fp8_rmsnorm_quant.  Apart from that, no output
  * shares memory with an input or another output, nor in FP8L_NQ_DYNAMIC the
  * workspace with anything (FP8L_EINVAL).  workspace is
- * used in FP8L_NQ_DYNAMIC only, by one call at a time (two words of it, zero
- * between calls); nothing in the call waits.  Deterministic. */
+ * used in FP8L_NQ_DYNAMIC only, by one call at a time: four words of it, zero
+ * before the first call, keep a call counter, the half of a pair of maxima
+ * that the last call used, and that pair from call to call (bytes [32, 48),
+ * no other entry point's).  Nothing in the call waits.  Deterministic. */
 FP8L_API int fp8_add_rmsnorm_quant(const void *x, const void *residual, int x_dtype,
                                    const void *gamma, float eps, int64_t M, int64_t K, void *total,
                                    uint8_t *q, float *scale, int mode, void *h, void *workspace,
