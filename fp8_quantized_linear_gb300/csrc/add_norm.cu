@@ -191,34 +191,30 @@ __device__ __forceinline__ float pair_sum(uint64_t acc) {
 }
 
 // What a row's threads do, WARPS warps a row, NW words (of 8 elements) a
-// thread, words tid, tid + 32 WARPS, ...  Loads go in batches of kBatch words
-// of x and res.
+// thread, words tid, tid + 32 WARPS, ...  All of a thread's loads are on their
+// way before the first is used.
 template <int DT, int WARPS, int NW>
 struct Row {
     static constexpr int kSpan = 32 * WARPS;
-    static constexpr int kBatch = NW > 4 ? 2 : NW;
 
     // the sum x + res, stored as the new stream; words beyond the row are zeros
     __device__ __forceinline__ static void add(const AddNormArgs &a, size_t at, int tid, int words,
                                                uint4 (&t)[NW]) {
+        uint4 x[NW], r[NW];
 #pragma unroll
-        for (int j0 = 0; j0 < NW; j0 += kBatch) {
-            uint4 x[kBatch], r[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int w = tid + (j0 + j) * kSpan;
-                x[j] = r[j] = make_uint4(0, 0, 0, 0);
-                if (w < words) {
-                    x[j] = ld_once16(static_cast<const uint4 *>(a.x) + at + w);
-                    r[j] = ld_once16(static_cast<const uint4 *>(a.res) + at + w);
-                }
+        for (int j = 0; j < NW; ++j) {
+            const int w = tid + j * kSpan;
+            x[j] = r[j] = make_uint4(0, 0, 0, 0);
+            if (w < words) {
+                x[j] = ld_once16(static_cast<const uint4 *>(a.x) + at + w);
+                r[j] = ld_once16(static_cast<const uint4 *>(a.res) + at + w);
             }
+        }
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int w = tid + (j0 + j) * kSpan;
-                t[j0 + j] = add_word<DT>(x[j], r[j]);
-                if (w < words) static_cast<uint4 *>(a.total)[at + w] = t[j0 + j];
-            }
+        for (int j = 0; j < NW; ++j) {
+            const int w = tid + j * kSpan;
+            t[j] = add_word<DT>(x[j], r[j]);
+            if (w < words) static_cast<uint4 *>(a.total)[at + w] = t[j];
         }
     }
 
@@ -233,17 +229,14 @@ struct Row {
     // h in place of t
     __device__ __forceinline__ static void scale(const AddNormArgs &a, int tid, int words, uint64_t r2,
                                                  uint4 (&t)[NW]) {
+        uint4 g[NW];
 #pragma unroll
-        for (int j0 = 0; j0 < NW; j0 += kBatch) {
-            uint4 g[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int w = tid + (j0 + j) * kSpan;
-                g[j] = w < words ? ld_act16(static_cast<const uint4 *>(a.gamma) + w) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) t[j0 + j] = scaled_word<DT>(t[j0 + j], g[j], r2);
+        for (int j = 0; j < NW; ++j) {
+            const int w = tid + j * kSpan;
+            g[j] = w < words ? ld_act16(static_cast<const uint4 *>(a.gamma) + w) : make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int j = 0; j < NW; ++j) t[j] = scaled_word<DT>(t[j], g[j], r2);
     }
 
     __device__ __forceinline__ static uint32_t magnitude(const uint4 (&t)[NW], uint32_t m) {
