@@ -49,7 +49,7 @@
 // and E4M3 output, 78.4 to 79.2 us (0.79 of twice the bf16 burst peak; tensor
 // pipe 68 % active), down of 4096 tokens, 8192 x 28672 with bias and residual,
 // 560 to 568 us cool (0.89; 84 %), 620 to 660 under the power cap; 4096 x 28672
-// x 4096 with a residual 299 us (330 for fp8_scaled_mm).
+// x 4096 with a residual 303 us (297 for fp8_scaled_mm without one).
 // Waits are bounded; a time-out raises both CTAs' abort flags, and all CTAs of
 // a cluster meet at its barrier before TMEM is released.
 #include <atomic>
