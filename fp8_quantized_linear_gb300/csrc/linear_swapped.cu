@@ -461,25 +461,30 @@ linear_swapped_kernel(const __grid_constant__ CUtensorMap tmap_w,
         next = after;
         if (p.e.residual != nullptr) after = load_batch(i + 2 * kStep);
         uint32_t off[B];
-        float sa[B], v[4 * B];
+        float pre[B], sa[B], v[4 * B];
 #pragma unroll
         for (int u = 0; u < B; ++u) {
             const bool valid = i + u * kLsThreads < i1;  // (else the first once more)
             off[u] = valid ? at + u * at_step : at;
-            sa[u] = scale[valid ? u * t_step : 0];
+            // a token's own scale (of its parts, a power of two) goes to the
+            // sums: times a channel's it may leave the normal range
+            const float s = scale[valid ? u * t_step : 0];
+            pre[u] = p.parts > 1 ? s : 1.0f;
+            sa[u] = p.parts > 1 ? 1.0f : s;
         }
         at += B * at_step;
         scale += B * t_step;
         const int valid = (i1 - i + kLsThreads - 1) / kLsThreads;
         ls_sums(off, valid, 0, split, v);
 #pragma unroll
-        for (int j = 0; j < 4 * B; ++j) v[j] = fmaf(v[j], sa[j / 4] * sw[j % 4], bias[j % 4]);
+        for (int j = 0; j < 4 * B; ++j) v[j] = fmaf(v[j] * pre[j / 4], sa[j / 4] * sw[j % 4], bias[j % 4]);
         activate(v, p.e.act);
         if (p.gated) {
             float up[4 * B];
             ls_sums(off, valid, LS_BM / 2 * 4, split, up);
 #pragma unroll
-            for (int j = 0; j < 4 * B; ++j) v[j] *= fmaf(up[j], sa[j / 4] * sw_up[j % 4], bias_up[j % 4]);
+            for (int j = 0; j < 4 * B; ++j)
+                v[j] *= fmaf(up[j] * pre[j / 4], sa[j / 4] * sw_up[j % 4], bias_up[j % 4]);
         }
         if (p.e.out_dtype == FP8L_E4M3) {
 #pragma unroll

@@ -197,6 +197,32 @@ def test_w8a16_rows_near_the_types_ends(dtype, size, kernel):
     assert_status_ok()
 
 
+@pytest.mark.parametrize("kernel", ["stream", "swapped"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M", [3, 20, 100])
+def test_w8a16_scales_whose_product_is_subnormal(kernel, gated, M):
+    """Sums of zeros and ones times 2^-119, and weight scales of about 2^-16: a
+    token's own scale times a weight's is below 2^-126, the result above it,
+    and exact before its rounding but for the product with the weight's scale,
+    which is rounded once to float32."""
+    N, K = 96, 16384
+    gen = torch.Generator(device=DEV).manual_seed(M)
+    x = torch.randint(0, 2, (M, K), generator=gen, device=DEV).to(BF) * 2.0 ** -119
+    w = torch.randint(0, 2, (N, K), generator=gen, device=DEV, dtype=U8) * 0x38
+    sw = (0.5 + torch.rand(N, generator=gen, device=DEV)) * 2.0 ** -16
+    bias = None
+    if gated:  # (up: one, from its bias; its sums are far below one's last place)
+        bias = torch.zeros(N, device=DEV)
+        bias[N // 2:] = 1.0
+    t = ((x.double() @ ref.e4m3_values(w).T) * sw.double()).float()
+    if gated:
+        t = t[:, : N // 2]
+    assert (t > 2.0 ** -125).all()
+    y = w8a16(x, w, sw, bias=bias, activation="relu", gated=gated, kernel=kernel)
+    assert torch.equal(y, t.to(BF))
+    assert_status_ok()
+
+
 # ------------------------------------------------------------------ repeats
 
 def test_the_same_bits_on_every_call():
