@@ -908,8 +908,9 @@ _norm_capture_workspaces = {}  # (device, stream): (capture, workspace) of its l
 def _norm_workspace(index: int) -> torch.Tensor:
     """A workspace of a dynamic fp8_add_rmsnorm_quant for the current stream:
     the words through which the tensor's maximum passes belong to one call at
-    a time, so streams do not share one, and a graph capture gets its own from the graph's memory, zeroed
-    by every replay (a graph may run beside eager calls and other graphs)."""
+    a time, so streams do not share one, and a graph capture gets its own from
+    the graph's memory, zeroed by every replay (a graph may run beside eager
+    calls and other graphs)."""
     key = (index, _stream_handle(index))
     capture = _capture_id(*key)
     if capture:
